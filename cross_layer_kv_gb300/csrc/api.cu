@@ -153,6 +153,66 @@ fkv::DecodeArgs decode_args(const fkv_ctx* c) {
   return d;
 }
 
+constexpr int kTreeNodes = 128;   // drafted nodes of a sequence, at most
+
+unsigned next_epoch() {
+  unsigned ep = g_decode_epoch.fetch_add(1);
+  if (ep == 0) ep = g_decode_epoch.fetch_add(1);
+  return ep;
+}
+
+fkv::TreeArgs tree_args(const fkv_ctx* c, int T) {
+  fkv::TreeArgs t{};
+  t.batch = c->cfg.batch;
+  t.kv_heads = c->cfg.num_kv_heads;
+  t.group = c->group;
+  t.max_seq = c->cfg.max_seq;
+  t.head_dim = c->cfg.head_dim;
+  t.T = T;
+  t.is_f32 = c->cfg.dtype == FKV_F32;
+  t.num_ctas = c->cfg.decode_ctas;
+  t.softmax_scale = c->scale;
+  t.status = c->status;
+  t.wait_limit = c->wait_limit;
+  return t;
+}
+
+// Run `launch` over the K and V planes of every layer with bound caches, each
+// buffer once (layers may share one), kMovePlanes at a time.
+// FKV_ERR_INVALID_ARG where none is bound.
+template <typename Launch>
+fkv_status for_bound_planes(const fkv_ctx* c, Launch launch) {
+  fkv::MoveTable tb{};
+  bool any = false;
+  auto seen = [&](const void* ptr, int layer, bool value) {
+    for (int l = 1; l <= layer; ++l)
+      if ((c->k[l] == ptr && (l < layer || value)) || (c->v[l] == ptr && l < layer)) return true;
+    return false;
+  };
+  for (int l = 1; l <= c->cfg.num_layers; ++l)
+    for (int kv = 0; kv < 2; ++kv) {
+      void* ptr = kv ? c->v[l] : c->k[l];
+      if (!ptr || seen(ptr, l, kv == 1)) continue;
+      any = true;
+      tb.plane[tb.planes] = ptr;
+      tb.rows[tb.planes] = c->ring[l] > 0 ? c->ring[l] : c->cfg.max_seq;
+      tb.row_bytes[tb.planes] = c->q4[l] ? fkv::q4_row_bytes(c->cfg.head_dim)
+                                         : c->cfg.head_dim * elem_bytes(c->cfg);
+      if (++tb.planes == fkv::kMovePlanes) {
+        if (launch(tb) != cudaSuccess) return FKV_ERR_CUDA;
+        tb.planes = 0;
+      }
+    }
+  if (tb.planes > 0 && launch(tb) != cudaSuccess) return FKV_ERR_CUDA;
+  return any ? FKV_OK : FKV_ERR_INVALID_ARG;
+}
+
+// Whether the context's device is the calling thread's current one.
+bool on_device(const fkv_ctx* c) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
+}
+
 }  // namespace
 
 namespace fkv {
@@ -186,9 +246,7 @@ fkv_status decode_attn_impl(fkv_ctx* c, const void* q, int layer, int mode,
   d.workspace = static_cast<float*>(workspace);
   d.window = c->window[layer];
   d.ring = ring;
-  unsigned ep = g_decode_epoch.fetch_add(1);
-  if (ep == 0) ep = g_decode_epoch.fetch_add(1);
-  d.epoch = ep;
+  d.epoch = next_epoch();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_counts &&
       cudaMemsetAsync(static_cast<char*>(workspace) + plan.partial_bytes, 0,
@@ -420,6 +478,103 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   const cudaError_t e = fkv::prefill_launch(p, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return FKV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+size_t fkv_tree_workspace_bytes(const fkv_ctx* c, int T) {
+  if (!c || T < 1 || T > kTreeNodes) return 0;
+  size_t best = 0;
+  for (int nsrc = 1; nsrc <= 2; ++nsrc)
+    for (int q4 = 0; q4 <= 1; ++q4) {
+      fkv::TreeArgs t = tree_args(c, T);
+      t.q4 = q4;
+      t.k[1] = nsrc == 2 ? c : nullptr;   // only whether there is a second source counts
+      fkv::TreePlan p{};
+      if (fkv::tree_plan(t, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
+        best = p.workspace_bytes;
+    }
+  return best;
+}
+
+fkv_status fkv_tree_attn(fkv_ctx* c, const void* q, int layer, int mode, const int32_t* seq_lens,
+                         const int32_t* node_counts, const uint64_t* tree_mask, int T, void* out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (!c || !on_device(c)) return FKV_ERR_INVALID_ARG;
+  if (T < 1 || T > kTreeNodes || T > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
+  fkv::TreeArgs t = tree_args(c, T);
+  int q4 = 0, ring = 0, nsrc = 0;
+  fkv_status s = resolve_sources(c, layer, mode, t.k, t.v, t.a, t.b, &nsrc, &q4, &ring);
+  if (s != FKV_OK) return s;
+  t.window = c->window[layer];
+  if (ring > 0) {
+    // every position that a node may see has to be in the ring still, with
+    // all T drafted rows appended
+    if (t.window < 1 || t.window > ring) return FKV_ERR_INVALID_ARG;
+    if ((long long)t.window + T - 1 > ring) return FKV_ERR_UNSUPPORTED;
+  }
+  if (!q || !out || !seq_lens || !tree_mask || !aligned16(q) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(node_counts) & 3u) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return FKV_ERR_INVALID_ARG;
+  t.q4 = q4;
+  t.ring = ring;
+  fkv::TreePlan plan{};
+  if (fkv::tree_plan(t, c->num_sms, &plan) != cudaSuccess) return FKV_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < plan.workspace_bytes)
+    return FKV_ERR_WORKSPACE;
+  t.q = q;
+  t.out = out;
+  t.seq_lens = seq_lens;
+  t.node_counts = node_counts;
+  t.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  t.workspace = workspace;
+  t.epoch = next_epoch();
+  const cudaError_t e = fkv::tree_launch(t, plan, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return FKV_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+fkv_status fkv_compact_rows(fkv_ctx* c, const int32_t* pos, const int32_t* idx,
+                            const int32_t* counts, int A, void* stream) {
+  if (!c || !on_device(c) || A < 0 || A > fkv::kMaxAccepted || A > c->cfg.max_seq)
+    return FKV_ERR_INVALID_ARG;
+  if (A == 0) return FKV_OK;
+  if (!pos || !idx || !counts ||
+      ((reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(idx) |
+        reinterpret_cast<uintptr_t>(counts)) & 3u))
+    return FKV_ERR_INVALID_ARG;
+  fkv::CompactArgs a{};
+  a.pos = pos;
+  a.idx = idx;
+  a.counts = counts;
+  a.status = c->status;
+  a.batch = c->cfg.batch;
+  a.kv_heads = c->cfg.num_kv_heads;
+  a.max_seq = c->cfg.max_seq;
+  a.A = A;
+  a.min_rows = c->cfg.max_seq;
+  for (int l = 1; l <= c->cfg.num_layers; ++l)
+    if (c->k[l] && c->ring[l] > 0 && c->ring[l] < a.min_rows) a.min_rows = c->ring[l];
+  return for_bound_planes(c, [&](const fkv::MoveTable& tb) {
+    return fkv::compact_launch(tb, a, static_cast<cudaStream_t>(stream));
+  });
+}
+
+fkv_status fkv_reorder_seqs(fkv_ctx* c, const int32_t* src, const int32_t* seq_lens,
+                            void* stream) {
+  if (!c || !on_device(c) || !src || !seq_lens ||
+      ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u))
+    return FKV_ERR_INVALID_ARG;
+  fkv::ReorderArgs a{};
+  a.src = src;
+  a.seq_lens = seq_lens;
+  a.status = c->status;
+  a.wait_limit = c->wait_limit;
+  a.batch = c->cfg.batch;
+  a.kv_heads = c->cfg.num_kv_heads;
+  a.max_seq = c->cfg.max_seq;
+  return for_bound_planes(c, [&](const fkv::MoveTable& tb) {
+    return fkv::reorder_launch(tb, a, c->num_sms, static_cast<cudaStream_t>(stream));
+  });
 }
 
 fkv_status fkv_get_device_status(fkv_ctx* c, void* stream) {

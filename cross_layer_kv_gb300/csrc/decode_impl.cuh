@@ -215,23 +215,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Count one arrival on a unit's word for call `epoch`; returns the count of
-// this epoch including this arrival (0 if the retry bound ran out).  A word
-// holding another epoch restarts at 1.
-__device__ __forceinline__ unsigned unit_arrive(unsigned long long* word, unsigned epoch) {
-  unsigned long long old = atomicAdd(word, 0ull);
-#pragma unroll 1
-  for (int i = 0; i < (1 << 20); ++i) {
-    const unsigned long long nv = (unsigned)(old >> 32) == epoch
-                                      ? old + 1ull
-                                      : (((unsigned long long)epoch << 32) | 1ull);
-    const unsigned long long prev = atomicCAS(word, old, nv);
-    if (prev == old) return (unsigned)(nv & 0xffffffffull);
-    old = prev;
-  }
-  return 0;
-}
-
 // Merge the partials of unit (b, h) -- written by warps wf..wl at slots
 // w + u, skipping the warps with empty ranges -- into the G output rows.  One
 // warp; partials are read through L2 (__ldcg), since other SMs wrote them in

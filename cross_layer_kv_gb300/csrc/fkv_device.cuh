@@ -168,4 +168,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Count one arrival on a unit's word for call `epoch`; returns the count of
+// this epoch including this arrival (0 if the retry bound ran out).  A word
+// holding another epoch restarts at 1.
+__device__ __forceinline__ unsigned unit_arrive(unsigned long long* word, unsigned epoch) {
+  unsigned long long old = atomicAdd(word, 0ull);
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i) {
+    const unsigned long long nv = (unsigned)(old >> 32) == epoch
+                                      ? old + 1ull
+                                      : (((unsigned long long)epoch << 32) | 1ull);
+    const unsigned long long prev = atomicCAS(word, old, nv);
+    if (prev == old) return (unsigned)(nv & 0xffffffffull);
+    old = prev;
+  }
+  return 0;
+}
+
 }  // namespace fkv

@@ -127,6 +127,75 @@ cudaError_t prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_wide_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_fused_wide_launch(const PrefillArgs& a, cudaStream_t stream);
 
+// One fkv_tree_attn call, after host validation.
+struct TreeArgs {
+  const void* k[2];          // second source null unless fused
+  const void* v[2];
+  const float* a[2];         // null for vanilla and lite
+  const float* b[2];
+  const void* q;             // [B, H_q, T, D]
+  void* out;                 // [B, H_q, T, D]
+  const int32_t* seq_lens;
+  const int32_t* node_counts;      // may be null
+  const unsigned long long* mask;  // [B, T, ceil(T / 64)]
+  void* workspace;
+  int* status;
+  const unsigned long long* wait_limit;
+  int batch, kv_heads, group, max_seq, head_dim, T;
+  int is_f32, q4;
+  int window, ring;
+  int num_ctas;              // > 0: that many key ranges
+  float softmax_scale;
+  unsigned epoch;            // distinct per call
+};
+
+// Launch configuration of a tree attention call.
+struct TreePlan {
+  int ranges;       // key ranges (grid.x)
+  int rows;         // query rows per CTA
+  int row_tiles;    // grid.y
+  size_t smem_bytes;
+  size_t partial_bytes;    // partials, then one 8-byte arrival word per unit and row tile
+  size_t workspace_bytes;
+};
+
+cudaError_t tree_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
+cudaError_t tree_launch(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream);
+
+// The planes that one launch of compact or reorder moves rows in: the K or V
+// caches of a layer, `rows` rows of row_bytes bytes per (sequence, KV head).
+constexpr int kMovePlanes = 128;
+struct MoveTable {
+  void* plane[kMovePlanes];
+  int rows[kMovePlanes];
+  int row_bytes[kMovePlanes];
+  int planes;
+};
+
+struct CompactArgs {
+  const int32_t* pos;      // [B]
+  const int32_t* idx;      // [B, A]
+  const int32_t* counts;   // [B]
+  int* status;
+  int batch, kv_heads, max_seq, A;
+  int min_rows;            // fewest rows of any bound layer's planes
+  int cols;                // 16-byte columns per CTA (set by the launch)
+};
+
+struct ReorderArgs {
+  const int32_t* src;        // [B]
+  const int32_t* seq_lens;   // [B]
+  int* status;
+  const unsigned long long* wait_limit;
+  int batch, kv_heads, max_seq;
+};
+
+constexpr int kMaxAccepted = 128;   // rows a sequence may compact in one call
+
+cudaError_t compact_launch(const MoveTable& tb, CompactArgs a, cudaStream_t stream);
+cudaError_t reorder_launch(const MoveTable& tb, const ReorderArgs& a, int num_sms,
+                           cudaStream_t stream);
+
 // The body of fkv_decode_attn (api.cu); clear_counts zeroes the call's unit
 // arrival words on the stream before the launch.  Internal to the library.
 __attribute__((visibility("hidden"))) fkv_status decode_attn_impl(

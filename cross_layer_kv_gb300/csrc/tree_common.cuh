@@ -1,0 +1,302 @@
+// What the kernels of fkv_tree_attn share: the drafted sequences of a call,
+// the cut of its key tiles into one range per CTA, and the merge of the
+// partial results of a (sequence, KV head) unit that several ranges share.
+//
+// What a call computes: sequence b has P committed rows and N drafted nodes
+// whose keys and values lie at positions P .. P + N - 1.  Node i of query
+// head h sees every position t < P and position P + j where bit j of its mask
+// word is set:
+//     o_{h,i} = sum_t softmax_t(scale * q_{h,i} . K_t) V_t,  t visible to i,
+// and 0 where nothing is visible.  With a window W the node's depth is
+// d_i = max(popcount(mask_i), 1) - 1, its position P + d_i, and it sees the
+// visible keys whose position (P + d_j for drafted node j) is above
+// P + d_i - W.
+#pragma once
+
+#include <cfloat>
+#include <cstdint>
+
+#include "fkv_device.cuh"
+#include "fkv_kernels.h"
+
+namespace fkv {
+
+constexpr int kTreeMaxNodes = 128;
+
+struct TreeParams;
+void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
+cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
+                             cudaStream_t stream);
+
+struct TreeParams {
+  const void* k[2];
+  const void* v[2];
+  const float* a[2];
+  const float* b[2];
+  const void* q;                   // [B, H_q, T, D]
+  void* out;                       // [B, H_q, T, D]
+  const int32_t* seq_lens;         // [B] committed rows
+  const int32_t* node_counts;      // [B] drafted nodes, or null: T
+  const unsigned long long* mask;  // [B, T, words]
+  float* ws;                       // partials
+  unsigned long long* counters;    // one arrival word per (b, kh, row tile)
+  int* status;
+  const unsigned long long* wait_limit;
+  int B, H, G, S_max, T, words;
+  int window, ring;
+  int row_tiles;    // row tiles of a unit (grid.y)
+  unsigned epoch;
+  float scale_log2; // softmax scale * log2(e)
+};
+
+// One sequence of a call: its attended positions [start, n) lie in the cache
+// rows as one run of cntA rows and, in a ring that wraps, a second of cntB.
+struct TreeSeq {
+  int P, N, n, start, cntA, cntB;
+  bool bad;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  TreeSeq s;
+  s.P = p.seq_lens[b];
+  s.N = p.node_counts ? p.node_counts[b] : p.T;
+  s.bad = s.P < 0 || s.N < 0 || s.N > p.T || s.P > p.S_max - s.N;
+  if (s.bad) s.P = s.N = 0;
+  s.n = s.N > 0 ? s.P + s.N : 0;
+  s.start = p.window > 0 && s.P >= p.window ? s.P - p.window + 1 : 0;
+  if (s.N == 0) s.start = 0;
+  int end = s.n;
+  if (p.ring > 0) {
+    const long long wrap = ((long long)s.start / p.ring + 1) * p.ring;
+    if (wrap < s.n) end = (int)wrap;
+  }
+  s.cntA = end - s.start;
+  s.cntB = s.n - end;
+  return s;
+}
+
+__device__ __forceinline__ int tree_tiles(const TreeSeq& s, int KT) {
+  return (s.cntA + KT - 1) / KT + (s.cntB + KT - 1) / KT;
+}
+
+// Tile k of a sequence: its first position and cache row, and its row count.
+// A tile never crosses the end of a ring.
+struct TreeTile {
+  int pos, row, cnt;
+};
+
+__device__ __forceinline__ TreeTile tree_tile(const TreeParams& p, const TreeSeq& s, int k, int KT) {
+  const int tA = (s.cntA + KT - 1) / KT;
+  TreeTile t;
+  if (k < tA) {
+    t.pos = s.start + k * KT;
+    t.cnt = min(KT, s.cntA - k * KT);
+  } else {
+    t.pos = s.start + s.cntA + (k - tA) * KT;
+    t.cnt = min(KT, s.cntB - (k - tA) * KT);
+  }
+  t.row = p.ring > 0 ? t.pos % p.ring : t.pos;
+  return t;
+}
+
+// Word w of node i's mask with the bits of nodes that do not exist cleared.
+__device__ __forceinline__ unsigned long long tree_mask_word(const TreeParams& p, int b, int i,
+                                                             int w, int N) {
+  const unsigned long long m = p.mask[((size_t)b * p.T + i) * p.words + w];
+  const int left = N - 64 * w;
+  return left >= 64 ? m : left <= 0 ? 0ull : m & ((1ull << left) - 1);
+}
+
+__device__ __forceinline__ int tree_depth(const TreeParams& p, int b, int i, int N) {
+  int c = 0;
+  for (int w = 0; w < p.words; ++w) c += __popcll(tree_mask_word(p, b, i, w, N));
+  return c > 1 ? c - 1 : 0;
+}
+
+// The cut: the tiles of all units, unit by unit, in `ranges` equal contiguous
+// ranges.  pre[b] = tiles of one head of the sequences before b (B + 1 words
+// of shared memory).  Every thread of the CTA takes part.
+struct TreeCut {
+  long long total;
+  int ranges;
+};
+
+__device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, int* pre, int KT, int max_ranges) {
+  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+    const TreeSeq s = tree_seq(p, i);
+    if (s.bad && blockIdx.x == 0 && blockIdx.y == 0) flag_status(p.status, kDevBadArg);
+    pre[i + 1] = tree_tiles(s, KT);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int run = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      int x = base + lane < p.B ? pre[base + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (base + lane < p.B) pre[base + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+  __syncthreads();
+  TreeCut c;
+  c.total = (long long)p.H * pre[p.B];
+  c.ranges = (int)min((long long)max_ranges, c.total);
+  return c;
+}
+
+// A run of tiles [k0, k1) of unit (b, h) inside a range.
+struct TreePiece {
+  int b, h, k0, k1, tiles;
+  bool first;   // the range's first piece
+};
+
+struct TreeWalk {
+  long long t, t1;
+  int b, h, k;
+  bool first;
+
+  __device__ __forceinline__ void begin(const TreeCut& c, const int* pre, int B, int H, int range) {
+    t = range * c.total / c.ranges;
+    t1 = (range + 1) * c.total / c.ranges;
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)H * pre[mid + 1] > t) hi = mid; else lo = mid + 1;
+    }
+    const long long off = t - (long long)H * pre[lo];
+    const int n = pre[lo + 1] - pre[lo];
+    b = lo;
+    h = (int)(off / n);
+    k = (int)(off - (long long)h * n);
+    first = true;
+  }
+  __device__ __forceinline__ bool next(const int* pre, int B, int H, TreePiece& pc) {
+    if (t >= t1) return false;
+    const int n = pre[b + 1] - pre[b];
+    pc.b = b;
+    pc.h = h;
+    pc.k0 = k;
+    pc.k1 = (int)min((long long)n, k + (t1 - t));
+    pc.tiles = n;
+    pc.first = first;
+    first = false;
+    t += pc.k1 - pc.k0;
+    k = 0;
+    if (++h == H) {
+      h = 0;
+      ++b;
+      while (b < B && pre[b + 1] == pre[b]) ++b;
+    }
+    return true;
+  }
+};
+
+// Partials.  A piece that is not its whole unit leaves (o, m, l) of its rows
+// in the slot 2 * range (the range's first piece) or 2 * range + 1 (its last);
+// a record is o[ROWS][D], m[ROWS], l[ROWS].
+__host__ __device__ constexpr int tree_record_floats(int rows, int D) { return rows * (D + 2); }
+
+// The ranges that hold tiles of unit (b, h), and the slot of one of them.
+struct TreeUnit {
+  long long first, last;   // ranges
+  bool first_is_tail;      // the first range's piece is its last one
+};
+
+__device__ __forceinline__ TreeUnit tree_unit(const TreeCut& c, const int* pre, int H, int b, int h) {
+  const long long n = pre[b + 1] - pre[b];
+  const long long u0 = (long long)H * pre[b] + h * n, u1 = u0 + n;
+  TreeUnit u;
+  u.first = ((u0 + 1) * c.ranges - 1) / c.total;
+  u.last = (u1 * c.ranges - 1) / c.total;
+  u.first_is_tail = u.first * c.total / c.ranges < u0;
+  return u;
+}
+
+// Zero output rows of the sequences whose lengths are out of range.
+template <typename E>
+__device__ __forceinline__ void tree_zero_bad(const TreeParams& p, int D) {
+  if (blockIdx.x != 0 || blockIdx.y != 0) return;
+  for (int b = 0; b < p.B; ++b) {
+    if (!tree_seq(p, b).bad) continue;
+    const size_t n = (size_t)p.H * p.G * p.T * D * sizeof(E) / 16;
+    uint4* o = reinterpret_cast<uint4*>(p.out) + (size_t)b * n;
+    for (size_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void tree_store4(float* dst, const float* x) {
+  *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void tree_store4(__nv_bfloat16* dst, const float* x) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                              *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Announce a written partial of unit (b, h), row tile blockIdx.y; the CTA
+// whose arrival completes the unit merges its pieces by their log-sum-exp
+// weights into the output rows.  Called by `nthreads` threads (index tid)
+// that `sync` brings together; all of them have written their part before.
+template <typename E, int D, int ROWS, typename Sync>
+__device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut& c, const int* pre,
+                                             int b, int h, int N, int tid, int nthreads, int* flag,
+                                             Sync sync) {
+  const TreeUnit u = tree_unit(c, pre, p.H, b, h);
+  const int P = (int)(u.last - u.first + 1);
+  const int rt = blockIdx.y;
+  __threadfence();
+  sync();
+  if (tid == 0) {
+    unsigned long long* word = p.counters + ((size_t)b * p.H + h) * p.row_tiles + rt;
+    const unsigned got = unit_arrive(word, p.epoch);
+    if (got == 0) flag_status(p.status, kDevTimeout);
+    // no arrival of this call can follow the last: clear the word, so that a
+    // replay of this launch (the same epoch) starts at one
+    if (got == (unsigned)P) *word = 0ull;
+    *flag = got == (unsigned)P;
+    __threadfence();
+  }
+  sync();
+  if (!*flag) return;
+  constexpr int REC = tree_record_floats(ROWS, D);
+  constexpr int C4 = D / 4;
+  const int rows = min(ROWS, p.G * p.T - rt * ROWS);
+  auto rec = [&](int i) {
+    const long long slot = 2 * (u.first + i) + (i == 0 && u.first_is_tail ? 1 : 0);
+    return p.ws + ((size_t)slot * p.row_tiles + rt) * REC;
+  };
+  for (int it = tid; it < rows * C4; it += nthreads) {
+    const int r = it / C4, d = (it - r * C4) * 4;
+    const int row = rt * ROWS + r;
+    if (row % p.T >= N) continue;
+    float M = -FLT_MAX;
+#pragma unroll 4
+    for (int i = 0; i < P; ++i) M = fmaxf(M, __ldcg(rec(i) + ROWS * D + r));
+    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < P; ++i) {
+      const float* q = rec(i);
+      const float w = exp2f(__ldcg(q + ROWS * D + r) - M);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
+      L = fmaf(w, __ldcg(q + ROWS * D + ROWS + r), L);
+      acc[0] = fmaf(w, o.x, acc[0]);
+      acc[1] = fmaf(w, o.y, acc[1]);
+      acc[2] = fmaf(w, o.z, acc[2]);
+      acc[3] = fmaf(w, o.w, acc[3]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= inv;
+    tree_store4(static_cast<E*>(p.out) +
+                    (((size_t)b * p.H + h) * p.G * p.T + row) * D + d, acc);
+  }
+  sync();   // the flag may be written again
+}
+
+}  // namespace fkv

@@ -80,6 +80,11 @@ _SIGS = {
     "fkv_prefill_attn": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P]),
     "fkv_prefill_attn_chunk": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                               ctypes.c_int, _P, _P]),
+    "fkv_tree_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int]),
+    "fkv_tree_attn": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.c_int,
+                                     _P, _P, ctypes.c_size_t, _P]),
+    "fkv_compact_rows": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _P]),
+    "fkv_reorder_seqs": (ctypes.c_int, [_P, _P, _P, _P]),
     "fkv_get_device_status": (ctypes.c_int, [_P, _P]),
     "fkv_set_wait_limit": (ctypes.c_int, [_P, ctypes.c_ulonglong]),
     "fkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -316,6 +321,59 @@ class Context:
         _check(self._lib.fkv_prefill_attn_chunk(self.handle, _ptr(q), layer, m, q_start, C, _ptr(out),
                                                 _stream(stream)), "fkv_prefill_attn_chunk")
         return out
+
+    def _need_cuda(self, t, shape, dtype, name):
+        self._need(t, shape, dtype, name)
+        if isinstance(t, torch.Tensor) and not t.is_cuda:
+            raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
+
+    def fkv_tree_workspace_bytes(self, T: int) -> int:
+        return int(self._lib.fkv_tree_workspace_bytes(self.handle, T))
+
+    def tree_workspace(self, T: int, device="cuda") -> torch.Tensor:
+        """A caller-owned workspace buffer for fkv_tree_attn with T nodes per sequence."""
+        n = (self.fkv_tree_workspace_bytes(T) + 15) // 16 * 16
+        if n == 0:
+            raise ValueError("T: expected 1 to 128 nodes, got %d" % T)
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+    def fkv_tree_attn(self, q, layer: int, mode, seq_lens, tree_mask, out, workspace,
+                      node_counts=None, T: Optional[int] = None, stream=None):
+        """Attention of T drafted nodes per sequence; tree_mask is int64
+        [B, T, ceil(T / 64)], bit j of row i: node i sees node j."""
+        c = self.cfg
+        if T is None:
+            T = q.shape[2]
+        shape = (c.batch, c.num_q_heads, T, c.head_dim)
+        self._need_cuda(q, shape, self.torch_dtype, "q")
+        self._need_cuda(out, shape, self.torch_dtype, "out")
+        self._need_cuda(seq_lens, (c.batch,), torch.int32, "seq_lens")
+        self._need_cuda(tree_mask, (c.batch, T, (T + 63) // 64), torch.int64, "tree_mask")
+        self._need_cuda(node_counts, (c.batch,), torch.int32, "node_counts")
+        m = MODES[mode] if isinstance(mode, str) else int(mode)
+        nbytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) \
+            else int(getattr(workspace, "nbytes", 0))
+        _check(self._lib.fkv_tree_attn(self.handle, _ptr(q), layer, m, _ptr(seq_lens),
+                                       _ptr(node_counts), _ptr(tree_mask), T, _ptr(out),
+                                       _ptr(workspace), nbytes, _stream(stream)), "fkv_tree_attn")
+        return out
+
+    def fkv_compact_rows(self, pos, idx, counts, A: Optional[int] = None, stream=None):
+        c = self.cfg
+        if A is None:
+            A = idx.shape[1]
+        self._need_cuda(pos, (c.batch,), torch.int32, "pos")
+        self._need_cuda(idx, (c.batch, A), torch.int32, "idx")
+        self._need_cuda(counts, (c.batch,), torch.int32, "counts")
+        _check(self._lib.fkv_compact_rows(self.handle, _ptr(pos), _ptr(idx), _ptr(counts), A,
+                                          _stream(stream)), "fkv_compact_rows")
+
+    def fkv_reorder_seqs(self, src, seq_lens, stream=None):
+        c = self.cfg
+        self._need_cuda(src, (c.batch,), torch.int32, "src")
+        self._need_cuda(seq_lens, (c.batch,), torch.int32, "seq_lens")
+        _check(self._lib.fkv_reorder_seqs(self.handle, _ptr(src), _ptr(seq_lens), _stream(stream)),
+               "fkv_reorder_seqs")
 
     def fkv_get_device_status(self, stream=None) -> int:
         """The device status code (FKV_OK, FKV_ERR_DEVICE_ARG, FKV_ERR_TIMEOUT);

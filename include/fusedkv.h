@@ -284,6 +284,87 @@ fkv_status fkv_prefill_attn(fkv_ctx* ctx, const void* q, int layer, int mode, in
 fkv_status fkv_prefill_attn_chunk(fkv_ctx* ctx, const void* q, int layer, int mode, int q_start,
                                   int C, void* out, void* stream);
 
+/* Speculative and beam decoding over the caches.  The pages stop at one token
+ * a step; the three calls below are this library's, on the same caches, modes
+ * and layers.  A round of speculative decoding:
+ *   1. draft up to T tokens per sequence that form a tree (a chain is a tree),
+ *      and fkv_append_kv their keys and values, at the rotary angles of their
+ *      depths, at positions seq_lens[b] .. seq_lens[b] + T - 1 of the storage
+ *      layers;
+ *   2. fkv_tree_attn in every layer, in the place of fkv_decode_attn;
+ *   3. accept a path of the tree and fkv_compact_rows its rows; the caller's
+ *      seq_lens grow by the path's length.  Rows behind the new length are
+ *      free, and the next append overwrites them.
+ * Beam search and parallel sampling call fkv_reorder_seqs between steps.
+ * All three are made with the context's device current
+ * (FKV_ERR_INVALID_ARG otherwise) and can be captured into a CUDA graph. */
+
+/* Bytes of device workspace fkv_tree_attn needs for T nodes per sequence, in
+ * any mode and cache format of this context (0 for a T that it refuses). */
+size_t fkv_tree_workspace_bytes(const fkv_ctx* ctx, int T);
+
+/* Attention of a tree of drafted tokens over a layer's cache.  Sequence b has
+ * P = seq_lens[b] committed rows, 0 <= P, and N = node_counts[b] drafted nodes
+ * (T where node_counts is NULL) whose rows lie at positions P .. P + N - 1,
+ * already appended; P + N <= S_max.  Node i sees every committed row, and the
+ * row of node j where bit j % 64 of tree_mask[b][i][j / 64] is set: for a tree,
+ * its ancestors and itself, though any mask is taken (bits of nodes that do
+ * not exist are ignored).  A node that sees nothing (P = 0 and no bit) gets
+ * zeros.  T = 1 with bit 0 set is fkv_decode_attn with length P + 1.
+ * Modes and sources are those of fkv_decode_attn, over bf16, fp32 and 4-bit
+ * caches.  Sliding windows: the depth of a node is the number of its set bits
+ * less one (0 where none or one is set), its position P + depth, and with a
+ * window W a node at position m sees the visible rows of positions above
+ * m - W (a drafted row's position is its node's).  Ring caches need every
+ * source to be a ring of the same size R (FKV_ERR_UNSUPPORTED otherwise), a
+ * window 1 <= W <= R (FKV_ERR_INVALID_ARG otherwise) and W + T - 1 <= R
+ * (FKV_ERR_UNSUPPORTED otherwise), so that the T appended rows have not
+ * overwritten a row that a node sees.
+ * q, out: device [B, H_q, T, D], context dtype.  seq_lens, node_counts: device
+ * int32 [B].  tree_mask: device [B, T, ceil(T / 64)] 64-bit words, 8-byte
+ * aligned.  1 <= T <= 128 (and T <= S_max).
+ * Outputs of nodes i >= N are left as they were; N = 0 skips a sequence.  A
+ * sequence with P < 0, N outside [0, T] or P + N > S_max gets zeros in all its
+ * T rows and FKV_ERR_DEVICE_ARG in the device status.
+ * Rows behind position P + N - 1, and rows that no node of the sequence sees,
+ * are not used, whatever they hold.
+ * workspace: device, 16-byte aligned, at least fkv_tree_workspace_bytes(ctx,
+ * T) bytes, no initialisation, as for fkv_decode_attn (also its note on graph
+ * replays that stopped early); not shared with a call that may run at the same
+ * time. */
+fkv_status fkv_tree_attn(fkv_ctx* ctx, const void* q, int layer, int mode,
+                         const int32_t* seq_lens, const int32_t* node_counts,
+                         const uint64_t* tree_mask, int T, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Keep an accepted path: in every layer with bound caches (of any format), K
+ * and V, and for every KV head, the row of position pos[b] + j takes what the
+ * row of position pos[b] + idx[b][j] held, 0 <= j < counts[b].  All rows are
+ * read before any is written, so idx may be in any order and may repeat.
+ * pos, counts: device int32 [B]; idx: device int32 [B, A], 0 <= A <= 128 (and
+ * A <= S_max); entries behind counts[b] are not read.  Other rows keep their
+ * contents.  Ring caches take positions modulo their rows.
+ * A buffer that is bound to several layers is moved once.
+ * A sequence with counts[b] outside [0, A], a position outside [0, S_max), or
+ * counts or an idx above the rows of the smallest ring bound is left as it was
+ * and flagged as FKV_ERR_DEVICE_ARG.  FKV_ERR_INVALID_ARG if no layer has
+ * caches. */
+fkv_status fkv_compact_rows(fkv_ctx* ctx, const int32_t* pos, const int32_t* idx,
+                            const int32_t* counts, int A, void* stream);
+
+/* Make sequences copies of others (a beam forks, samples share a prompt, the
+ * batch is sorted): in every layer with bound caches, K and V, rows
+ * [0, seq_lens[b]) of sequence b take what those rows of sequence src[b] held
+ * before the call.  Any map is taken, cycles too, in place.  src[b] = b or -1
+ * leaves the sequence as it is; rows from seq_lens[b] on keep their contents.
+ * Of a ring cache of R rows, min(seq_lens[b], R) rows are copied.
+ * src, seq_lens (the lengths after the call): device int32 [B].  A sequence
+ * with src[b] outside [-1, B) or seq_lens[b] outside [0, S_max] is left as it
+ * was and flagged as FKV_ERR_DEVICE_ARG.  A buffer that is bound to several
+ * layers is moved once.  FKV_ERR_INVALID_ARG if no layer has caches. */
+fkv_status fkv_reorder_seqs(fkv_ctx* ctx, const int32_t* src, const int32_t* seq_lens,
+                            void* stream);
+
 /* Synchronise the stream, then report and clear the device status word:
  * FKV_OK, FKV_ERR_DEVICE_ARG or FKV_ERR_TIMEOUT (FKV_ERR_CUDA if the sync
  * itself fails). */

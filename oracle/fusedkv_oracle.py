@@ -297,6 +297,61 @@ def append_kv(cache: np.ndarray, new: np.ndarray, pos: Sequence[int]) -> np.ndar
 
 
 # ---------------------------------------------------------------------------
+# Speculative and beam decoding (no counterpart on the pages): the definitions
+# that include/fusedkv.h states for the tree, compaction and reordering calls
+# ---------------------------------------------------------------------------
+
+def tree_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, seq_lens: Sequence[int],
+                   masks: Sequence[Sequence[int]], counts: Optional[Sequence[int]] = None,
+                   scale: Optional[float] = None, window: int = 0) -> np.ndarray:
+    """Drafted nodes of ``q[B, H_q, T, D]`` over ``k, v[B, H_kv, S, D]``.
+
+    Sequence b has ``P = seq_lens[b]`` committed rows and ``N = counts[b]``
+    nodes at rows P..P+N-1; ``masks[b][i]`` is an integer whose bit j says that
+    node i sees node j.  Rows of nodes i >= N are NaN (the call leaves them).
+    """
+    B, H, T, D = q.shape
+    G = H // k.shape[1]
+    scale = default_scale(D) if scale is None else scale
+    out = np.full((B, H, T, D), np.nan)
+    for b in range(B):
+        P, N = int(seq_lens[b]), T if counts is None else int(counts[b])
+        bits = [[(masks[b][i] >> j) & 1 for j in range(N)] for i in range(N)]
+        depth = [max(sum(r) - 1, 0) for r in bits]
+        for i in range(N):
+            rows = [t for t in range(P) if not window or t > P + depth[i] - window]
+            rows += [P + j for j in range(N)
+                     if bits[i][j] and (not window or P + depth[j] > P + depth[i] - window)]
+            for h in range(H):
+                if not rows:
+                    out[b, h, i] = 0.0
+                    continue
+                out[b, h, i] = attend(q[b, h, i], k[b, h // G][rows], v[b, h // G][rows], scale)
+    return out
+
+
+def compact_rows(cache: np.ndarray, pos: Sequence[int], idx: Sequence[Sequence[int]],
+                 counts: Sequence[int], ring: int = 0) -> np.ndarray:
+    """``cache[B, H_kv, S, X]`` after row pos+j took row pos+idx[j], j < count."""
+    new = cache.copy()
+    rows = ring or cache.shape[2]
+    for b in range(cache.shape[0]):
+        for j in range(int(counts[b])):
+            new[b, :, (pos[b] + j) % rows] = cache[b, :, (pos[b] + idx[b][j]) % rows]
+    return new
+
+
+def reorder_seqs(cache: np.ndarray, src: Sequence[int], seq_lens: Sequence[int]) -> np.ndarray:
+    """``cache[B, H_kv, S, X]`` after sequence b took the rows of src[b]."""
+    new = cache.copy()
+    for b in range(cache.shape[0]):
+        n = min(int(seq_lens[b]), cache.shape[2])
+        if src[b] >= 0:
+            new[b, :, :n] = cache[src[b], :, :n]
+    return new
+
+
+# ---------------------------------------------------------------------------
 # 4-bit KV cache ([Slides] "Four-bit KV quantization is the stronger
 # combination", Table 14).  KIVI's grouping is not on the pages; this library
 # quantises each token row of each head in groups of Q4_GROUP channels with
