@@ -151,6 +151,8 @@ struct TreeArgs {
 
 // Launch configuration of a tree attention call.
 struct TreePlan {
+  bool tensor;      // the tensor-core kernel (tree_tc.cu), else tree_simt.cu
+  int slots;        // its key / value tile slots
   int ranges;       // key ranges (grid.x)
   int rows;         // query rows per CTA
   int row_tiles;    // grid.y

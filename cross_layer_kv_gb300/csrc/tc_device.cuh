@@ -127,6 +127,17 @@ __device__ __forceinline__ void prefill_cta_tile(int& unit, int& mt) {
   mt = T - 1 - idx / gsz;
 }
 
+// 8 consecutive 32-bit TMEM columns of this thread's lane -> v.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // max(a, b, c) in one instruction.
 __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   float d;
@@ -224,6 +235,11 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with A MN-major too (both operands transposed).
+__host__ __device__ constexpr uint32_t idesc_bf16_tt(int M, int N) {
+  return idesc_bf16(M, N, true) | (1u << 15);
 }
 
 // Byte offset of the 16-byte chunk `lc` of row `r` inside one 64-byte-swizzled

@@ -5,7 +5,7 @@
 namespace fkv {
 
 cudaError_t tree_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
-  tree_simt_plan(a, num_sms, plan);
+  if (!tree_tc_plan(a, num_sms, plan)) tree_simt_plan(a, num_sms, plan);
   // two partial records per range and row tile, then the arrival words
   plan->partial_bytes = (size_t)plan->ranges * 2 * plan->row_tiles *
                         tree_record_floats(plan->rows, a.head_dim) * sizeof(float);
@@ -44,7 +44,7 @@ cudaError_t tree_launch(const TreeArgs& a, const TreePlan& plan, cudaStream_t st
   // recycled workspace may hold
   p.epoch = a.epoch * 0x9E3779B1u;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-  return tree_simt_launch(p, a, plan, stream);
+  return plan.tensor ? tree_tc_launch(p, a, plan, stream) : tree_simt_launch(p, a, plan, stream);
 }
 
 }  // namespace fkv

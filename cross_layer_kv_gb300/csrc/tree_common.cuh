@@ -24,6 +24,9 @@ namespace fkv {
 constexpr int kTreeMaxNodes = 128;
 
 struct TreeParams;
+bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
+cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
+                           cudaStream_t stream);
 void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
 cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
                              cudaStream_t stream);
@@ -49,29 +52,43 @@ struct TreeParams {
   float scale_log2; // softmax scale * log2(e)
 };
 
+// What a CTA keeps of the sequences in shared memory (3 B + 1 words).
+struct TreeSeqs {
+  int* pre;   // [B + 1] key tiles of one head of the sequences before b
+  int* P;     // [B] committed rows
+  int* N;     // [B] drafted nodes (0: nothing to do)
+};
+__host__ __device__ constexpr size_t tree_seqs_bytes(int B) { return (size_t)(3 * B + 1) * 4; }
+
+__device__ __forceinline__ TreeSeqs tree_seqs(int* words, int B) {
+  return TreeSeqs{words, words + B + 1, words + 2 * B + 1};
+}
+
 // One sequence of a call: its attended positions [start, n) lie in the cache
 // rows as one run of cntA rows and, in a ring that wraps, a second of cntB.
 struct TreeSeq {
-  int P, N, n, start, cntA, cntB;
-  bool bad;
+  int P, N, start, cntA, cntB;
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
-  TreeSeq s;
-  s.P = p.seq_lens[b];
-  s.N = p.node_counts ? p.node_counts[b] : p.T;
-  s.bad = s.P < 0 || s.N < 0 || s.N > p.T || s.P > p.S_max - s.N;
-  if (s.bad) s.P = s.N = 0;
-  s.n = s.N > 0 ? s.P + s.N : 0;
-  s.start = p.window > 0 && s.P >= p.window ? s.P - p.window + 1 : 0;
-  if (s.N == 0) s.start = 0;
-  int end = s.n;
+// The lengths of sequence b as the caller gave them; false if out of range.
+__device__ __forceinline__ bool tree_lengths(const TreeParams& p, int b, int& P, int& N) {
+  P = p.seq_lens[b];
+  N = p.node_counts ? p.node_counts[b] : p.T;
+  return P >= 0 && N >= 0 && N <= p.T && P <= p.S_max - N;
+}
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int P, int N) {
+  TreeSeq s{P, N, 0, 0, 0};
+  if (N == 0) return s;
+  const int n = P + N;
+  if (p.window > 0 && P >= p.window) s.start = P - p.window + 1;
+  int end = n;
   if (p.ring > 0) {
     const long long wrap = ((long long)s.start / p.ring + 1) * p.ring;
-    if (wrap < s.n) end = (int)wrap;
+    if (wrap < n) end = (int)wrap;
   }
   s.cntA = end - s.start;
-  s.cntB = s.n - end;
+  s.cntB = n - end;
   return s;
 }
 
@@ -114,38 +131,43 @@ __device__ __forceinline__ int tree_depth(const TreeParams& p, int b, int i, int
 }
 
 // The cut: the tiles of all units, unit by unit, in `ranges` equal contiguous
-// ranges.  pre[b] = tiles of one head of the sequences before b (B + 1 words
-// of shared memory).  Every thread of the CTA takes part.
+// ranges.  Fills sq; every thread of the CTA takes part.
 struct TreeCut {
   long long total;
   int ranges;
 };
 
-__device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, int* pre, int KT, int max_ranges) {
+__device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, const TreeSeqs& sq, int KT,
+                                            int max_ranges) {
   for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-    const TreeSeq s = tree_seq(p, i);
-    if (s.bad && blockIdx.x == 0 && blockIdx.y == 0) flag_status(p.status, kDevBadArg);
-    pre[i + 1] = tree_tiles(s, KT);
+    int P, N;
+    if (!tree_lengths(p, i, P, N)) {
+      if (blockIdx.x == 0 && blockIdx.y == 0) flag_status(p.status, kDevBadArg);
+      P = N = 0;
+    }
+    sq.P[i] = P;
+    sq.N[i] = N;
+    sq.pre[i + 1] = tree_tiles(tree_seq(p, P, N), KT);
   }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int run = 0;
     for (int base = 0; base < p.B; base += 32) {
-      int x = base + lane < p.B ? pre[base + lane + 1] : 0;
+      int x = base + lane < p.B ? sq.pre[base + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (base + lane < p.B) pre[base + lane + 1] = run + x;
+      if (base + lane < p.B) sq.pre[base + lane + 1] = run + x;
       run += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) pre[0] = 0;
+    if (lane == 0) sq.pre[0] = 0;
   }
   __syncthreads();
   TreeCut c;
-  c.total = (long long)p.H * pre[p.B];
+  c.total = (long long)p.H * sq.pre[p.B];
   c.ranges = (int)min((long long)max_ranges, c.total);
   return c;
 }
@@ -223,7 +245,8 @@ template <typename E>
 __device__ __forceinline__ void tree_zero_bad(const TreeParams& p, int D) {
   if (blockIdx.x != 0 || blockIdx.y != 0) return;
   for (int b = 0; b < p.B; ++b) {
-    if (!tree_seq(p, b).bad) continue;
+    int P, N;
+    if (tree_lengths(p, b, P, N)) continue;
     const size_t n = (size_t)p.H * p.G * p.T * D * sizeof(E) / 16;
     uint4* o = reinterpret_cast<uint4*>(p.out) + (size_t)b * n;
     for (size_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);

@@ -55,13 +55,14 @@ __global__ void __launch_bounds__(NT) tree_simt_kernel(const TreeParams p) {
   unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sA + RT);   // [RT][2]
   int* sDepth = reinterpret_cast<int*>(sMask + RT * 2);                          // [kTreeMaxNodes]
   int* flag = sDepth + kTreeMaxNodes;
-  int* pre = flag + 1;                                                           // [B + 1]
+  const TreeSeqs sq = tree_seqs(flag + 1, p.B);
+  const int* pre = sq.pre;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_trigger();
   grid_dep_wait();
   tree_zero_bad<E>(p, D);
-  const TreeCut cut = tree_cut(p, pre, KT, gridDim.x);
+  const TreeCut cut = tree_cut(p, sq, KT, gridDim.x);
   if ((int)blockIdx.x >= cut.ranges) return;
   const int rt = blockIdx.y;
   const size_t plane = p.ring > 0 ? p.ring : p.S_max;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(NT) tree_simt_kernel(const TreeParams p) {
   walk.begin(cut, pre, p.B, p.H, blockIdx.x);
   TreePiece pc;
   while (walk.next(pre, p.B, p.H, pc)) {
-    const TreeSeq s = tree_seq(p, pc.b);
+    const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
     const size_t unit = (size_t)pc.b * p.H + pc.h;
     const int rows = min(RT, p.G * p.T - rt * RT);
     __syncthreads();
@@ -271,7 +272,7 @@ void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
   // where there are fewer key tiles
   plan->ranges = a.num_ctas > 0 ? a.num_ctas : (2 * num_sms + plan->row_tiles - 1) / plan->row_tiles;
   plan->smem_bytes = (size_t)(RT * (a.head_dim + 4) + 2 * KT * (a.head_dim + 4) + RT * KT + 3 * RT) * 4 +
-                     RT * 16 + kTreeMaxNodes * 4 + (size_t)(a.batch + 2) * 4;
+                     RT * 16 + kTreeMaxNodes * 4 + 4 + tree_seqs_bytes(a.batch);
 }
 
 cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,

@@ -1,0 +1,746 @@
+// fkv_tree_attn on the tcgen05 tensor cores (bf16 caches).
+//
+// A drafted tree gives a (sequence, KV head) unit G * T query rows, few
+// against the cached keys, so the call is bound by reading the cache once.
+// The products are taken transposed, keys as the 128 rows of the MMA and the
+// query rows as its NC = 16 .. 128 columns: S^T = K Q^T, O^T = V^T P^T.  A
+// thread of the softmax then owns a key, not a query row, so that all 256
+// threads work however few query rows there are.
+//
+// Math.  Online softmax in base 2 with one reference m_c per column c; a tile
+// keeps the reference unless a score exceeds it by more than 2^8 (P stays
+// below 256, exact scaling), so the column maximum over the 128 threads is
+// only taken on the first tile of a piece and when the scores grow.  Fused
+// layers need no fused tile: S = K^1 (q a_1)^T + K^n (q a_n)^T accumulates in
+// one product, and O = b_1 (V^1 P) + b_n (V^n P) keeps two accumulators.
+// q a is rounded to bf16 (2^-9 of each product's term, random over channels),
+// and P to bf16 as in the prefill kernels; sums are fp32.
+//
+// A CTA takes a contiguous range of key tiles of 128 rows (tree_common.cuh)
+// and one tile of NC query rows:
+//  * the producer warp loads K and V tiles by TMA (64-byte swizzle) into a
+//    ring of slots, in the order in which the MMAs read them:
+//    K_0, K_1, V_0, K_2, V_1, ...;
+//  * the MMA warp issues S_j = K_j Q^T one tile ahead (S has two buffers in
+//    tensor memory) and O += V_j^T P_j;
+//  * two softmax warpgroups take half of the columns each: scores from tensor
+//    memory, P to shared memory as an MN-major operand (a thread writes its
+//    key's columns, 16 bytes at a time, without bank conflicts).
+// Tiles with drafted rows, a window's edge or a ragged end are masked, and the
+// value rows that nobody sees are zeroed in shared memory, since 0 * NaN is
+// no 0.  A drafted value row that is not finite is zeroed too and its score
+// made NaN, so that it stays with the nodes that see it.
+#include <cfloat>
+#include <cstring>
+
+#include "tc_device.cuh"
+#include "tree_common.cuh"
+
+namespace fkv {
+namespace {
+
+constexpr int KT = 128;               // keys per tile
+constexpr int SM_THREADS = 256;       // softmax threads
+constexpr int THREADS = SM_THREADS + 64;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
+constexpr int MAX_SLOTS = 12;
+constexpr int TAIL_ROWS = 16;         // rows of the boxes of a ragged tile
+constexpr int SMEM_LIMIT = 232448;
+constexpr float SLACK = 8.f;          // log2 growth of a score over its reference
+
+template <int D, int NSRC, int NC>
+struct TcCfg {
+  static constexpr int CB = (D + kSWE - 1) / kSWE;       // 32-channel blocks
+  static constexpr int SLOT = CB * KT * kSW;             // one K or V tile
+  static constexpr int Q_BYTES = NSRC * CB * NC * kSW;
+  static constexpr int P_BYTES = (NC + 31) / 32 * KT * kSW;
+  static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
+  // V^T is read as 128 channels: the MMA reads up to 4 blocks from a slot on,
+  // past its end into what follows (rows that are not used)
+  static constexpr int OVERRUN = (4 - CB) * KT * kSW;
+  static constexpr int MISC = 2 * MAX_SLOTS * 8 + 16 * 8 + 64          // barriers, words
+                              + NC * 4 * 8                             // reference, alpha, depth, node, sums
+                              + kTreeMaxNodes * (16 + 4 + NW * 4)      // masks, depths, column masks
+                              + 4 * NC * 4;                            // warp maxima / sums
+  static constexpr int FIXED = 512 + Q_BYTES + MISC;
+  static constexpr int TMEM_USED = (2 + NSRC) * NC;
+  static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
+                                   : TMEM_USED <= 256 ? 256 : 512;
+  static_assert(TMEM_USED <= 512, "tensor memory");
+  // two P buffers where at least five tile slots remain beside them
+  static constexpr int NPB = (SMEM_LIMIT - FIXED - 2 * P_BYTES - 12 * 64) / SLOT >= 5 ? 2 : 1;
+  static constexpr int HC = NC / 2;                      // columns of a softmax warpgroup
+};
+
+struct TcMaps {
+  CUtensorMap full[4];   // K first, K second, V first, V second: boxes of 128 rows
+  CUtensorMap tail[4];   // boxes of TAIL_ROWS rows
+};
+
+// Sum or maximum over the warp's lanes of N values a lane; afterwards lane i
+// holds the result of value i % N.  N = 8, 16 or 32.
+template <int N, typename Op>
+__device__ __forceinline__ float reduce_scatter(float* v, int lane, Op op) {
+#pragma unroll
+  for (int h = N / 2; h >= 1; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? v[i] : v[i + h];
+      const float keep = up ? v[i + h] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, h));
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (int h = N; h < 32; h <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, h));
+  return r;
+}
+
+__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__device__ __forceinline__ bool sm_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// Slot (counted from a piece's first) of the first source of K_i or V_i: the
+// order of a piece's n tiles is K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
+__device__ __forceinline__ int k_slot(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_slot(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 + 2 * i; }
+
+template <int D, int NSRC, bool WGT, int NC>
+__global__ void __launch_bounds__(THREADS, 1)
+    tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots) {
+  using C = TcCfg<D, NSRC, NC>;
+  constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~uintptr_t(511));
+  uint8_t* sRing = smem;
+  uint8_t* sQ = sRing + (size_t)nslots * C::SLOT;
+  uint8_t* sP = sQ + C::Q_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sP + NPB * C::P_BYTES);
+  uint64_t* empty = full + MAX_SLOTS;
+  uint64_t* q_ready = empty + MAX_SLOTS;
+  uint64_t* s_full = q_ready + 1;   // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* o_done = p_full + 2;    // [2]
+  uint64_t* drain = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
+  int* merge_flag = sm_issued + 1;
+  int* sm_span = merge_flag + 1;                               // [2] least and largest depth
+  unsigned long long* sMask =
+      reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(sm_span + 2) + 15) & ~uintptr_t(15));
+  float* sRef = reinterpret_cast<float*>(sMask + 2 * kTreeMaxNodes);   // [NC] reference
+  float* sAlpha = sRef + NC;                                   // [NC] rescale, then 1 / sum
+  int* sDepth = reinterpret_cast<int*>(sAlpha + NC);           // [NC] depth of the column's node
+  int* sNode = sDepth + NC;                                    // [NC] node of the column, -1: none
+  float* sWarp = reinterpret_cast<float*>(sNode + NC);         // [4][NC]
+  int* sNodeDepth = reinterpret_cast<int*>(sWarp + 4 * NC);    // [kTreeMaxNodes]
+  uint32_t* sVis = reinterpret_cast<uint32_t*>(sNodeDepth + kTreeMaxNodes);   // [kTreeMaxNodes][NW]
+  const TreeSeqs sq = tree_seqs(reinterpret_cast<int*>(sVis + kTreeMaxNodes * NW), p.B);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rt = blockIdx.y;
+  if (tid == 0) {
+    for (int s = 0; s < nslots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(q_ready, SM_THREADS);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], SM_THREADS);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *sm_issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  for (int c = tid; c < NC; c += THREADS) {
+    const int row = rt * NC + c;
+    sNode[c] = row < p.G * p.T ? row % p.T : -1;
+  }
+  grid_dep_trigger();
+  grid_dep_wait();
+  const unsigned long long wlim = wait_limit_ns(p.wait_limit);
+  tree_zero_bad<__nv_bfloat16>(p, D);
+  tc_fence_before();
+  const TreeCut cut = tree_cut(p, sq, KT, gridDim.x);   // ends with a __syncthreads
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool active = (int)blockIdx.x < cut.ranges;
+  TreeWalk walk;
+  if (active) walk.begin(cut, sq.pre, p.B, p.H, blockIdx.x);
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(bar, parity, wlim)) return true;
+    *abort_flag = 1;
+    flag_status(p.status, kDevTimeout);
+    return false;
+  };
+  auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
+
+  if (active && warp == PRODUCER_WARP) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      int g = 0;   // slots filled
+      bool ok = true;
+      TreePiece pc;
+      while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
+        const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
+        const int unit = pc.b * p.H + pc.h, n = pc.k1 - pc.k0;
+        // first the keys of tile i, then the values of tile i - 1
+        for (int i = 0; ok && i <= n; ++i)
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            const int tile = kv == 0 ? i : i - 1;
+            if (tile < 0 || tile >= n) continue;
+            const TreeTile t = tree_tile(p, s, pc.k0 + tile, KT);
+            for (int src = 0; src < NSRC; ++src, ++g) {
+              const int sl = g % nslots, u = g / nslots;
+              if (u > 0 && !wait(&empty[sl], (uint32_t)(u - 1) & 1u)) {
+                ok = false;
+                break;
+              }
+              const int m = kv * 2 + src;
+              uint8_t* dst = slot_ptr(sl);
+              if (t.cnt == KT) {
+                mbar_arrive_expect_tx(&full[sl], C::SLOT);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                  tma_load_3d(dst + cb * KT * kSW, &maps.full[m], cb * kSWE, t.row, unit, &full[sl]);
+              } else {
+                const int boxes = (t.cnt + TAIL_ROWS - 1) / TAIL_ROWS;
+                mbar_arrive_expect_tx(&full[sl], boxes * CB * TAIL_ROWS * kSW);
+                for (int x = 0; x < boxes; ++x)
+#pragma unroll
+                  for (int cb = 0; cb < CB; ++cb)
+                    tma_load_3d(dst + cb * KT * kSW + x * TAIL_ROWS * kSW, &maps.tail[m], cb * kSWE,
+                                t.row + x * TAIL_ROWS, unit, &full[sl]);
+              }
+            }
+          }
+      }
+      *sm_issued = g;
+    }
+  } else if (active && warp == MMA_WARP) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
+      constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
+      int base = 0;   // slots of the pieces before
+      int jt = 0;     // tiles of the pieces before
+      int piece = 0;
+      bool ok = true;
+      TreePiece pc;
+      while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
+        const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
+        const int n = pc.k1 - pc.k0;
+        auto full_wait = [&](int g) { return wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u); };
+        auto issue_qk = [&](int i) -> bool {
+          const int g0 = base + k_slot(i) * NSRC;
+          const uint32_t d = tmem + ((jt + i) & 1) * NC;
+          for (int src = 0; src < NSRC; ++src) {
+            if (!full_wait(g0 + src)) return false;
+            tc_fence_after();
+            const uint32_t kb = smem_u32(slot_ptr((g0 + src) % nslots));
+            const uint32_t qb = smem_u32(sQ + src * CB * NC * kSW);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (uint32_t)(k & 1) * 32;
+              mma_bf16(d, sdesc(kb + (k >> 1) * KT * kSW + off, 16, 8 * kSW),
+                       sdesc(qb + (k >> 1) * NC * kSW + off, 16, 8 * kSW), IDESC_QK, (src | k) ? 1u : 0u);
+            }
+            mma_commit(&empty[(g0 + src) % nslots]);
+          }
+          mma_commit(&s_full[(jt + i) & 1]);
+          return true;
+        };
+        ok = wait(q_ready, (uint32_t)piece & 1u);
+        if (ok) tc_fence_after();
+        ok = ok && issue_qk(0);
+        for (int i = 0; ok && i < n; ++i) {
+          if (i + 1 < n && !issue_qk(i + 1)) {
+            ok = false;
+            break;
+          }
+          const int j = jt + i;
+          if (!wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          const int g0 = base + v_slot(i, n) * NSRC;
+          const int ks = (tree_tile(p, s, pc.k0 + i, KT).cnt + 15) / 16;
+          const uint32_t pb = smem_u32(sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0));
+          for (int src = 0; src < NSRC; ++src) {
+            if (!full_wait(g0 + src)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t vb = smem_u32(slot_ptr((g0 + src) % nslots));
+            const uint32_t d = tmem + (2 + src) * NC;
+            for (int k = 0; k < ks; ++k)
+              mma_bf16(d, sdesc(vb + k * 16 * kSW, KT * kSW, 8 * kSW),
+                       sdesc(pb + k * 16 * kSW, KT * kSW, 8 * kSW), IDESC_PV, (i | k) ? 1u : 0u);
+            mma_commit(&empty[(g0 + src) % nslots]);
+          }
+          if (ok) mma_commit(&o_done[j & 1]);
+        }
+        base += 2 * n * NSRC;
+        jt += n;
+        ++piece;
+      }
+    }
+  } else if (active && warp < 8) {
+    // ---------------- softmax ----------------
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
+    const int c0 = wg * HC;                // first column
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+    auto fmaxop = [](float a, float b) { return fmaxf(a, b); };
+    auto addop = [](float a, float b) { return a + b; };
+    int base = 0, jt = 0;
+    bool ok = true;
+    TreePiece pc;
+    while (walk.next(sq.pre, p.B, p.H, pc)) {
+      const int P = sq.P[pc.b], N = sq.N[pc.b];
+      const TreeSeq s = tree_seq(p, P, N);
+      const size_t unit = (size_t)pc.b * p.H + pc.h;
+      const int n = pc.k1 - pc.k0;
+      const int rows = min(NC, p.G * p.T - rt * NC);
+
+      // the piece's queries times the key weights, in the MMA's layout
+      for (int it = tid; it < NC * (CB * 4); it += SM_THREADS) {
+        const int r = it / (CB * 4), ch = it - r * (CB * 4);   // 16-byte chunk of a row
+        const int d = ch * 8;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < rows && d < D)
+          w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                              (unit * p.G * p.T + rt * NC + r) * D + d);
+        float f[8];
+        unpack16<__nv_bfloat16>(w, f);
+#pragma unroll
+        for (int src = 0; src < NSRC; ++src) {
+          uint4 o = w;
+          if constexpr (WGT) {
+            if (d < D) {
+              const float4* ap = reinterpret_cast<const float4*>(p.a[src] + (size_t)pc.h * D + d);
+              const float4 a0 = ap[0], a1 = ap[1];
+              uint32_t x[4];
+              const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v2 =
+                    __floats2bfloat162_rn(f[2 * e] * av[2 * e], f[2 * e + 1] * av[2 * e + 1]);
+                x[e] = *reinterpret_cast<const uint32_t*>(&v2);
+              }
+              o = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          *reinterpret_cast<uint4*>(sQ + src * CB * NC * kSW + (ch >> 2) * NC * kSW + swz64(r, ch & 3)) = o;
+        }
+      }
+      // the nodes' masks and depths, then per drafted key the columns that see it
+      if (tid < kTreeMaxNodes) {
+        unsigned long long m0 = 0, m1 = 0;
+        if (tid < N) {
+          m0 = tree_mask_word(p, pc.b, tid, 0, N);
+          if (p.words > 1) m1 = tree_mask_word(p, pc.b, tid, 1, N);
+        }
+        sMask[2 * tid] = m0;
+        sMask[2 * tid + 1] = m1;
+        sNodeDepth[tid] = max(__popcll(m0) + __popcll(m1), 1) - 1;
+      }
+      if (tid == 0) {
+        sm_span[0] = kTreeMaxNodes;
+        sm_span[1] = 0;
+      }
+      if (tid < NC) sRef[tid] = -FLT_MAX;
+      sm_sync();
+      if (tid < NC) {
+        const int i = sNode[tid];
+        const int d = i >= 0 && i < N ? sNodeDepth[i] : 0;
+        sDepth[tid] = d;
+        if (i >= 0 && i < N) {
+          atomicMin(&sm_span[0], d);
+          atomicMax(&sm_span[1], d);
+        }
+      }
+      for (int it = tid; it < N * NW; it += SM_THREADS) {
+        const int j = it / NW, w = it - j * NW;
+        uint32_t v = 0;
+#pragma unroll 4
+        for (int c = 0; c < 32 && w * 32 + c < NC; ++c) {
+          const int i = sNode[w * 32 + c];
+          if (i < 0 || i >= N) continue;
+          const bool in = p.window == 0 || sNodeDepth[j] > sNodeDepth[i] - p.window;
+          v |= (uint32_t)(in && (sMask[2 * i + (j >> 6)] >> (j & 63) & 1)) << c;
+        }
+        sVis[j * NW + w] = v;
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(q_ready);
+      sm_sync();
+      const int least = sm_span[0], most = sm_span[1];
+
+      float l[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) l[c] = 0.f;
+
+      for (int i = 0; i < n; ++i) {
+        const int j = jt + i;
+        const TreeTile t = tree_tile(p, s, pc.k0 + i, KT);
+        if (ok && !__all_sync(0xffffffffu, wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u))) ok = false;
+        tc_fence_after();
+        float sv[HC];
+        const uint32_t ts = t_lane + (j & 1) * NC;
+        if constexpr (HC == 8) {
+          tmem_ld8(ts, sv);
+        } else if constexpr (HC == 16) {
+          tmem_ld16(ts, sv);
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) tmem_ld32(ts + c, sv + c);
+        }
+        tmem_wait_ld();
+
+        const bool edge = p.window > 0 && t.pos <= P + most - p.window;
+        if (t.cnt < KT || t.pos + t.cnt > P || edge) {   // uniform over the CTA
+          // wait for the tile's values: unseen rows are zeroed, rows that are
+          // not finite are noted
+          // (once the products of the tile before are done, the slots' phases
+          // before the awaited ones are known to be over)
+          if (i > 0 && ok &&
+              !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
+            ok = false;
+          const int g0 = base + v_slot(i, n) * NSRC;
+#pragma unroll
+          for (int src = 0; src < NSRC; ++src) {
+            const int g = g0 + src;
+            if (ok && !__all_sync(0xffffffffu, wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u)))
+              ok = false;
+          }
+          const int q = t.pos + key - P;   // >= 0: drafted node q
+          bool seen = false, poison = false;
+          if (key < t.cnt) {
+            if (q < 0) {
+              seen = p.window == 0 || least < q + p.window;
+            } else {
+#pragma unroll
+              for (int w = 0; w < NW; ++w) seen |= sVis[q * NW + w] != 0;
+            }
+            if (seen && ok && (q >= 0 || p.window > 0)) {
+#pragma unroll 1
+              for (int src = 0; src < NSRC; ++src) {
+                const uint8_t* v = slot_ptr((g0 + src) % nslots);
+#pragma unroll 1
+                for (int ch = 0; ch < D / 8; ++ch) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(v + (ch >> 2) * KT * kSW + swz64(key, ch & 3));
+                  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    poison |= (xs[e] & 0x7f80u) == 0x7f80u || (xs[e] & 0x7f800000u) == 0x7f800000u;
+                }
+              }
+            }
+          }
+          sm_sync();   // both warpgroups have looked
+          if (wg == 0 && ok && (!seen || poison) && key < (t.cnt + 15) / 16 * 16) {
+#pragma unroll 1
+            for (int src = 0; src < NSRC; ++src) {
+              uint8_t* v = slot_ptr((g0 + src) % nslots);
+#pragma unroll 1
+              for (int ch = 0; ch < CB * 4; ++ch)
+                *reinterpret_cast<uint4*>(v + (ch >> 2) * KT * kSW + swz64(key, ch & 3)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          uint32_t vis[NW];
+#pragma unroll
+          for (int w = 0; w < NW; ++w) vis[w] = key >= t.cnt ? 0u : q >= 0 ? sVis[q * NW + w] : ~0u;
+          const int reach = q < 0 && p.window > 0 ? q + p.window : kTreeMaxNodes;   // depths below it see the key
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            const int cc = c0 + c;
+            const bool see = (vis[cc >> 5] >> (cc & 31) & 1u) && sDepth[cc] < reach;
+            sv[c] = !see ? -INFINITY : poison ? NAN : sv[c];
+          }
+        }
+
+        // does a score exceed its reference by more than the slack?
+        float over = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < HC; c += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(sRef + c0 + c);
+          over = fmaxf(over, fmaf(sv[c], p.scale_log2, -r.x));
+          over = fmaxf(over, fmaf(sv[c + 1], p.scale_log2, -r.y));
+          over = fmaxf(over, fmaf(sv[c + 2], p.scale_log2, -r.z));
+          over = fmaxf(over, fmaf(sv[c + 3], p.scale_log2, -r.w));
+        }
+        if (sm_any(over > SLACK || !ok)) {
+          if (sm_any(!ok)) {
+            ok = false;
+            break;
+          }
+          // new references: the columns' maxima so far
+          constexpr int RN = HC < 32 ? HC : 32;
+#pragma unroll
+          for (int b0 = 0; b0 < HC; b0 += RN) {
+            float v[RN];
+#pragma unroll
+            for (int c = 0; c < RN; ++c) v[c] = sv[b0 + c];
+            const float m = reduce_scatter<RN>(v, lane, fmaxop);
+            if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
+          }
+          sm_sync();
+          if (tid < NC) {
+            const float m = fmaxf(fmaxf(sWarp[tid], sWarp[NC + tid]), fmaxf(sWarp[2 * NC + tid], sWarp[3 * NC + tid]));
+            const float old = sRef[tid], top = fmaxf(old, m * p.scale_log2);
+            sAlpha[tid] = fast_exp2(old - top);
+            sRef[tid] = top;
+          }
+          // O holds every product before this tile once the last one is done
+          if (i > 0 && !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
+            ok = false;
+          tc_fence_after();
+          sm_sync();
+#pragma unroll
+          for (int c = 0; c < HC; c += 8) {
+            float al[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              al[e] = sAlpha[c0 + c + e];
+              l[c + e] *= al[e];
+            }
+            if (i > 0) {
+#pragma unroll
+              for (int src = 0; src < NSRC; ++src) {
+                const uint32_t to = t_lane + (2 + src) * NC + c;
+                float o[8];
+                tmem_ld8(to, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= al[e];
+                tmem_st8(to, o);
+              }
+            }
+          }
+          tmem_wait_st();
+        }
+
+        // P of this key: exp2(s * scale - reference), bf16
+        const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
+        if (pj >= 0 && ok && !__all_sync(0xffffffffu, wait(&o_done[pj & 1], (uint32_t)(pj >> 1) & 1u)))
+          ok = false;
+        uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
+#pragma unroll
+        for (int c = 0; c < HC; c += 8) {
+          float ref[8];
+          *reinterpret_cast<float4*>(ref) = *reinterpret_cast<const float4*>(sRef + c0 + c);
+          *reinterpret_cast<float4*>(ref + 4) = *reinterpret_cast<const float4*>(sRef + c0 + c + 4);
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float e0 = fast_exp2(fmaf(sv[c + e], p.scale_log2, -ref[e]));
+            const float e1 = fast_exp2(fmaf(sv[c + e + 1], p.scale_log2, -ref[e + 1]));
+            add2(l[c + e], l[c + e + 1], e0, e1);
+            const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
+            w[e / 2] = *reinterpret_cast<const uint32_t*>(&v2);
+          }
+          const int cc = c0 + c;
+          *reinterpret_cast<uint4*>(pb + (cc >> 5) * KT * kSW + swz64(key, (cc & 31) >> 3)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (ok) mbar_arrive(&p_full[j & 1]);
+      }
+      // the sums of the columns over all keys, and the last products
+      const int jl = jt + n - 1;
+      if (ok && !__all_sync(0xffffffffu, wait(&o_done[jl & 1], (uint32_t)(jl >> 1) & 1u))) ok = false;
+      if (sm_any(!ok)) break;
+      tc_fence_after();
+      constexpr int RN = HC < 32 ? HC : 32;
+#pragma unroll
+      for (int b0 = 0; b0 < HC; b0 += RN) {
+        const float m = reduce_scatter<RN>(l + b0, lane, addop);
+        if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
+      }
+      sm_sync();
+      const bool whole = n == pc.tiles;
+      float* rec = p.ws + ((size_t)(2 * blockIdx.x + (pc.first ? 0 : 1)) * p.row_tiles + rt) *
+                              tree_record_floats(NC, D);
+      if (tid < NC) {
+        const float sum = (sWarp[tid] + sWarp[NC + tid]) + (sWarp[2 * NC + tid] + sWarp[3 * NC + tid]);
+        sAlpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole) {
+          rec[NC * D + tid] = sRef[tid];
+          rec[NC * D + NC + tid] = sum;
+        }
+      }
+      sm_sync();
+      float b0w = 1.f, b1w = 0.f;
+      if (WGT && key < D) {
+        b0w = p.b[0][(size_t)pc.h * D + key];
+        if constexpr (NSRC == 2) b1w = p.b[1][(size_t)pc.h * D + key];
+      }
+#pragma unroll 1
+      for (int c = 0; c < HC; c += 8) {
+        float o[8], o2[8];
+        tmem_ld8(t_lane + 2 * NC + c, o);
+        if constexpr (NSRC == 2) tmem_ld8(t_lane + 3 * NC + c, o2);
+        tmem_wait_ld();
+        if (key < D) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float x = o[e];
+            if constexpr (WGT) x *= b0w;
+            if constexpr (NSRC == 2) x = fmaf(b1w, o2[e], x);
+            const int cc = c0 + c + e;
+            if (whole) {
+              const int node = sNode[cc];
+              const float inv = sAlpha[cc];
+              if (node >= 0 && node < N)
+                static_cast<__nv_bfloat16*>(p.out)[(unit * p.G * p.T + rt * NC + cc) * D + key] =
+                    __float2bfloat16_rn(inv == 0.f ? 0.f : x * inv);
+            } else {
+              rec[(size_t)cc * D + key] = x;
+            }
+          }
+        }
+      }
+      if (!whole)
+        tree_publish<__nv_bfloat16, D, NC>(p, cut, sq.pre, pc.b, pc.h, N, tid, SM_THREADS, merge_flag, sm_sync);
+      sm_sync();   // shared words are free for the next piece
+      base += 2 * n * NSRC;
+      jt += n;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // no role may have awaited the last copies and products: let them finish
+    if (warp == PRODUCER_WARP && lane == 0) {
+      const int issued = *sm_issued;
+      for (int g = max(0, issued - nslots); g < issued; ++g)
+        (void)mbar_wait_bounded(&full[g % nslots], (uint32_t)(g / nslots) & 1u, kDrainLimitNs);
+    }
+    if (warp == MMA_WARP && lane == 0) {
+      mma_commit(drain);
+      (void)mbar_wait_bounded(drain, 0, kDrainLimitNs);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Tile slots and shared memory of a configuration, or 0 slots if it does not fit.
+template <int D, int NSRC, int NC>
+void size_tc(int B, TreePlan* plan) {
+  using C = TcCfg<D, NSRC, NC>;
+  const size_t fixed = C::FIXED + C::NPB * C::P_BYTES + tree_seqs_bytes(B) + 64;
+  int slots = fixed < SMEM_LIMIT ? (int)((SMEM_LIMIT - fixed) / C::SLOT) : 0;
+  if (slots > MAX_SLOTS) slots = MAX_SLOTS;
+  // the blocks past the last slot's end lie in Q and P
+  if (slots < 2 * NSRC || C::OVERRUN > C::Q_BYTES + C::NPB * C::P_BYTES) slots = 0;
+  plan->slots = slots;
+  plan->smem_bytes = fixed + (size_t)slots * C::SLOT;
+}
+
+template <int D, int NSRC, bool WGT, int NC>
+cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+  TcMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int rows = a.ring > 0 ? a.ring : a.max_seq;
+  const long long units = (long long)a.batch * a.kv_heads;
+  bool ok = true;
+  for (int i = 0; i < 4; ++i) {
+    if ((i & 1) >= NSRC) continue;
+    const void* ptr = i < 2 ? a.k[i & 1] : a.v[i & 1];
+    ok = ok && make_map(&maps.full[i], ptr, D, rows, units, (size_t)rows * D * 2, KT);
+    ok = ok && make_map(&maps.tail[i], ptr, D, rows, units, (size_t)rows * D * 2, TAIL_ROWS);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  auto kern = tree_tc_kernel<D, NSRC, WGT, NC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(THREADS), plan.smem_bytes, stream, maps, p,
+                    plan.slots);
+}
+
+// Call f.template operator()<D, NSRC, NC>() for the plan's configuration.
+template <typename F>
+auto dispatch_tc(int D, int nsrc, int rows, F f) {
+  auto cols = [&](auto d, auto ns) {
+    switch (rows) {
+      case 16: return f(d, ns, std::integral_constant<int, 16>());
+      case 32: return f(d, ns, std::integral_constant<int, 32>());
+      case 64: return f(d, ns, std::integral_constant<int, 64>());
+      default: return f(d, ns, std::integral_constant<int, 128>());
+    }
+  };
+  auto dims = [&](auto ns) {
+    switch (D) {
+      case 64: return cols(std::integral_constant<int, 64>(), ns);
+      case 80: return cols(std::integral_constant<int, 80>(), ns);
+      case 96: return cols(std::integral_constant<int, 96>(), ns);
+      default: return cols(std::integral_constant<int, 128>(), ns);
+    }
+  };
+  return nsrc == 2 ? dims(std::integral_constant<int, 2>()) : dims(std::integral_constant<int, 1>());
+}
+
+}  // namespace
+
+bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
+  if (a.is_f32 || a.q4) return false;
+  const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
+  plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  // fused rows of 128 channels leave too little room for tiles beside 128 columns
+  if (nsrc == 2 && a.head_dim == 128 && plan->rows == 128) plan->rows = 64;
+  plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
+  dispatch_tc(a.head_dim, nsrc, plan->rows, [&](auto d, auto ns, auto nc) {
+    size_tc<decltype(d)::value, decltype(ns)::value, decltype(nc)::value>(a.batch, plan);
+  });
+  if (plan->slots == 0) return false;
+  // one CTA an SM over ranges and row tiles; the device takes fewer ranges
+  // where there are fewer key tiles
+  plan->ranges = a.num_ctas > 0 ? a.num_ctas : num_sms / plan->row_tiles > 0 ? num_sms / plan->row_tiles : 1;
+  plan->tensor = true;
+  return true;
+}
+
+cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+  return dispatch_tc(a.head_dim, a.k[1] ? 2 : 1, plan.rows, [&](auto d, auto ns, auto nc) {
+    constexpr int D = decltype(d)::value, NS = decltype(ns)::value, NC = decltype(nc)::value;
+    if constexpr (NS == 2) {
+      return launch_tc<D, 2, true, NC>(p, a, plan, stream);
+    } else {
+      if (a.a[0]) return launch_tc<D, 1, true, NC>(p, a, plan, stream);
+      return launch_tc<D, 1, false, NC>(p, a, plan, stream);
+    }
+  });
+}
+
+}  // namespace fkv
