@@ -1,7 +1,9 @@
 // tcgen05 (tensor memory, MMA) and tensor-map TMA wrappers shared by the
-// prefill kernels.  sm_103a only; every operand layout here is the 64-byte
-// swizzle: rows of 64 bytes (32 bf16), 16-byte chunks XOR-permuted by
-// ((row >> 1) & 3), the pattern TMA writes and the MMA descriptors read.
+// prefill and tree kernels.  sm_103a only.  Operand layouts are the 64-byte
+// swizzle (prefill: rows of 64 bytes, 32 bf16, 16-byte chunks XOR-permuted by
+// ((row >> 1) & 3)) and the 128-byte one (tree: rows of 128 bytes, chunks
+// permuted by (row & 7)), the patterns TMA writes and the MMA descriptors
+// read.
 #pragma once
 
 #include <cuda.h>
@@ -44,6 +46,18 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with the accumulate flag known at compile time.
+template <bool ACC>
+__device__ __forceinline__ void mma_bf16_t(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
 }
 
@@ -230,6 +244,22 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
   return d;
 }
 
+// The same for the 128-byte swizzle (mode 2), as its two words: the low one
+// takes (byte offset >> 4) added for another start in the same layout, so that
+// an issuing thread spends one addition on an operand.
+struct SDesc128 {
+  uint32_t lo, hi;
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return d;
+  }
+};
+__device__ __forceinline__ SDesc128 sdesc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return SDesc128{((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16),
+                  ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29)};
+}
+
 // Instruction descriptor for kind::f16: fp32 accumulator, bf16 A and B,
 // A K-major, B K-major or MN-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
@@ -246,6 +276,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16_tt(int M, int N) {
 // block whose rows are 64 bytes (the pattern TMA writes and the MMA reads).
 __device__ __forceinline__ uint32_t swz64(int r, int lc) {
   return (uint32_t)(r * kSW + ((lc ^ ((r >> 1) & 3)) << 4));
+}
+
+// The same for a 128-byte-swizzled block whose rows are 128 bytes.
+__device__ __forceinline__ uint32_t swz128(int r, int lc) {
+  return (uint32_t)(r * 128 + ((lc ^ (r & 7)) << 4));
+}
+
+// Fetch a tensor map ahead of its first use.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // --- host: tensor maps ---------------------------------------------------------
@@ -265,20 +305,26 @@ inline PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 }
 
 // 3-D bf16 map over rows of D elements: dims {D, rows, planes}, row stride
-// D*2 bytes, plane stride `plane_bytes`; box {32, box_rows, 1}, 64-byte swizzle.
-// Rows at or beyond `rows` read as zero.
-inline bool make_map(CUtensorMap* m, const void* base, int D, int rows, long long planes,
-              size_t plane_bytes, int box_rows) {
+// D*2 bytes, plane stride `plane_bytes`; box {box_cols, box_rows, 1}, swizzle
+// as given.  Rows at or beyond `rows` and columns beyond D read as zero.
+inline bool make_map_box(CUtensorMap* m, const void* base, int D, int rows, long long planes,
+                         size_t plane_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   auto enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)plane_bytes};
-  cuuint32_t box[3] = {(cuuint32_t)kSWE, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// Boxes of 32 columns, 64-byte swizzle.
+inline bool make_map(CUtensorMap* m, const void* base, int D, int rows, long long planes,
+                     size_t plane_bytes, int box_rows) {
+  return make_map_box(m, base, D, rows, planes, plane_bytes, kSWE, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace fkv

@@ -55,7 +55,7 @@ struct TreeParams {
 // What a CTA keeps of the sequences in shared memory (3 B + 1 words).
 struct TreeSeqs {
   int* pre;   // [B + 1] key tiles of one head of the sequences before b
-  int* P;     // [B] committed rows
+  int* P;     // [B] committed rows (-1: lengths out of range)
   int* N;     // [B] drafted nodes (0: nothing to do)
 };
 __host__ __device__ constexpr size_t tree_seqs_bytes(int B) { return (size_t)(3 * B + 1) * 4; }
@@ -131,25 +131,38 @@ __device__ __forceinline__ int tree_depth(const TreeParams& p, int b, int i, int
 }
 
 // The cut: the tiles of all units, unit by unit, in `ranges` equal contiguous
-// ranges.  Fills sq; every thread of the CTA takes part.
+// ranges.  Fills sq, and zeros the output of the sequences whose lengths are
+// out of range; every thread of the CTA takes part.
 struct TreeCut {
   long long total;
   int ranges;
 };
 
+template <typename E, int D>
 __device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, const TreeSeqs& sq, int KT,
                                             int max_ranges) {
+  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+  bool bad = false;
   for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
     int P, N;
     if (!tree_lengths(p, i, P, N)) {
-      if (blockIdx.x == 0 && blockIdx.y == 0) flag_status(p.status, kDevBadArg);
-      P = N = 0;
+      bad = true;
+      P = -1;
+      N = 0;
     }
     sq.P[i] = P;
     sq.N[i] = N;
     sq.pre[i + 1] = tree_tiles(tree_seq(p, P, N), KT);
   }
-  __syncthreads();
+  if (__syncthreads_or(bad) && first) {
+    if (threadIdx.x == 0) flag_status(p.status, kDevBadArg);
+    const size_t n = (size_t)p.H * p.G * p.T * D * sizeof(E) / 16;
+    for (int b = 0; b < p.B; ++b) {
+      if (sq.P[b] >= 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(p.out) + (size_t)b * n;
+      for (size_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int run = 0;
@@ -240,19 +253,6 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeCut& c, const int* pre, 
   return u;
 }
 
-// Zero output rows of the sequences whose lengths are out of range.
-template <typename E>
-__device__ __forceinline__ void tree_zero_bad(const TreeParams& p, int D) {
-  if (blockIdx.x != 0 || blockIdx.y != 0) return;
-  for (int b = 0; b < p.B; ++b) {
-    int P, N;
-    if (tree_lengths(p, b, P, N)) continue;
-    const size_t n = (size_t)p.H * p.G * p.T * D * sizeof(E) / 16;
-    uint4* o = reinterpret_cast<uint4*>(p.out) + (size_t)b * n;
-    for (size_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);
-  }
-}
-
 __device__ __forceinline__ void tree_store4(float* dst, const float* x) {
   *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
 }
@@ -264,11 +264,13 @@ __device__ __forceinline__ void tree_store4(__nv_bfloat16* dst, const float* x) 
 
 // Announce a written partial of unit (b, h), row tile blockIdx.y; the CTA
 // whose arrival completes the unit merges its pieces by their log-sum-exp
-// weights into the output rows.  Called by `nthreads` threads (index tid)
-// that `sync` brings together; all of them have written their part before.
-template <typename E, int D, int ROWS, typename Sync>
+// weights into the output rows.  Called by NT threads (index tid) that `sync`
+// brings together; all of them have written their part before.  scratch holds
+// 2 * ROWS floats of shared memory.  A thread's items (four channels of a row)
+// are loaded together, so a merge of P pieces takes P + 1 trips to L2.
+template <typename E, int D, int ROWS, int NT, typename Sync>
 __device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut& c, const int* pre,
-                                             int b, int h, int N, int tid, int nthreads, int* flag,
+                                             int b, int h, int N, int tid, int* flag, float* scratch,
                                              Sync sync) {
   const TreeUnit u = tree_unit(c, pre, p.H, b, h);
   const int P = (int)(u.last - u.first + 1);
@@ -289,37 +291,61 @@ __device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut&
   if (!*flag) return;
   constexpr int REC = tree_record_floats(ROWS, D);
   constexpr int C4 = D / 4;
+  constexpr int ITEMS = (ROWS * C4 + NT - 1) / NT;
   const int rows = min(ROWS, p.G * p.T - rt * ROWS);
   auto rec = [&](int i) {
     const long long slot = 2 * (u.first + i) + (i == 0 && u.first_is_tail ? 1 : 0);
-    return p.ws + ((size_t)slot * p.row_tiles + rt) * REC;
+    return p.ws + ((size_t)slot * p.row_tiles + rt) * REC + ROWS * D;   // its m; o lies before
   };
-  for (int it = tid; it < rows * C4; it += nthreads) {
-    const int r = it / C4, d = (it - r * C4) * 4;
-    const int row = rt * ROWS + r;
-    if (row % p.T >= N) continue;
-    float M = -FLT_MAX;
-#pragma unroll 4
-    for (int i = 0; i < P; ++i) M = fmaxf(M, __ldcg(rec(i) + ROWS * D + r));
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float* sTop = scratch;
+  float* sInv = scratch + ROWS;
+  if (tid < ROWS) {
+    float M = -FLT_MAX, L = 0.f;
 #pragma unroll 4
     for (int i = 0; i < P; ++i) {
-      const float* q = rec(i);
-      const float w = exp2f(__ldcg(q + ROWS * D + r) - M);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
-      L = fmaf(w, __ldcg(q + ROWS * D + ROWS + r), L);
-      acc[0] = fmaf(w, o.x, acc[0]);
-      acc[1] = fmaf(w, o.y, acc[1]);
-      acc[2] = fmaf(w, o.z, acc[2]);
-      acc[3] = fmaf(w, o.w, acc[3]);
+      const float m = __ldcg(rec(i) + tid), l = __ldcg(rec(i) + ROWS + tid);
+      const float top = fmaxf(M, m);
+      L = L * exp2f(M - top) + l * exp2f(m - top);
+      M = top;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= inv;
-    tree_store4(static_cast<E*>(p.out) +
-                    (((size_t)b * p.H + h) * p.G * p.T + row) * D + d, acc);
+    sTop[tid] = M;
+    sInv[tid] = L == 0.f ? 0.f : 1.f / L;
   }
-  sync();   // the flag may be written again
+  sync();
+  float acc[ITEMS][4];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < P; ++i) {
+    const float* m = rec(i);
+    const float* o = m - ROWS * D;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int it = tid + k * NT;
+      if (it >= ROWS * C4) break;
+      const int r = it / C4;
+      const float w = exp2f(__ldcg(m + r) - sTop[r]);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(o + it * 4));
+      acc[k][0] = fmaf(w, x.x, acc[k][0]);
+      acc[k][1] = fmaf(w, x.y, acc[k][1]);
+      acc[k][2] = fmaf(w, x.z, acc[k][2]);
+      acc[k][3] = fmaf(w, x.w, acc[k][3]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int it = tid + k * NT;
+    if (it >= ROWS * C4) break;
+    const int r = it / C4, d = (it - r * C4) * 4;
+    const int row = rt * ROWS + r;
+    if (r >= rows || row % p.T >= N) continue;
+    const float inv = sInv[r];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[k][e] = inv == 0.f ? 0.f : acc[k][e] * inv;
+    tree_store4(static_cast<E*>(p.out) + (((size_t)b * p.H + h) * p.G * p.T + row) * D + d, acc[k]);
+  }
 }
 
 }  // namespace fkv

@@ -61,8 +61,7 @@ __global__ void __launch_bounds__(NT) tree_simt_kernel(const TreeParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_trigger();
   grid_dep_wait();
-  tree_zero_bad<E>(p, D);
-  const TreeCut cut = tree_cut(p, sq, KT, gridDim.x);
+  const TreeCut cut = tree_cut<E, D>(p, sq, KT, gridDim.x);
   if ((int)blockIdx.x >= cut.ranges) return;
   const int rt = blockIdx.y;
   const size_t plane = p.ring > 0 ? p.ring : p.S_max;
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(NT) tree_simt_kernel(const TreeParams p) {
         rec[RT * D + tid] = sM[tid];
         rec[RT * D + RT + tid] = sL[tid];
       }
-      tree_publish<E, D, RT>(p, cut, pre, pc.b, pc.h, s.N, tid, NT, flag, [] { __syncthreads(); });
+      tree_publish<E, D, RT, NT>(p, cut, pre, pc.b, pc.h, s.N, tid, flag, sM, [] { __syncthreads(); });
     }
   }
 }

@@ -18,11 +18,14 @@
 //
 // A CTA takes a contiguous range of key tiles of 128 rows (tree_common.cuh)
 // and one tile of NC query rows:
-//  * the producer warp loads K and V tiles by TMA (64-byte swizzle) into a
-//    ring of slots, in the order in which the MMAs read them:
+//  * the producer warp loads K and V tiles by TMA (boxes of 128-byte rows: with
+//    64-byte rows the copy engine itself held the kernel at 25 bytes a clock
+//    and SM, half of its share of HBM) into a ring of slots, in the order in which the MMAs read them:
 //    K_0, K_1, V_0, K_2, V_1, ...;
-//  * the MMA warp issues S_j = K_j Q^T one tile ahead (S has two buffers in
-//    tensor memory) and O += V_j^T P_j;
+//  * one warp issues S_j = K_j Q^T up to two tiles ahead (S has two buffers in
+//    tensor memory), another O += V_j^T P_j: an MMA of these sizes costs its
+//    issuing thread 46 clocks at 16 to 64 columns (64 at 128), as long as the
+//    tensor pipe, so one thread for both was the bound of small trees;
 //  * two softmax warpgroups take half of the columns each: scores from tensor
 //    memory, P to shared memory as an MN-major operand (a thread writes its
 //    key's columns, 16 bytes at a time, without bank conflicts).
@@ -41,28 +44,33 @@ namespace {
 
 constexpr int KT = 128;               // keys per tile
 constexpr int SM_THREADS = 256;       // softmax threads
-constexpr int THREADS = SM_THREADS + 64;
-constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
+constexpr int THREADS = SM_THREADS + 128;
+constexpr int PRODUCER_WARP = 8, QK_WARP = 9, PV_WARP = 10;
 constexpr int MAX_SLOTS = 12;
 constexpr int TAIL_ROWS = 16;         // rows of the boxes of a ragged tile
 constexpr int SMEM_LIMIT = 232448;
+constexpr int SWB = 128;              // bytes of a swizzled row: 64 channels or columns
+constexpr int SWC = SWB / 2;
+// registers: 168 a thread at launch (65536 / 384); the control warpgroup gives
+// up to 88 and the softmax takes 208: 256 * 208 + 128 * 88 = 384 * 168
+constexpr int REGS_CONTROL = 88, REGS_SOFTMAX = 208;
 constexpr float SLACK = 8.f;          // log2 growth of a score over its reference
 
 template <int D, int NSRC, int NC>
 struct TcCfg {
-  static constexpr int CB = (D + kSWE - 1) / kSWE;       // 32-channel blocks
-  static constexpr int SLOT = CB * KT * kSW;             // one K or V tile
-  static constexpr int Q_BYTES = NSRC * CB * NC * kSW;
-  static constexpr int P_BYTES = (NC + 31) / 32 * KT * kSW;
+  static constexpr int CB = (D + SWC - 1) / SWC;         // 64-channel blocks
+  static constexpr int SLOT = CB * KT * SWB;             // one K or V tile
+  static constexpr int Q_BYTES = NSRC * CB * NC * SWB;
+  static constexpr int P_BYTES = (NC + SWC - 1) / SWC * KT * SWB;
   static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
-  // V^T is read as 128 channels: the MMA reads up to 4 blocks from a slot on,
+  // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
   // past its end into what follows (rows that are not used)
-  static constexpr int OVERRUN = (4 - CB) * KT * kSW;
+  static constexpr int OVERRUN = (2 - CB) * KT * SWB;
   static constexpr int MISC = 2 * MAX_SLOTS * 8 + 16 * 8 + 64          // barriers, words
                               + NC * 4 * 8                             // reference, alpha, depth, node, sums
                               + kTreeMaxNodes * (16 + 4 + NW * 4)      // masks, depths, column masks
                               + 4 * NC * 4;                            // warp maxima / sums
-  static constexpr int FIXED = 512 + Q_BYTES + MISC;
+  static constexpr int FIXED = 1024 + Q_BYTES + MISC;
   static constexpr int TMEM_USED = (2 + NSRC) * NC;
   static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
@@ -99,22 +107,25 @@ __device__ __forceinline__ float reduce_scatter(float* v, int lane, Op op) {
 
 __device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__device__ __forceinline__ bool sm_any(bool x) {
+// Whether x holds in any thread of `count` threads that meet at barrier `id`.
+__device__ __forceinline__ bool any_of(int id, int count, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 2, 256, p;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(id), "r"(count)
       : "memory");
   return r != 0;
 }
 
-// Slot (counted from a piece's first) of the first source of K_i or V_i: the
-// order of a piece's n tiles is K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
-__device__ __forceinline__ int k_slot(int i) { return i == 0 ? 0 : 2 * i - 1; }
+// The 128 threads of softmax warpgroup wg.
+__device__ __forceinline__ void wg_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); }
+
+// Slot (counted from a piece's first, in tiles of one tensor) of the values of
+// tile i of a piece's n: the order is K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
 __device__ __forceinline__ int v_slot(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 + 2 * i; }
 
 template <int D, int NSRC, bool WGT, int NC>
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   using C = TcCfg<D, NSRC, NC>;
   constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~uintptr_t(511));
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sRing = smem;
   uint8_t* sQ = sRing + (size_t)nslots * C::SLOT;
   uint8_t* sP = sQ + C::Q_BYTES;
@@ -133,15 +144,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* s_full = q_ready + 1;   // [2]
   uint64_t* p_full = s_full + 2;    // [2]
   uint64_t* o_done = p_full + 2;    // [2]
-  uint64_t* drain = o_done + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = o_done + 2;     // [2] an issuer's last products, after an abort
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
   int* merge_flag = sm_issued + 1;
   int* sm_span = merge_flag + 1;                               // [2] least and largest depth
   unsigned long long* sMask =
       reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(sm_span + 2) + 15) & ~uintptr_t(15));
-  float* sRef = reinterpret_cast<float*>(sMask + 2 * kTreeMaxNodes);   // [NC] reference
+  float* sRef = reinterpret_cast<float*>(sMask + 2 * kTreeMaxNodes);   // [NC] negated reference
   float* sAlpha = sRef + NC;                                   // [NC] rescale, then 1 / sum
   int* sDepth = reinterpret_cast<int*>(sAlpha + NC);           // [NC] depth of the column's node
   int* sNode = sDepth + NC;                                    // [NC] node of the column, -1: none
@@ -163,22 +174,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&p_full[i], SM_THREADS);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     *sm_issued = 0;
     fence_mbar_init();
   }
-  if (warp == MMA_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  if (warp == QK_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
   for (int c = tid; c < NC; c += THREADS) {
     const int row = rt * NC + c;
     sNode[c] = row < p.G * p.T ? row % p.T : -1;
   }
+  if (warp == PRODUCER_WARP && lane < 8 && (lane & 1) < NSRC)
+    tma_prefetch(lane < 4 ? &maps.full[lane] : &maps.tail[lane - 4]);
   grid_dep_trigger();
   grid_dep_wait();
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
-  tree_zero_bad<__nv_bfloat16>(p, D);
   tc_fence_before();
-  const TreeCut cut = tree_cut(p, sq, KT, gridDim.x);   // ends with a __syncthreads
+  const TreeCut cut = tree_cut<__nv_bfloat16, D>(p, sq, KT, gridDim.x);   // ends with a __syncthreads
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool active = (int)blockIdx.x < cut.ranges;
@@ -194,118 +207,154 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
 
+  if (active && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
   if (active && warp == PRODUCER_WARP) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
-      int g = 0;   // slots filled
+      int g = 0, sl = 0;   // slots filled; the next one
+      uint32_t turn = 1;   // parity of its last release
       bool ok = true;
       TreePiece pc;
       while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
         const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
         const int unit = pc.b * p.H + pc.h, n = pc.k1 - pc.k0;
-        // first the keys of tile i, then the values of tile i - 1
-        for (int i = 0; ok && i <= n; ++i)
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            const int tile = kv == 0 ? i : i - 1;
-            if (tile < 0 || tile >= n) continue;
-            const TreeTile t = tree_tile(p, s, pc.k0 + tile, KT);
-            for (int src = 0; src < NSRC; ++src, ++g) {
-              const int sl = g % nslots, u = g / nslots;
-              if (u > 0 && !wait(&empty[sl], (uint32_t)(u - 1) & 1u)) {
-                ok = false;
-                break;
-              }
-              const int m = kv * 2 + src;
-              uint8_t* dst = slot_ptr(sl);
-              if (t.cnt == KT) {
-                mbar_arrive_expect_tx(&full[sl], C::SLOT);
+        auto load = [&](int kv, const TreeTile& t) {
+#pragma unroll
+          for (int src = 0; src < NSRC; ++src) {
+            if (g >= nslots && !wait(&empty[sl], turn)) return false;
+            const int m = kv * 2 + src;
+            uint8_t* dst = slot_ptr(sl);
+            if (t.cnt == KT) {
+              mbar_arrive_expect_tx(&full[sl], C::SLOT);
+#pragma unroll
+              for (int cb = 0; cb < CB; ++cb)
+                tma_load_3d(dst + cb * KT * SWB, &maps.full[m], cb * SWC, t.row, unit, &full[sl]);
+            } else {
+              const int boxes = (t.cnt + TAIL_ROWS - 1) / TAIL_ROWS;
+              mbar_arrive_expect_tx(&full[sl], boxes * CB * TAIL_ROWS * SWB);
+              for (int x = 0; x < boxes; ++x)
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb)
-                  tma_load_3d(dst + cb * KT * kSW, &maps.full[m], cb * kSWE, t.row, unit, &full[sl]);
-              } else {
-                const int boxes = (t.cnt + TAIL_ROWS - 1) / TAIL_ROWS;
-                mbar_arrive_expect_tx(&full[sl], boxes * CB * TAIL_ROWS * kSW);
-                for (int x = 0; x < boxes; ++x)
-#pragma unroll
-                  for (int cb = 0; cb < CB; ++cb)
-                    tma_load_3d(dst + cb * KT * kSW + x * TAIL_ROWS * kSW, &maps.tail[m], cb * kSWE,
-                                t.row + x * TAIL_ROWS, unit, &full[sl]);
-              }
+                  tma_load_3d(dst + cb * KT * SWB + x * TAIL_ROWS * SWB, &maps.tail[m], cb * SWC,
+                              t.row + x * TAIL_ROWS, unit, &full[sl]);
+            }
+            ++g;
+            if (++sl == nslots) {
+              sl = 0;
+              turn ^= 1;
             }
           }
+          return true;
+        };
+        // the keys of tile i + 1, then the values of tile i
+        TreeTile t = tree_tile(p, s, pc.k0, KT);
+        ok = load(0, t);
+        for (int i = 0; ok && i < n; ++i) {
+          TreeTile next = t;
+          if (i + 1 < n) {
+            next = tree_tile(p, s, pc.k0 + i + 1, KT);
+            ok = load(0, next);
+          }
+          ok = ok && load(1, t);
+          t = next;
+        }
       }
       *sm_issued = g;
     }
-  } else if (active && warp == MMA_WARP) {
-    // ---------------- MMA issuer ----------------
+  } else if (active && (warp == QK_WARP || warp == PV_WARP)) {
+    // ---------------- MMA issuers ----------------
     if (lane == 0) {
       constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
       constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
-      int base = 0;   // slots of the pieces before
-      int jt = 0;     // tiles of the pieces before
+      const bool qk = warp == QK_WARP;
+      // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
+      const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
+                             : sdesc128(smem_u32(sRing), KT * SWB, 8 * SWB);
+      const SDesc128 db = qk ? sdesc128(smem_u32(sQ), 16, 8 * SWB)
+                             : sdesc128(smem_u32(sP), KT * SWB, 8 * SWB);
+      int sl = 0;          // next slot
+      uint32_t turn = 0;   // parity of its filling
+      auto skip = [&](int n) {
+        sl += n;
+        if (sl >= nslots) {
+          sl -= nslots;
+          turn ^= 1;
+        }
+      };
+      int j = 0;   // tile of this CTA
       int piece = 0;
       bool ok = true;
       TreePiece pc;
       while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
-        const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
         const int n = pc.k1 - pc.k0;
-        auto full_wait = [&](int g) { return wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u); };
-        auto issue_qk = [&](int i) -> bool {
-          const int g0 = base + k_slot(i) * NSRC;
-          const uint32_t d = tmem + ((jt + i) & 1) * NC;
-          for (int src = 0; src < NSRC; ++src) {
-            if (!full_wait(g0 + src)) return false;
-            tc_fence_after();
-            const uint32_t kb = smem_u32(slot_ptr((g0 + src) % nslots));
-            const uint32_t qb = smem_u32(sQ + src * CB * NC * kSW);
+        if (qk) {
+          // S = K (q a)^T, both sources; its buffer is free once P of the
+          // tile two before is written
+          ok = wait(q_ready, (uint32_t)piece & 1u);
+          for (int i = 0; ok && i < n; ++i, ++j) {
+            const uint32_t d = tmem + (j & 1) * NC;
+            ok = j < 2 || wait(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (uint32_t)(k & 1) * 32;
-              mma_bf16(d, sdesc(kb + (k >> 1) * KT * kSW + off, 16, 8 * kSW),
-                       sdesc(qb + (k >> 1) * NC * kSW + off, 16, 8 * kSW), IDESC_QK, (src | k) ? 1u : 0u);
+            for (int src = 0; src < NSRC; ++src) {
+              if (!ok || !wait(&full[sl], turn)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint64_t ad = a.at((k >> 2) * KT * SWB + (k & 3) * 32);
+                const uint64_t bd = db.at((src * CB + (k >> 2)) * NC * SWB + (k & 3) * 32);
+                if (src == 0 && k == 0) mma_bf16_t<false>(d, ad, bd, IDESC_QK);
+                else mma_bf16_t<true>(d, ad, bd, IDESC_QK);
+              }
+              if (src == NSRC - 1) mma_commit(&s_full[j & 1]);
+              mma_commit(&empty[sl]);
+              skip(1);
             }
-            mma_commit(&empty[(g0 + src) % nslots]);
+            // the values of the tile before lie between K_i and K_i+1 (i > 0),
+            // those of the last two behind the piece's last keys
+            skip(i == n - 1 ? (n == 1 ? 1 : 2) * NSRC : i == 0 ? 0 : NSRC);
           }
-          mma_commit(&s_full[(jt + i) & 1]);
-          return true;
-        };
-        ok = wait(q_ready, (uint32_t)piece & 1u);
-        if (ok) tc_fence_after();
-        ok = ok && issue_qk(0);
-        for (int i = 0; ok && i < n; ++i) {
-          if (i + 1 < n && !issue_qk(i + 1)) {
-            ok = false;
-            break;
-          }
-          const int j = jt + i;
-          if (!wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          const int g0 = base + v_slot(i, n) * NSRC;
-          const int ks = (tree_tile(p, s, pc.k0 + i, KT).cnt + 15) / 16;
-          const uint32_t pb = smem_u32(sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0));
-          for (int src = 0; src < NSRC; ++src) {
-            if (!full_wait(g0 + src)) {
-              ok = false;
-              break;
+        } else {
+          const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
+          skip((n == 1 ? 1 : 2) * NSRC);   // V_0 follows K_0 and K_1
+          for (int i = 0; ok && i < n; ++i, ++j) {
+            const int ks = i + 1 == n || p.ring > 0 ? (tree_tile(p, s, pc.k0 + i, KT).cnt + 15) / 16
+                                                    : KT / 16;   // 16-key steps
+            ok = wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
+            const SDesc128 b{db.lo + (NPB == 2 && (j & 1) ? C::P_BYTES >> 4 : 0), db.hi};
+#pragma unroll
+            for (int src = 0; src < NSRC; ++src) {
+              if (!ok || !wait(&full[sl], turn)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
+              const uint32_t d = tmem + (2 + src) * NC;
+              mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i > 0 ? 1u : 0u);
+              if (ks == KT / 16) {
+#pragma unroll
+                for (int k = 1; k < KT / 16; ++k)
+                  mma_bf16_t<true>(d, a.at(k * 16 * SWB), b.at(k * 16 * SWB), IDESC_PV);
+              } else {
+                for (int k = 1; k < ks; ++k)
+                  mma_bf16_t<true>(d, a.at(k * 16 * SWB), b.at(k * 16 * SWB), IDESC_PV);
+              }
+              if (src == NSRC - 1) mma_commit(&o_done[j & 1]);
+              mma_commit(&empty[sl]);
+              skip(1);
             }
-            tc_fence_after();
-            const uint32_t vb = smem_u32(slot_ptr((g0 + src) % nslots));
-            const uint32_t d = tmem + (2 + src) * NC;
-            for (int k = 0; k < ks; ++k)
-              mma_bf16(d, sdesc(vb + k * 16 * kSW, KT * kSW, 8 * kSW),
-                       sdesc(pb + k * 16 * kSW, KT * kSW, 8 * kSW), IDESC_PV, (i | k) ? 1u : 0u);
-            mma_commit(&empty[(g0 + src) % nslots]);
+            if (i + 2 < n) skip(NSRC);   // the keys of the tile after next
           }
-          if (ok) mma_commit(&o_done[j & 1]);
         }
-        base += 2 * n * NSRC;
-        jt += n;
         ++piece;
       }
     }
   } else if (active && warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // ---------------- softmax ----------------
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
@@ -324,8 +373,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int rows = min(NC, p.G * p.T - rt * NC);
 
       // the piece's queries times the key weights, in the MMA's layout
-      for (int it = tid; it < NC * (CB * 4); it += SM_THREADS) {
-        const int r = it / (CB * 4), ch = it - r * (CB * 4);   // 16-byte chunk of a row
+      for (int it = tid; it < NC * (CB * 8); it += SM_THREADS) {
+        const int r = it / (CB * 8), ch = it - r * (CB * 8);   // 16-byte chunk of a row
         const int d = ch * 8;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (r < rows && d < D)
@@ -351,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               o = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
-          *reinterpret_cast<uint4*>(sQ + src * CB * NC * kSW + (ch >> 2) * NC * kSW + swz64(r, ch & 3)) = o;
+          *reinterpret_cast<uint4*>(sQ + src * CB * NC * SWB + (ch >> 3) * NC * SWB + swz128(r, ch & 7)) = o;
         }
       }
       // the nodes' masks and depths, then per drafted key the columns that see it
@@ -369,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         sm_span[0] = kTreeMaxNodes;
         sm_span[1] = 0;
       }
-      if (tid < NC) sRef[tid] = -FLT_MAX;
+      if (tid < NC) sRef[tid] = FLT_MAX;
       sm_sync();
       if (tid < NC) {
         const int i = sNode[tid];
@@ -380,17 +429,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           atomicMax(&sm_span[1], d);
         }
       }
-      for (int it = tid; it < N * NW; it += SM_THREADS) {
-        const int j = it / NW, w = it - j * NW;
-        uint32_t v = 0;
-#pragma unroll 4
-        for (int c = 0; c < 32 && w * 32 + c < NC; ++c) {
-          const int i = sNode[w * 32 + c];
-          if (i < 0 || i >= N) continue;
-          const bool in = p.window == 0 || sNodeDepth[j] > sNodeDepth[i] - p.window;
-          v |= (uint32_t)(in && (sMask[2 * i + (j >> 6)] >> (j & 63) & 1)) << c;
+      {
+        // a warp takes every (8 / NW)-th drafted key, its lanes 32 columns
+        const int w = warp % NW, c = w * 32 + lane;
+        const int node = c < NC ? sNode[c] : -1;
+        const bool live = node >= 0 && node < N;
+        const unsigned long long m0 = live ? sMask[2 * node] : 0ull, m1 = live ? sMask[2 * node + 1] : 0ull;
+        const int floor = live && p.window > 0 ? sNodeDepth[node] - p.window : -1;
+        for (int q = warp / NW; q < N; q += 8 / NW) {
+          const bool see = ((q < 64 ? m0 : m1) >> (q & 63) & 1) && sNodeDepth[q] > floor;
+          const uint32_t v = __ballot_sync(0xffffffffu, see);
+          if (lane == 0) sVis[q * NW + w] = v;
         }
-        sVis[j * NW + w] = v;
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -402,25 +452,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int c = 0; c < HC; ++c) l[c] = 0.f;
 
+      // A wait that runs out clears ok: the warp then goes through the piece's
+      // remaining tiles without waiting, so that every barrier below keeps its
+      // threads, and all leave together at the piece's end.
       for (int i = 0; i < n; ++i) {
         const int j = jt + i;
         const TreeTile t = tree_tile(p, s, pc.k0 + i, KT);
         if (ok && !__all_sync(0xffffffffu, wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u))) ok = false;
         tc_fence_after();
-        float sv[HC];
         const uint32_t ts = t_lane + (j & 1) * NC;
-        if constexpr (HC == 8) {
-          tmem_ld8(ts, sv);
-        } else if constexpr (HC == 16) {
-          tmem_ld16(ts, sv);
-        } else {
-#pragma unroll
-          for (int c = 0; c < HC; c += 32) tmem_ld32(ts + c, sv + c);
-        }
-        tmem_wait_ld();
-
         const bool edge = p.window > 0 && t.pos <= P + most - p.window;
-        if (t.cnt < KT || t.pos + t.cnt > P || edge) {   // uniform over the CTA
+        const bool masked = t.cnt < KT || t.pos + t.cnt > P || edge;   // uniform over the CTA
+        const int q = t.pos + key - P;   // >= 0: drafted node q
+        bool poison = false;
+        if (masked) {
           // wait for the tile's values: unseen rows are zeroed, rows that are
           // not finite are noted
           // (once the products of the tile before are done, the slots' phases
@@ -435,8 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (ok && !__all_sync(0xffffffffu, wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u)))
               ok = false;
           }
-          const int q = t.pos + key - P;   // >= 0: drafted node q
-          bool seen = false, poison = false;
+          bool seen = false;
           if (key < t.cnt) {
             if (q < 0) {
               seen = p.window == 0 || least < q + p.window;
@@ -450,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint8_t* v = slot_ptr((g0 + src) % nslots);
 #pragma unroll 1
                 for (int ch = 0; ch < D / 8; ++ch) {
-                  const uint4 x = *reinterpret_cast<const uint4*>(v + (ch >> 2) * KT * kSW + swz64(key, ch & 3));
+                  const uint4 x = *reinterpret_cast<const uint4*>(v + (ch >> 3) * KT * SWB + swz128(key, ch & 7));
                   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
@@ -465,38 +509,58 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int src = 0; src < NSRC; ++src) {
               uint8_t* v = slot_ptr((g0 + src) % nslots);
 #pragma unroll 1
-              for (int ch = 0; ch < CB * 4; ++ch)
-                *reinterpret_cast<uint4*>(v + (ch >> 2) * KT * kSW + swz64(key, ch & 3)) = make_uint4(0, 0, 0, 0);
+              for (int ch = 0; ch < CB * 8; ++ch)
+                *reinterpret_cast<uint4*>(v + (ch >> 3) * KT * SWB + swz128(key, ch & 7)) = make_uint4(0, 0, 0, 0);
             }
           }
-          uint32_t vis[NW];
-#pragma unroll
-          for (int w = 0; w < NW; ++w) vis[w] = key >= t.cnt ? 0u : q >= 0 ? sVis[q * NW + w] : ~0u;
-          const int reach = q < 0 && p.window > 0 ? q + p.window : kTreeMaxNodes;   // depths below it see the key
-#pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            const int cc = c0 + c;
-            const bool see = (vis[cc >> 5] >> (cc & 31) & 1u) && sDepth[cc] < reach;
-            sv[c] = !see ? -INFINITY : poison ? NAN : sv[c];
-          }
         }
-
-        // does a score exceed its reference by more than the slack?
-        float over = -INFINITY;
+        // this key's scores, -inf where a column does not see it
+        float sv[HC];
+        auto scores = [&]() {
+          if constexpr (HC == 8) {
+            tmem_ld8(ts, sv);
+          } else if constexpr (HC == 16) {
+            tmem_ld16(ts, sv);
+          } else {
 #pragma unroll
-        for (int c = 0; c < HC; c += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(sRef + c0 + c);
-          over = fmaxf(over, fmaf(sv[c], p.scale_log2, -r.x));
-          over = fmaxf(over, fmaf(sv[c + 1], p.scale_log2, -r.y));
-          over = fmaxf(over, fmaf(sv[c + 2], p.scale_log2, -r.z));
-          over = fmaxf(over, fmaf(sv[c + 3], p.scale_log2, -r.w));
-        }
-        if (sm_any(over > SLACK || !ok)) {
-          if (sm_any(!ok)) {
-            ok = false;
-            break;
+            for (int c = 0; c < HC; c += 32) tmem_ld32(ts + c, sv + c);
           }
-          // new references: the columns' maxima so far
+          tmem_wait_ld();
+          if (masked) {
+            uint32_t vis[(HC + 31) / 32];
+#pragma unroll
+            for (int w = 0; w < (HC + 31) / 32; ++w)
+              vis[w] = (key >= t.cnt ? 0u : q >= 0 ? sVis[q * NW + c0 / 32 + w] : ~0u) >> (c0 & 31);
+            const int reach = q < 0 && p.window > 0 ? q + p.window : kTreeMaxNodes;   // depths below it see the key
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+              const bool see = (vis[c >> 5] >> (c & 31) & 1u) && sDepth[c0 + c] < reach;
+              sv[c] = !see ? -INFINITY : poison ? NAN : sv[c];
+            }
+          }
+        };
+        // x = score * scale - reference, and the largest of them
+        auto shift = [&]() {
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < HC; c += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(sRef + c0 + c);   // negated references
+            float x0 = r.x, x1 = r.y, x2 = r.z, x3 = r.w;
+            fma2(x0, x1, sv[c], sv[c + 1], p.scale_log2, p.scale_log2);
+            fma2(x2, x3, sv[c + 2], sv[c + 3], p.scale_log2, p.scale_log2);
+            sv[c] = x0; sv[c + 1] = x1; sv[c + 2] = x2; sv[c + 3] = x3;
+            top[0] = fmax3f(top[0], x0, x1);
+            top[1] = fmax3f(top[1], x2, x3);
+          }
+          return fmaxf(top[0], top[1]);
+        };
+        scores();
+        // the first tile of a piece takes its maxima as references; later ones
+        // keep the references unless a score exceeds its own by more than the slack
+        bool grow = i == 0;
+        if (!grow) grow = any_of(2 + wg, 128, shift() > SLACK);
+        if (grow) {
+          if (i > 0) scores();
           constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
           for (int b0 = 0; b0 < HC; b0 += RN) {
@@ -506,27 +570,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float m = reduce_scatter<RN>(v, lane, fmaxop);
             if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
           }
-          sm_sync();
-          if (tid < NC) {
-            const float m = fmaxf(fmaxf(sWarp[tid], sWarp[NC + tid]), fmaxf(sWarp[2 * NC + tid], sWarp[3 * NC + tid]));
-            const float old = sRef[tid], top = fmaxf(old, m * p.scale_log2);
-            sAlpha[tid] = fast_exp2(old - top);
-            sRef[tid] = top;
+          wg_sync(wg);
+          if ((tid & 127) < HC) {
+            const int c = c0 + (tid & 127);
+            const float m = fmaxf(fmaxf(sWarp[c], sWarp[NC + c]), fmaxf(sWarp[2 * NC + c], sWarp[3 * NC + c]));
+            const float old = -sRef[c], ref = fmaxf(old, m * p.scale_log2);
+            sAlpha[c] = fast_exp2(old - ref);
+            sRef[c] = -ref;
           }
           // O holds every product before this tile once the last one is done
-          if (i > 0 && !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
+          if (i > 0 && ok &&
+              !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
             ok = false;
           tc_fence_after();
-          sm_sync();
+          wg_sync(wg);
+          if (i > 0) {
 #pragma unroll
-          for (int c = 0; c < HC; c += 8) {
-            float al[8];
+            for (int c = 0; c < HC; c += 8) {
+              float al[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              al[e] = sAlpha[c0 + c + e];
-              l[c + e] *= al[e];
-            }
-            if (i > 0) {
+              for (int e = 0; e < 8; ++e) {
+                al[e] = sAlpha[c0 + c + e];
+                l[c + e] *= al[e];
+              }
 #pragma unroll
               for (int src = 0; src < NSRC; ++src) {
                 const uint32_t to = t_lane + (2 + src) * NC + c;
@@ -538,31 +604,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st8(to, o);
               }
             }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+          shift();
         }
 
-        // P of this key: exp2(s * scale - reference), bf16
+        // P of this key: 2^x, bf16
         const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
         if (pj >= 0 && ok && !__all_sync(0xffffffffu, wait(&o_done[pj & 1], (uint32_t)(pj >> 1) & 1u)))
           ok = false;
         uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
-          float ref[8];
-          *reinterpret_cast<float4*>(ref) = *reinterpret_cast<const float4*>(sRef + c0 + c);
-          *reinterpret_cast<float4*>(ref + 4) = *reinterpret_cast<const float4*>(sRef + c0 + c + 4);
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float e0 = fast_exp2(fmaf(sv[c + e], p.scale_log2, -ref[e]));
-            const float e1 = fast_exp2(fmaf(sv[c + e + 1], p.scale_log2, -ref[e + 1]));
+            const float e0 = fast_exp2(sv[c + e]);
+            const float e1 = fast_exp2(sv[c + e + 1]);
             add2(l[c + e], l[c + e + 1], e0, e1);
             const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
             w[e / 2] = *reinterpret_cast<const uint32_t*>(&v2);
           }
           const int cc = c0 + c;
-          *reinterpret_cast<uint4*>(pb + (cc >> 5) * KT * kSW + swz64(key, (cc & 31) >> 3)) =
+          *reinterpret_cast<uint4*>(pb + (cc >> 6) * KT * SWB + swz128(key, (cc & 63) >> 3)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
@@ -572,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the sums of the columns over all keys, and the last products
       const int jl = jt + n - 1;
       if (ok && !__all_sync(0xffffffffu, wait(&o_done[jl & 1], (uint32_t)(jl >> 1) & 1u))) ok = false;
-      if (sm_any(!ok)) break;
+      if (any_of(1, SM_THREADS, !ok)) break;
       tc_fence_after();
       constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
@@ -588,7 +652,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float sum = (sWarp[tid] + sWarp[NC + tid]) + (sWarp[2 * NC + tid] + sWarp[3 * NC + tid]);
         sAlpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
         if (!whole) {
-          rec[NC * D + tid] = sRef[tid];
+          rec[NC * D + tid] = -sRef[tid];
           rec[NC * D + NC + tid] = sum;
         }
       }
@@ -624,7 +688,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!whole)
-        tree_publish<__nv_bfloat16, D, NC>(p, cut, sq.pre, pc.b, pc.h, N, tid, SM_THREADS, merge_flag, sm_sync);
+        tree_publish<__nv_bfloat16, D, NC, SM_THREADS>(p, cut, sq.pre, pc.b, pc.h, N, tid, merge_flag, sWarp,
+                                                       sm_sync);
       sm_sync();   // shared words are free for the next piece
       base += 2 * n * NSRC;
       jt += n;
@@ -641,15 +706,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int g = max(0, issued - nslots); g < issued; ++g)
         (void)mbar_wait_bounded(&full[g % nslots], (uint32_t)(g / nslots) & 1u, kDrainLimitNs);
     }
-    if (warp == MMA_WARP && lane == 0) {
-      mma_commit(drain);
-      (void)mbar_wait_bounded(drain, 0, kDrainLimitNs);
+    if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
+      mma_commit(&drain[warp - QK_WARP]);
+      (void)mbar_wait_bounded(&drain[warp - QK_WARP], 0, kDrainLimitNs);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
   }
-  if (warp == MMA_WARP) {
+  if (warp == QK_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -678,13 +743,21 @@ cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& pl
   for (int i = 0; i < 4; ++i) {
     if ((i & 1) >= NSRC) continue;
     const void* ptr = i < 2 ? a.k[i & 1] : a.v[i & 1];
-    ok = ok && make_map(&maps.full[i], ptr, D, rows, units, (size_t)rows * D * 2, KT);
-    ok = ok && make_map(&maps.tail[i], ptr, D, rows, units, (size_t)rows * D * 2, TAIL_ROWS);
+    ok = ok && make_map_box(&maps.full[i], ptr, D, rows, units, (size_t)rows * D * 2, SWC, KT,
+                            CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && make_map_box(&maps.tail[i], ptr, D, rows, units, (size_t)rows * D * 2, SWC, TAIL_ROWS,
+                            CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
   auto kern = tree_tc_kernel<D, NSRC, WGT, NC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_bytes);
   if (e != cudaSuccess) return e;
+  // the softmax warpgroups' larger share has to fit the launch allocation, or
+  // it would never be granted: refuse instead
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * THREADS < SM_THREADS * REGS_SOFTMAX + 128 * REGS_CONTROL) return cudaErrorNotSupported;
   return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(THREADS), plan.smem_bytes, stream, maps, p,
                     plan.slots);
 }
