@@ -153,6 +153,7 @@ struct TreeArgs {
 struct TreePlan {
   bool tensor;      // the tensor-core kernel (tree_tc.cu), else tree_simt.cu
   int slots;        // its key / value tile slots
+  int raw_slots;    // its slots of 4-bit records
   int ranges;       // key ranges (grid.x)
   int rows;         // query rows per CTA
   int row_tiles;    // grid.y

@@ -1,4 +1,4 @@
-// fkv_tree_attn on the tcgen05 tensor cores (bf16 caches).
+// fkv_tree_attn on the tcgen05 tensor cores (bf16 and 4-bit caches).
 //
 // A drafted tree gives a (sequence, KV head) unit G * T query rows, few
 // against the cached keys, so the call is bound by reading the cache once.
@@ -29,6 +29,15 @@
 //  * two softmax warpgroups take half of the columns each: scores from tensor
 //    memory, P to shared memory as an MN-major operand (a thread writes its
 //    key's columns, 16 bytes at a time, without bank conflicts).
+// 4-bit caches: the producer copies a tile's records (one contiguous run) to a
+// second ring, and two more warpgroups dequantise them into the slots, two
+// values an instruction: a nibble pair under the exponent of 128 is 128 + code
+// in bf16, exactly; less 128, times the scale, plus the minimum in one FMA is
+// the record's value rounded once to bf16 (2^-9 of it, the library's choice
+// for the tensor cores; decode keeps fp32).  The pairs that fall out of a word
+// are channels e and e + 4 of eight, so the tiles hold the channels in the
+// order 0 4 1 5 2 6 3 7 and so do the queries; the epilogue undoes it.
+//
 // Tiles with drafted rows, a window's edge or a ragged end are masked, and the
 // value rows that nobody sees are zeroed in shared memory, since 0 * NaN is
 // no 0.  A drafted value row that is not finite is zeroed too and its score
@@ -44,19 +53,17 @@ namespace {
 
 constexpr int KT = 128;               // keys per tile
 constexpr int SM_THREADS = 256;       // softmax threads
-constexpr int THREADS = SM_THREADS + 128;
+constexpr int DQ_THREADS = 256;       // dequantising threads (4-bit caches)
+constexpr int MAX_RAW = 12;           // slots of records
 constexpr int PRODUCER_WARP = 8, QK_WARP = 9, PV_WARP = 10;
 constexpr int MAX_SLOTS = 12;
 constexpr int TAIL_ROWS = 16;         // rows of the boxes of a ragged tile
 constexpr int SMEM_LIMIT = 232448;
 constexpr int SWB = 128;              // bytes of a swizzled row: 64 channels or columns
 constexpr int SWC = SWB / 2;
-// registers: 168 a thread at launch (65536 / 384); the control warpgroup gives
-// up to 88 and the softmax takes 208: 256 * 208 + 128 * 88 = 384 * 168
-constexpr int REGS_CONTROL = 88, REGS_SOFTMAX = 208;
 constexpr float SLACK = 8.f;          // log2 growth of a score over its reference
 
-template <int D, int NSRC, int NC>
+template <int D, int NSRC, int NC, bool Q4>
 struct TcCfg {
   static constexpr int CB = (D + SWC - 1) / SWC;         // 64-channel blocks
   static constexpr int SLOT = CB * KT * SWB;             // one K or V tile
@@ -66,7 +73,7 @@ struct TcCfg {
   // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
   // past its end into what follows (rows that are not used)
   static constexpr int OVERRUN = (2 - CB) * KT * SWB;
-  static constexpr int MISC = 2 * MAX_SLOTS * 8 + 16 * 8 + 64          // barriers, words
+  static constexpr int MISC = (2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 16 * 8 + 64   // barriers, words
                               + NC * 4 * 8                             // reference, alpha, depth, node, sums
                               + kTreeMaxNodes * (16 + 4 + NW * 4)      // masks, depths, column masks
                               + 4 * NC * 4;                            // warp maxima / sums
@@ -78,6 +85,14 @@ struct TcCfg {
   // two P buffers where at least five tile slots remain beside them
   static constexpr int NPB = (SMEM_LIMIT - FIXED - 2 * P_BYTES - 12 * 64) / SLOT >= 5 ? 2 : 1;
   static constexpr int HC = NC / 2;                      // columns of a softmax warpgroup
+  static constexpr int RAW = KT * q4_row_bytes(D);       // records of a tile
+  static constexpr int THREADS = SM_THREADS + 128 + (Q4 ? DQ_THREADS : 0);
+  // registers a thread: 168 at launch with 384 threads, 96 with 640; the
+  // control (and dequantising) warpgroups give some up for the softmax:
+  // 256 * 208 + 128 * 88 = 384 * 168, 256 * 128 + 128 * 64 + 256 * 80 = 640 * 96
+  static constexpr int REGS_CONTROL = Q4 ? 64 : 88, REGS_SOFTMAX = Q4 ? 128 : 208, REGS_DQ = 80;
+  static constexpr int REGS_SPLIT =
+      SM_THREADS * REGS_SOFTMAX + 128 * REGS_CONTROL + (Q4 ? DQ_THREADS * REGS_DQ : 0);
 };
 
 struct TcMaps {
@@ -128,19 +143,23 @@ __device__ __forceinline__ void wg_sync(int wg) { asm volatile("bar.sync %0, 128
 // tile i of a piece's n: the order is K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
 __device__ __forceinline__ int v_slot(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 + 2 * i; }
 
-template <int D, int NSRC, bool WGT, int NC>
-__global__ void __launch_bounds__(THREADS, 1)
-    tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots) {
-  using C = TcCfg<D, NSRC, NC>;
+template <int D, int NSRC, bool WGT, int NC, bool Q4>
+__global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
+    tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots,
+                   const int nraw) {
+  using C = TcCfg<D, NSRC, NC, Q4>;
   constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sRing = smem;
   uint8_t* sQ = sRing + (size_t)nslots * C::SLOT;
   uint8_t* sP = sQ + C::Q_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sP + NPB * C::P_BYTES);
+  uint8_t* sRaw = sP + NPB * C::P_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + (Q4 ? (size_t)nraw * C::RAW : 0));
   uint64_t* empty = full + MAX_SLOTS;
-  uint64_t* q_ready = empty + MAX_SLOTS;
+  uint64_t* raw_full = empty + MAX_SLOTS;
+  uint64_t* raw_empty = raw_full + MAX_RAW;
+  uint64_t* q_ready = raw_empty + MAX_RAW;
   uint64_t* s_full = q_ready + 1;   // [2]
   uint64_t* p_full = s_full + 2;    // [2]
   uint64_t* o_done = p_full + 2;    // [2]
@@ -165,8 +184,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int rt = blockIdx.y;
   if (tid == 0) {
     for (int s = 0; s < nslots; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], Q4 ? DQ_THREADS / 32 : 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; Q4 && s < nraw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], DQ_THREADS / 32);
     }
     mbar_init(q_ready, SM_THREADS);
     for (int i = 0; i < 2; ++i) {
@@ -181,11 +204,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
   }
   if (warp == QK_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
-  for (int c = tid; c < NC; c += THREADS) {
+  for (int c = tid; c < NC; c += C::THREADS) {
     const int row = rt * NC + c;
     sNode[c] = row < p.G * p.T ? row % p.T : -1;
   }
-  if (warp == PRODUCER_WARP && lane < 8 && (lane & 1) < NSRC)
+  if (!Q4 && warp == PRODUCER_WARP && lane < 8 && (lane & 1) < NSRC)
     tma_prefetch(lane < 4 ? &maps.full[lane] : &maps.tail[lane - 4]);
   grid_dep_trigger();
   grid_dep_wait();
@@ -207,10 +230,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
 
-  if (active && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
+  if (active && warp >= 8 && warp < 12)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
   if (active && warp == PRODUCER_WARP) {
-    // ---------------- TMA producer ----------------
+    // ---------------- producer ----------------
     if (lane == 0) {
+      const int nring = Q4 ? nraw : nslots;
+      uint64_t* ring_empty = Q4 ? raw_empty : empty;
+      const size_t plane = p.ring > 0 ? p.ring : p.S_max;
       int g = 0, sl = 0;   // slots filled; the next one
       uint32_t turn = 1;   // parity of its last release
       bool ok = true;
@@ -221,25 +248,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto load = [&](int kv, const TreeTile& t) {
 #pragma unroll
           for (int src = 0; src < NSRC; ++src) {
-            if (g >= nslots && !wait(&empty[sl], turn)) return false;
-            const int m = kv * 2 + src;
-            uint8_t* dst = slot_ptr(sl);
-            if (t.cnt == KT) {
-              mbar_arrive_expect_tx(&full[sl], C::SLOT);
-#pragma unroll
-              for (int cb = 0; cb < CB; ++cb)
-                tma_load_3d(dst + cb * KT * SWB, &maps.full[m], cb * SWC, t.row, unit, &full[sl]);
+            if (g >= nring && !wait(&ring_empty[sl], turn)) return false;
+            if constexpr (Q4) {
+              const uint8_t* rec = static_cast<const uint8_t*>(kv ? p.v[src] : p.k[src]);
+              const uint32_t bytes = t.cnt * q4_row_bytes(D);
+              fence_proxy_async_smem();
+              mbar_arrive_expect_tx(&raw_full[sl], bytes);
+              bulk_g2s(sRaw + (size_t)sl * C::RAW, rec + (unit * plane + t.row) * q4_row_bytes(D), bytes,
+                       &raw_full[sl], l2_policy_evict_first());
             } else {
-              const int boxes = (t.cnt + TAIL_ROWS - 1) / TAIL_ROWS;
-              mbar_arrive_expect_tx(&full[sl], boxes * CB * TAIL_ROWS * SWB);
-              for (int x = 0; x < boxes; ++x)
+              const int m = kv * 2 + src;
+              uint8_t* dst = slot_ptr(sl);
+              if (t.cnt == KT) {
+                mbar_arrive_expect_tx(&full[sl], C::SLOT);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb)
-                  tma_load_3d(dst + cb * KT * SWB + x * TAIL_ROWS * SWB, &maps.tail[m], cb * SWC,
-                              t.row + x * TAIL_ROWS, unit, &full[sl]);
+                  tma_load_3d(dst + cb * KT * SWB, &maps.full[m], cb * SWC, t.row, unit, &full[sl]);
+              } else {
+                const int boxes = (t.cnt + TAIL_ROWS - 1) / TAIL_ROWS;
+                mbar_arrive_expect_tx(&full[sl], boxes * CB * TAIL_ROWS * SWB);
+                for (int x = 0; x < boxes; ++x)
+#pragma unroll
+                  for (int cb = 0; cb < CB; ++cb)
+                    tma_load_3d(dst + cb * KT * SWB + x * TAIL_ROWS * SWB, &maps.tail[m], cb * SWC,
+                                t.row + x * TAIL_ROWS, unit, &full[sl]);
+              }
             }
             ++g;
-            if (++sl == nslots) {
+            if (++sl == nring) {
               sl = 0;
               turn ^= 1;
             }
@@ -260,6 +296,62 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       *sm_issued = g;
+    }
+  } else if (Q4 && active && warp >= 12) {
+    // ---------------- dequantisation ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_DQ));
+    if constexpr (Q4) {
+      constexpr int GR = D / kQ4Group, RB = q4_row_bytes(D);
+      const int t = tid - 12 * 32;
+      const __nv_bfloat162 bias = __floats2bfloat162_rn(-128.f, -128.f);
+      const long long total = (walk.t1 - walk.t) * 2 * NSRC;
+      int sl = 0, r = 0;
+      uint32_t turn = 1, rturn = 0;   // parities of the slot's last release and of the records' filling
+      for (long long g = 0; g < total; ++g) {
+        if (!__all_sync(0xffffffffu, wait(&raw_full[r], rturn) && (g < nslots || wait(&empty[sl], turn)))) break;
+        const uint8_t* rec = sRaw + (size_t)r * C::RAW;
+        uint8_t* dst = slot_ptr(sl);
+#pragma unroll
+        for (int k = 0; k < (KT * GR + DQ_THREADS - 1) / DQ_THREADS; ++k) {
+          const int it = t + k * DQ_THREADS;
+          if (KT * GR % DQ_THREADS != 0 && it >= KT * GR) break;
+          const int row = it / GR, gr = it - row * GR;
+          const uint2 codes = *reinterpret_cast<const uint2*>(rec + row * RB + gr * 8);
+          const uint32_t prm = *reinterpret_cast<const uint32_t*>(rec + row * RB + D / 2 + gr * 4);
+          const uint32_t s2 = __byte_perm(prm, 0, 0x1010), m2 = __byte_perm(prm, 0, 0x3232);
+          const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+          const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&m2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? codes.y : codes.x;
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+              const __nv_bfloat162 v =
+                  __hfma2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), bias), sc, lo);
+              o[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            const int ch = gr * 2 + h;
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * KT * SWB + swz128(row, ch & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[sl]);
+          mbar_arrive(&raw_empty[r]);
+        }
+        if (++sl == nslots) {
+          sl = 0;
+          turn ^= 1;
+        }
+        if (++r == nraw) {
+          r = 0;
+          rturn ^= 1;
+        }
+      }
     }
   } else if (active && (warp == QK_WARP || warp == PV_WARP)) {
     // ---------------- MMA issuers ----------------
@@ -354,11 +446,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (active && warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ---------------- softmax ----------------
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
     const int c0 = wg * HC;                // first column
+    const int chan = Q4 ? (key & ~7) | (key & 1) << 2 | (key >> 1 & 3) : key;   // channel of row `key` of V^T
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
     auto fmaxop = [](float a, float b) { return fmaxf(a, b); };
     auto addop = [](float a, float b) { return a + b; };
@@ -382,6 +475,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                                               (unit * p.G * p.T + rt * NC + r) * D + d);
         float f[8];
         unpack16<__nv_bfloat16>(w, f);
+        if constexpr (Q4)   // the order of the tiles' channels: 0 4 1 5 2 6 3 7
+          w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
+                         __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
 #pragma unroll
         for (int src = 0; src < NSRC; ++src) {
           uint4 o = w;
@@ -393,8 +489,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v2 =
-                    __floats2bfloat162_rn(f[2 * e] * av[2 * e], f[2 * e + 1] * av[2 * e + 1]);
+                const int e0 = Q4 ? e : 2 * e, e1 = Q4 ? e + 4 : 2 * e + 1;
+                const __nv_bfloat162 v2 = __floats2bfloat162_rn(f[e0] * av[e0], f[e1] * av[e1]);
                 x[e] = *reinterpret_cast<const uint32_t*>(&v2);
               }
               o = make_uint4(x[0], x[1], x[2], x[3]);
@@ -659,8 +755,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       sm_sync();
       float b0w = 1.f, b1w = 0.f;
       if (WGT && key < D) {
-        b0w = p.b[0][(size_t)pc.h * D + key];
-        if constexpr (NSRC == 2) b1w = p.b[1][(size_t)pc.h * D + key];
+        b0w = p.b[0][(size_t)pc.h * D + chan];
+        if constexpr (NSRC == 2) b1w = p.b[1][(size_t)pc.h * D + chan];
       }
 #pragma unroll 1
       for (int c = 0; c < HC; c += 8) {
@@ -679,10 +775,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               const int node = sNode[cc];
               const float inv = sAlpha[cc];
               if (node >= 0 && node < N)
-                static_cast<__nv_bfloat16*>(p.out)[(unit * p.G * p.T + rt * NC + cc) * D + key] =
+                static_cast<__nv_bfloat16*>(p.out)[(unit * p.G * p.T + rt * NC + cc) * D + chan] =
                     __float2bfloat16_rn(inv == 0.f ? 0.f : x * inv);
             } else {
-              rec[(size_t)cc * D + key] = x;
+              rec[(size_t)cc * D + chan] = x;
             }
           }
         }
@@ -702,9 +798,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (*abort_flag) {
     // no role may have awaited the last copies and products: let them finish
     if (warp == PRODUCER_WARP && lane == 0) {
-      const int issued = *sm_issued;
-      for (int g = max(0, issued - nslots); g < issued; ++g)
-        (void)mbar_wait_bounded(&full[g % nslots], (uint32_t)(g / nslots) & 1u, kDrainLimitNs);
+      const int issued = *sm_issued, nring = Q4 ? nraw : nslots;
+      uint64_t* ring_full = Q4 ? raw_full : full;
+      for (int g = max(0, issued - nring); g < issued; ++g)
+        (void)mbar_wait_bounded(&ring_full[g % nring], (uint32_t)(g / nring) & 1u, kDrainLimitNs);
     }
     if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
       mma_commit(&drain[warp - QK_WARP]);
@@ -720,27 +817,38 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Tile slots and shared memory of a configuration, or 0 slots if it does not fit.
-template <int D, int NSRC, int NC>
+// Tile slots and shared memory of a configuration; 0 slots if it does not fit.
+template <int D, int NSRC, int NC, bool Q4>
 void size_tc(int B, TreePlan* plan) {
-  using C = TcCfg<D, NSRC, NC>;
-  const size_t fixed = C::FIXED + C::NPB * C::P_BYTES + tree_seqs_bytes(B) + 64;
-  int slots = fixed < SMEM_LIMIT ? (int)((SMEM_LIMIT - fixed) / C::SLOT) : 0;
+  using C = TcCfg<D, NSRC, NC, Q4>;
+  const int fixed = (int)(C::FIXED + C::NPB * C::P_BYTES + tree_seqs_bytes(B) + 64);
+  int left = SMEM_LIMIT - fixed;
+  plan->raw_slots = 0;
+  if (Q4) {
+    // records for at least two tiles, the rest beside as many tile slots as
+    // the MMAs need (and two tiles more where they are small)
+    const int want = C::SLOT <= 16384 ? 4 * NSRC : 2 * NSRC;
+    int raw = (left - want * C::SLOT) / C::RAW;
+    raw = raw > MAX_RAW ? MAX_RAW : raw < 2 * NSRC ? 2 * NSRC : raw;
+    plan->raw_slots = raw;
+    left -= raw * C::RAW;
+  }
+  int slots = left > 0 ? left / C::SLOT : 0;
   if (slots > MAX_SLOTS) slots = MAX_SLOTS;
-  // the blocks past the last slot's end lie in Q and P
+  // the block past the last slot's end lies in Q and P
   if (slots < 2 * NSRC || C::OVERRUN > C::Q_BYTES + C::NPB * C::P_BYTES) slots = 0;
   plan->slots = slots;
-  plan->smem_bytes = fixed + (size_t)slots * C::SLOT;
+  plan->smem_bytes = (size_t)fixed + (size_t)slots * C::SLOT + (size_t)plan->raw_slots * C::RAW;
 }
 
-template <int D, int NSRC, bool WGT, int NC>
+template <int D, int NSRC, bool WGT, int NC, bool Q4>
 cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
   TcMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   const int rows = a.ring > 0 ? a.ring : a.max_seq;
   const long long units = (long long)a.batch * a.kv_heads;
   bool ok = true;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4 && !Q4; ++i) {
     if ((i & 1) >= NSRC) continue;
     const void* ptr = i < 2 ? a.k[i & 1] : a.v[i & 1];
     ok = ok && make_map_box(&maps.full[i], ptr, D, rows, units, (size_t)rows * D * 2, SWC, KT,
@@ -749,7 +857,8 @@ cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& pl
                             CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  auto kern = tree_tc_kernel<D, NSRC, WGT, NC>;
+  using C = TcCfg<D, NSRC, NC, Q4>;
+  auto kern = tree_tc_kernel<D, NSRC, WGT, NC, Q4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_bytes);
   if (e != cudaSuccess) return e;
   // the softmax warpgroups' larger share has to fit the launch allocation, or
@@ -757,20 +866,30 @@ cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& pl
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * THREADS < SM_THREADS * REGS_SOFTMAX + 128 * REGS_CONTROL) return cudaErrorNotSupported;
-  return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(THREADS), plan.smem_bytes, stream, maps, p,
-                    plan.slots);
+  if (fa.numRegs * C::THREADS < C::REGS_SPLIT) return cudaErrorNotSupported;
+  return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(C::THREADS), plan.smem_bytes, stream, maps,
+                    p, plan.slots, plan.raw_slots);
 }
 
-// Call f.template operator()<D, NSRC, NC>() for the plan's configuration.
+// Call f with the plan's configuration as integral constants: head dim,
+// sources, columns and whether the caches are 4-bit.
 template <typename F>
-auto dispatch_tc(int D, int nsrc, int rows, F f) {
+auto dispatch_tc(int D, int nsrc, int rows, bool q4, F f) {
+  auto fmt = [&](auto d, auto ns, auto nc) {
+    // 4-bit caches take at most 64 columns: 128 registers a softmax thread
+    if constexpr (decltype(nc)::value <= 64) {
+      if (q4) return f(d, ns, nc, std::true_type());
+    }
+    return f(d, ns, nc, std::false_type());
+  };
   auto cols = [&](auto d, auto ns) {
+    // fused rows of 128 channels leave too little room for tiles beside 128 columns
+    constexpr bool wide = !(decltype(d)::value == 128 && decltype(ns)::value == 2);
     switch (rows) {
-      case 16: return f(d, ns, std::integral_constant<int, 16>());
-      case 32: return f(d, ns, std::integral_constant<int, 32>());
-      case 64: return f(d, ns, std::integral_constant<int, 64>());
-      default: return f(d, ns, std::integral_constant<int, 128>());
+      case 16: return fmt(d, ns, std::integral_constant<int, 16>());
+      case 32: return fmt(d, ns, std::integral_constant<int, 32>());
+      case 64: return fmt(d, ns, std::integral_constant<int, 64>());
+      default: return fmt(d, ns, std::integral_constant<int, wide ? 128 : 64>());
     }
   };
   auto dims = [&](auto ns) {
@@ -787,14 +906,13 @@ auto dispatch_tc(int D, int nsrc, int rows, F f) {
 }  // namespace
 
 bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
-  if (a.is_f32 || a.q4) return false;
+  if (a.is_f32) return false;
   const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
   plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  // fused rows of 128 channels leave too little room for tiles beside 128 columns
-  if (nsrc == 2 && a.head_dim == 128 && plan->rows == 128) plan->rows = 64;
+  if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim == 128))) plan->rows = 64;
   plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
-  dispatch_tc(a.head_dim, nsrc, plan->rows, [&](auto d, auto ns, auto nc) {
-    size_tc<decltype(d)::value, decltype(ns)::value, decltype(nc)::value>(a.batch, plan);
+  dispatch_tc(a.head_dim, nsrc, plan->rows, a.q4, [&](auto d, auto ns, auto nc, auto q4) {
+    size_tc<decltype(d)::value, decltype(ns)::value, decltype(nc)::value, decltype(q4)::value>(a.batch, plan);
   });
   if (plan->slots == 0) return false;
   // one CTA an SM over ranges and row tiles; the device takes fewer ranges
@@ -805,13 +923,14 @@ bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
 }
 
 cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  return dispatch_tc(a.head_dim, a.k[1] ? 2 : 1, plan.rows, [&](auto d, auto ns, auto nc) {
+  return dispatch_tc(a.head_dim, a.k[1] ? 2 : 1, plan.rows, a.q4, [&](auto d, auto ns, auto nc, auto q4) {
     constexpr int D = decltype(d)::value, NS = decltype(ns)::value, NC = decltype(nc)::value;
+    constexpr bool Q4 = decltype(q4)::value;
     if constexpr (NS == 2) {
-      return launch_tc<D, 2, true, NC>(p, a, plan, stream);
+      return launch_tc<D, 2, true, NC, Q4>(p, a, plan, stream);
     } else {
-      if (a.a[0]) return launch_tc<D, 1, true, NC>(p, a, plan, stream);
-      return launch_tc<D, 1, false, NC>(p, a, plan, stream);
+      if (a.a[0]) return launch_tc<D, 1, true, NC, Q4>(p, a, plan, stream);
+      return launch_tc<D, 1, false, NC, Q4>(p, a, plan, stream);
     }
   });
 }
