@@ -54,6 +54,7 @@ namespace {
 constexpr int KT = 128;               // keys per tile
 constexpr int SM_THREADS = 256;       // softmax threads
 constexpr int DQ_THREADS = 256;       // dequantising threads (4-bit caches)
+constexpr int DQ_GROUP = 64;          // of them that share a tile: four tiles are in work at a time
 constexpr int MAX_RAW = 12;           // slots of records
 constexpr int PRODUCER_WARP = 8, QK_WARP = 9, PV_WARP = 10;
 constexpr int MAX_SLOTS = 12;
@@ -73,7 +74,7 @@ struct TcCfg {
   // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
   // past its end into what follows (rows that are not used)
   static constexpr int OVERRUN = (2 - CB) * KT * SWB;
-  static constexpr int MISC = (2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 16 * 8 + 64   // barriers, words
+  static constexpr int MISC = (2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 18 * 8 + 64   // barriers, words
                               + NC * 4 * 8                             // reference, alpha, depth, node, sums
                               + kTreeMaxNodes * (16 + 4 + NW * 4)      // masks, depths, column masks
                               + 4 * NC * 4;                            // warp maxima / sums
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   uint64_t* q_ready = raw_empty + MAX_RAW;
   uint64_t* s_full = q_ready + 1;   // [2]
   uint64_t* p_full = s_full + 2;    // [2]
-  uint64_t* o_done = p_full + 2;    // [2]
-  uint64_t* drain = o_done + 2;     // [2] an issuer's last products, after an abort
+  uint64_t* o_done = p_full + 2;    // [4]
+  uint64_t* drain = o_done + 4;     // [2] an issuer's last products, after an abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
@@ -184,19 +185,19 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   const int rt = blockIdx.y;
   if (tid == 0) {
     for (int s = 0; s < nslots; ++s) {
-      mbar_init(&full[s], Q4 ? DQ_THREADS / 32 : 1);
+      mbar_init(&full[s], Q4 ? DQ_GROUP / 32 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; Q4 && s < nraw; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], DQ_THREADS / 32);
+      mbar_init(&raw_empty[s], DQ_GROUP / 32);
     }
     mbar_init(q_ready, SM_THREADS);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], SM_THREADS);
-      mbar_init(&o_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&o_done[i], 1);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
@@ -228,6 +229,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     flag_status(p.status, kDevTimeout);
     return false;
   };
+  // the value products of tile t are done
+  auto products = [&](int t) { return wait(&o_done[t & 3], (uint32_t)(t >> 2) & 1u); };
   auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
 
   if (active && warp >= 8 && warp < 12)
@@ -302,19 +305,33 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_DQ));
     if constexpr (Q4) {
       constexpr int GR = D / kQ4Group, RB = q4_row_bytes(D);
-      const int t = tid - 12 * 32;
+      constexpr int GROUPS = DQ_THREADS / DQ_GROUP;
+      const int t = (tid - 12 * 32) % DQ_GROUP;
       const __nv_bfloat162 bias = __floats2bfloat162_rn(-128.f, -128.f);
       const long long total = (walk.t1 - walk.t) * 2 * NSRC;
       int sl = 0, r = 0;
       uint32_t turn = 1, rturn = 0;   // parities of the slot's last release and of the records' filling
-      for (long long g = 0; g < total; ++g) {
+      auto step = [&]() {
+        if (++sl == nslots) {
+          sl = 0;
+          turn ^= 1;
+        }
+        if (++r == nraw) {
+          r = 0;
+          rturn ^= 1;
+        }
+      };
+      // Both rings hold a multiple of GROUPS slots, so a slot stays with one
+      // group and no phase of its barriers is awaited before the last is over.
+      const int first = (tid - 12 * 32) / DQ_GROUP;
+      for (int k = 0; k < first; ++k) step();
+      for (long long g = first; g < total; g += GROUPS) {
         if (!__all_sync(0xffffffffu, wait(&raw_full[r], rturn) && (g < nslots || wait(&empty[sl], turn)))) break;
         const uint8_t* rec = sRaw + (size_t)r * C::RAW;
         uint8_t* dst = slot_ptr(sl);
-#pragma unroll
-        for (int k = 0; k < (KT * GR + DQ_THREADS - 1) / DQ_THREADS; ++k) {
-          const int it = t + k * DQ_THREADS;
-          if (KT * GR % DQ_THREADS != 0 && it >= KT * GR) break;
+#pragma unroll 4
+        for (int k = 0; k < KT * GR / DQ_GROUP; ++k) {   // a multiple: KT = 2 * DQ_GROUP
+          const int it = t + k * DQ_GROUP;
           const int row = it / GR, gr = it - row * GR;
           const uint2 codes = *reinterpret_cast<const uint2*>(rec + row * RB + gr * 8);
           const uint32_t prm = *reinterpret_cast<const uint32_t*>(rec + row * RB + D / 2 + gr * 4);
@@ -343,14 +360,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
           mbar_arrive(&full[sl]);
           mbar_arrive(&raw_empty[r]);
         }
-        if (++sl == nslots) {
-          sl = 0;
-          turn ^= 1;
-        }
-        if (++r == nraw) {
-          r = 0;
-          rturn ^= 1;
-        }
+        for (int k = 0; k < GROUPS; ++k) step();
       }
     }
   } else if (active && (warp == QK_WARP || warp == PV_WARP)) {
@@ -381,11 +391,13 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         const int n = pc.k1 - pc.k0;
         if (qk) {
           // S = K (q a)^T, both sources; its buffer is free once P of the
-          // tile two before is written
+          // tile two before is written.  A slot's phase may only be awaited
+          // when the one before it is known to be over: the slot of K_j held
+          // keys, or the values of tile j - 3 at the latest.
           ok = wait(q_ready, (uint32_t)piece & 1u);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const uint32_t d = tmem + (j & 1) * NC;
-            ok = j < 2 || wait(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u);
+            ok = (j < 2 || wait(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u)) && (j < 3 || products(j - 3));
 #pragma unroll
             for (int src = 0; src < NSRC; ++src) {
               if (!ok || !wait(&full[sl], turn)) {
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
                 for (int k = 1; k < ks; ++k)
                   mma_bf16_t<true>(d, a.at(k * 16 * SWB), b.at(k * 16 * SWB), IDESC_PV);
               }
-              if (src == NSRC - 1) mma_commit(&o_done[j & 1]);
+              if (src == NSRC - 1) mma_commit(&o_done[j & 3]);
               mma_commit(&empty[sl]);
               skip(1);
             }
@@ -567,7 +579,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
           // (once the products of the tile before are done, the slots' phases
           // before the awaited ones are known to be over)
           if (i > 0 && ok &&
-              !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
+              !__all_sync(0xffffffffu, products(j - 1)))
             ok = false;
           const int g0 = base + v_slot(i, n) * NSRC;
 #pragma unroll
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
           }
           // O holds every product before this tile once the last one is done
           if (i > 0 && ok &&
-              !__all_sync(0xffffffffu, wait(&o_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u)))
+              !__all_sync(0xffffffffu, products(j - 1)))
             ok = false;
           tc_fence_after();
           wg_sync(wg);
@@ -707,7 +719,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
 
         // P of this key: 2^x, bf16
         const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
-        if (pj >= 0 && ok && !__all_sync(0xffffffffu, wait(&o_done[pj & 1], (uint32_t)(pj >> 1) & 1u)))
+        if (pj >= 0 && ok && !__all_sync(0xffffffffu, products(pj)))
           ok = false;
         uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
 #pragma unroll
@@ -731,7 +743,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
       // the sums of the columns over all keys, and the last products
       const int jl = jt + n - 1;
-      if (ok && !__all_sync(0xffffffffu, wait(&o_done[jl & 1], (uint32_t)(jl >> 1) & 1u))) ok = false;
+      if (ok && !__all_sync(0xffffffffu, products(jl))) ok = false;
       if (any_of(1, SM_THREADS, !ok)) break;
       tc_fence_after();
       constexpr int RN = HC < 32 ? HC : 32;
@@ -825,16 +837,18 @@ void size_tc(int B, TreePlan* plan) {
   int left = SMEM_LIMIT - fixed;
   plan->raw_slots = 0;
   if (Q4) {
-    // records for at least two tiles, the rest beside as many tile slots as
+    // records for at least a tile a group, the rest beside as many tile slots as
     // the MMAs need (and two tiles more where they are small)
-    const int want = C::SLOT <= 16384 ? 4 * NSRC : 2 * NSRC;
-    int raw = (left - want * C::SLOT) / C::RAW;
-    raw = raw > MAX_RAW ? MAX_RAW : raw < 2 * NSRC ? 2 * NSRC : raw;
+    constexpr int GROUPS = DQ_THREADS / DQ_GROUP;
+    const int want = C::SLOT <= 16384 ? 4 * NSRC : GROUPS;
+    int raw = (left - want * C::SLOT) / C::RAW / GROUPS * GROUPS;
+    raw = raw > MAX_RAW ? MAX_RAW : raw < GROUPS ? GROUPS : raw;
     plan->raw_slots = raw;
     left -= raw * C::RAW;
   }
   int slots = left > 0 ? left / C::SLOT : 0;
   if (slots > MAX_SLOTS) slots = MAX_SLOTS;
+  if (Q4) slots = slots / (DQ_THREADS / DQ_GROUP) * (DQ_THREADS / DQ_GROUP);
   // the block past the last slot's end lies in Q and P
   if (slots < 2 * NSRC || C::OVERRUN > C::Q_BYTES + C::NPB * C::P_BYTES) slots = 0;
   plan->slots = slots;
