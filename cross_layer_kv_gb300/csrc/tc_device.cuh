@@ -49,7 +49,19 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-// The same with the accumulate flag known at compile time.
+// True in one lane of the (converged) warp, the same one every time.  An
+// issuing loop that the whole warp runs, with only the MMAs under this
+// predicate, keeps the operand descriptors in uniform registers: a burst of 8
+// MMAs then takes 48 clocks an MMA, against 87 from a lane-0 branch.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// mma_bf16 with the accumulate flag known at compile time.
 template <bool ACC>
 __device__ __forceinline__ void mma_bf16_t(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                            uint32_t idesc) {

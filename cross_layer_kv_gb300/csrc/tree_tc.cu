@@ -24,8 +24,8 @@
 //    K_0, K_1, V_0, K_2, V_1, ...;
 //  * one warp issues S_j = K_j Q^T up to two tiles ahead (S has two buffers in
 //    tensor memory), another O += V_j^T P_j: an MMA of these sizes costs its
-//    issuing thread 46 clocks at 16 to 64 columns (64 at 128), as long as the
-//    tensor pipe, so one thread for both was the bound of small trees;
+//    issuer 40 to 48 clocks at 16 to 64 columns (64 at 128), as long as the
+//    tensor pipe, so one issuer for both was the bound of small trees;
 //  * two softmax warpgroups take half of the columns each: scores from tensor
 //    memory, P to shared memory as an MN-major operand (a thread writes its
 //    key's columns, 16 bytes at a time, without bank conflicts).
@@ -364,47 +364,49 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
     }
   } else if (active && (warp == QK_WARP || warp == PV_WARP)) {
-    // ---------------- MMA issuers ----------------
-    if (lane == 0) {
-      constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
-      constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
-      const bool qk = warp == QK_WARP;
-      // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
-      const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
-                             : sdesc128(smem_u32(sRing), KT * SWB, 8 * SWB);
-      const SDesc128 db = qk ? sdesc128(smem_u32(sQ), 16, 8 * SWB)
-                             : sdesc128(smem_u32(sP), KT * SWB, 8 * SWB);
-      int sl = 0;          // next slot
-      uint32_t turn = 0;   // parity of its filling
-      auto skip = [&](int n) {
-        sl += n;
-        if (sl >= nslots) {
-          sl -= nslots;
-          turn ^= 1;
-        }
-      };
-      int j = 0;   // tile of this CTA
-      int piece = 0;
-      bool ok = true;
-      TreePiece pc;
-      while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
-        const int n = pc.k1 - pc.k0;
-        if (qk) {
-          // S = K (q a)^T, both sources; its buffer is free once P of the
-          // tile two before is written.  A slot's phase may only be awaited
-          // when the one before it is known to be over: the slot of K_j held
-          // keys, or the values of tile j - 3 at the latest.
-          ok = wait(q_ready, (uint32_t)piece & 1u);
-          for (int i = 0; ok && i < n; ++i, ++j) {
-            const uint32_t d = tmem + (j & 1) * NC;
-            ok = (j < 2 || wait(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u)) && (j < 3 || products(j - 3));
+    // ---------------- MMA issuers (the whole warp; one lane issues) ----------------
+    constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
+    constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
+    const bool qk = warp == QK_WARP;
+    auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
+    const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
+                           : sdesc128(smem_u32(sRing), KT * SWB, 8 * SWB);
+    const SDesc128 db = qk ? sdesc128(smem_u32(sQ), 16, 8 * SWB)
+                           : sdesc128(smem_u32(sP), KT * SWB, 8 * SWB);
+    int sl = 0;          // next slot
+    uint32_t turn = 0;   // parity of its filling
+    auto skip = [&](int n) {
+      sl += n;
+      if (sl >= nslots) {
+        sl -= nslots;
+        turn ^= 1;
+      }
+    };
+    int j = 0;   // tile of this CTA
+    int piece = 0;
+    bool ok = true;
+    TreePiece pc;
+    while (ok && walk.next(sq.pre, p.B, p.H, pc)) {
+      const int n = pc.k1 - pc.k0;
+      if (qk) {
+        // S = K (q a)^T, both sources; its buffer is free once P of the tile
+        // two before is written.  A slot's phase may only be awaited when the
+        // one before it is known to be over: the slot of K_j held keys, or the
+        // values of tile j - 3 at the latest.
+        ok = await(q_ready, (uint32_t)piece & 1u);
+        for (int i = 0; ok && i < n; ++i, ++j) {
+          const uint32_t d = tmem + (j & 1) * NC;
+          ok = (j < 2 || await(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u)) &&
+               (j < 3 || __all_sync(0xffffffffu, products(j - 3)));
 #pragma unroll
-            for (int src = 0; src < NSRC; ++src) {
-              if (!ok || !wait(&full[sl], turn)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+          for (int src = 0; src < NSRC; ++src) {
+            if (!ok || !await(&full[sl], turn)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
@@ -415,27 +417,30 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
               }
               if (src == NSRC - 1) mma_commit(&s_full[j & 1]);
               mma_commit(&empty[sl]);
-              skip(1);
             }
-            // the values of the tile before lie between K_i and K_i+1 (i > 0),
-            // those of the last two behind the piece's last keys
-            skip(i == n - 1 ? (n == 1 ? 1 : 2) * NSRC : i == 0 ? 0 : NSRC);
+            __syncwarp();
+            skip(1);
           }
-        } else {
-          const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
-          skip((n == 1 ? 1 : 2) * NSRC);   // V_0 follows K_0 and K_1
-          for (int i = 0; ok && i < n; ++i, ++j) {
-            const int ks = i + 1 == n || p.ring > 0 ? (tree_tile(p, s, pc.k0 + i, KT).cnt + 15) / 16
-                                                    : KT / 16;   // 16-key steps
-            ok = wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
-            const SDesc128 b{db.lo + (NPB == 2 && (j & 1) ? C::P_BYTES >> 4 : 0), db.hi};
+          // the values of the tile before lie between K_i and K_i+1 (i > 0),
+          // those of the last two behind the piece's last keys
+          skip(i == n - 1 ? (n == 1 ? 1 : 2) * NSRC : i == 0 ? 0 : NSRC);
+        }
+      } else {
+        const TreeSeq s = tree_seq(p, sq.P[pc.b], sq.N[pc.b]);
+        skip((n == 1 ? 1 : 2) * NSRC);   // V_0 follows K_0 and K_1
+        for (int i = 0; ok && i < n; ++i, ++j) {
+          const int ks = i + 1 == n || p.ring > 0 ? (tree_tile(p, s, pc.k0 + i, KT).cnt + 15) / 16
+                                                  : KT / 16;   // 16-key steps
+          ok = await(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
+          const SDesc128 b{db.lo + (NPB == 2 && (j & 1) ? C::P_BYTES >> 4 : 0), db.hi};
 #pragma unroll
-            for (int src = 0; src < NSRC; ++src) {
-              if (!ok || !wait(&full[sl], turn)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+          for (int src = 0; src < NSRC; ++src) {
+            if (!ok || !await(&full[sl], turn)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
               const uint32_t d = tmem + (2 + src) * NC;
               mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i > 0 ? 1u : 0u);
@@ -449,13 +454,14 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
               }
               if (src == NSRC - 1) mma_commit(&o_done[j & 3]);
               mma_commit(&empty[sl]);
-              skip(1);
             }
-            if (i + 2 < n) skip(NSRC);   // the keys of the tile after next
+            __syncwarp();
+            skip(1);
           }
+          if (i + 2 < n) skip(NSRC);   // the keys of the tile after next
         }
-        ++piece;
       }
+      ++piece;
     }
   } else if (active && warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
@@ -815,7 +821,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       for (int g = max(0, issued - nring); g < issued; ++g)
         (void)mbar_wait_bounded(&ring_full[g % nring], (uint32_t)(g / nring) & 1u, kDrainLimitNs);
     }
-    if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
+    if ((warp == QK_WARP || warp == PV_WARP) && elect_one()) {
       mma_commit(&drain[warp - QK_WARP]);
       (void)mbar_wait_bounded(&drain[warp - QK_WARP], 0, kDrainLimitNs);
     }
