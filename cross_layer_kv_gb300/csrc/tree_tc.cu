@@ -4,8 +4,8 @@
 // against the cached keys, so the call is bound by reading the cache once.
 // The products are taken transposed, keys as the 128 rows of the MMA and the
 // query rows as its NC = 16 .. 128 columns: S^T = K Q^T, O^T = V^T P^T.  A
-// thread of the softmax then owns a key, not a query row, so that all 256
-// threads work however few query rows there are.
+// thread of the softmax then owns a key, not a query row, so that all threads
+// work however few query rows there are.
 //
 // Math.  Online softmax in base 2 with one reference m_c per column c; a tile
 // keeps the reference unless a score exceeds it by more than 2^8 (P stays
@@ -26,8 +26,8 @@
 //    tensor memory), another O += V_j^T P_j: an MMA of these sizes costs its
 //    issuer 40 to 48 clocks at 16 to 64 columns (64 at 128), as long as the
 //    tensor pipe, so one issuer for both was the bound of small trees;
-//  * two softmax warpgroups take half of the columns each: scores from tensor
-//    memory, P to shared memory as an MN-major operand (a thread writes its
+//  * two or four softmax warpgroups take every second tile or a part of the
+//    columns (TcCfg): scores from tensor memory, P to shared memory as an MN-major operand (a thread writes its
 //    key's columns, 16 bytes at a time, without bank conflicts).
 // 4-bit caches: the producer copies a tile's records (one contiguous run) to a
 // second ring, and two more warpgroups dequantise them into the slots, two
@@ -52,11 +52,9 @@ namespace fkv {
 namespace {
 
 constexpr int KT = 128;               // keys per tile
-constexpr int SM_THREADS = 256;       // softmax threads
 constexpr int DQ_THREADS = 256;       // dequantising threads (4-bit caches)
 constexpr int DQ_GROUP = 64;          // of them that share a tile: four tiles are in work at a time
 constexpr int MAX_RAW = 12;           // slots of records
-constexpr int PRODUCER_WARP = 8, QK_WARP = 9, PV_WARP = 10;
 constexpr int MAX_SLOTS = 12;
 constexpr int TAIL_ROWS = 16;         // rows of the boxes of a ragged tile
 constexpr int SMEM_LIMIT = 232448;
@@ -73,27 +71,44 @@ struct TcCfg {
   static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
   // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
   // past its end into what follows (rows that are not used)
-  static constexpr int OVERRUN = (2 - CB) * KT * SWB;
-  static constexpr int MISC = (2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 18 * 8 + 64   // barriers, words
-                              + NC * 4 * 8                             // reference, alpha, depth, node, sums
-                              + kTreeMaxNodes * (16 + 4 + NW * 4)      // masks, depths, column masks
-                              + 4 * NC * 4;                            // warp maxima / sums
-  static constexpr int FIXED = 1024 + Q_BYTES + MISC;
-  static constexpr int TMEM_USED = (2 + NSRC) * NC;
+  static constexpr int OVERRUN = Q4 ? 0 : (2 - CB) * KT * SWB;   // (the records follow 4-bit slots)
+  // Softmax warpgroups.  Up to 32 columns: two, each with every second tile,
+  // its own references, sums and accumulators (joined when a piece ends), so
+  // that one's waits overlap the other's work.  More columns: each warpgroup
+  // takes a part of the columns of every tile.
+  static constexpr int TS = NC <= 32 ? 2 : 1;            // tiles in work
+  static constexpr int CS = NC <= 32 ? 1 : Q4 ? 2 : 4;   // column parts
+  static constexpr int NWG = TS * CS;
+  static constexpr int SM = NWG * 128;                   // softmax threads
+  static constexpr int HC = NC / CS;                     // columns of a softmax thread
+  static constexpr int EC = NC / NWG;                    // columns a warpgroup writes out
+  static constexpr int PRODUCER_WARP = 4 * NWG, QK_WARP = PRODUCER_WARP + 1, PV_WARP = PRODUCER_WARP + 2;
+  static constexpr int DQ_WARP = PRODUCER_WARP + 4;      // the first of the dequantising warps
+  static constexpr int TMEM_USED = (2 + TS * NSRC) * NC;
   static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
   static_assert(TMEM_USED <= 512, "tensor memory");
-  // two P buffers where at least five tile slots remain beside them
-  static constexpr int NPB = (SMEM_LIMIT - FIXED - 2 * P_BYTES - 12 * 64) / SLOT >= 5 ? 2 : 1;
-  static constexpr int HC = NC / 2;                      // columns of a softmax warpgroup
+  // barriers and words, then the arrays of floats and masks
+  static constexpr int BAR_BYTES = ((2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 11 * 8 + 6 * 4 + 127) / 128 * 128;
+  static constexpr int ARRAY_BYTES = NC * 4 * (2 * TS + 2 + 4 * TS) + kTreeMaxNodes * (16 + 4 + NW * 4);
+  // two P buffers where warpgroups take whole tiles, or where at least five
+  // tile slots remain beside them
+  static constexpr int NPB =
+      TS == 2 || (SMEM_LIMIT - 3072 - Q_BYTES - BAR_BYTES - ARRAY_BYTES - OVERRUN - 2 * P_BYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int REF_OFF = Q_BYTES + NPB * P_BYTES + BAR_BYTES;
+  __host__ __device__ static constexpr int ring_off(int B) {
+    return (REF_OFF + ARRAY_BYTES + (int)tree_seqs_bytes(B) + 1023) / 1024 * 1024;
+  }
   static constexpr int RAW = KT * q4_row_bytes(D);       // records of a tile
-  static constexpr int THREADS = SM_THREADS + 128 + (Q4 ? DQ_THREADS : 0);
+  static constexpr int THREADS = SM + 128 + (Q4 ? DQ_THREADS : 0);
   // registers a thread: 168 at launch with 384 threads, 96 with 640; the
   // control (and dequantising) warpgroups give some up for the softmax:
-  // 256 * 208 + 128 * 88 = 384 * 168, 256 * 128 + 128 * 64 + 256 * 80 = 640 * 96
-  static constexpr int REGS_CONTROL = Q4 ? 64 : 88, REGS_SOFTMAX = Q4 ? 128 : 208, REGS_DQ = 80;
+  // 256 * 208 + 128 * 88 = 384 * 168, 512 * 104 + 128 * 64 = 640 * 96,
+  // 256 * 128 + 128 * 64 + 256 * 80 = 640 * 96
+  static constexpr int REGS_CONTROL = THREADS > 384 ? 64 : 88;
+  static constexpr int REGS_SOFTMAX = Q4 ? 128 : NWG == 4 ? 104 : 208, REGS_DQ = 80;
   static constexpr int REGS_SPLIT =
-      SM_THREADS * REGS_SOFTMAX + 128 * REGS_CONTROL + (Q4 ? DQ_THREADS * REGS_DQ : 0);
+      SM * REGS_SOFTMAX + 128 * REGS_CONTROL + (Q4 ? DQ_THREADS * REGS_DQ : 0);
 };
 
 struct TcMaps {
@@ -121,7 +136,9 @@ __device__ __forceinline__ float reduce_scatter(float* v, int lane, Op op) {
   return r;
 }
 
-__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// All softmax threads.
+template <int COUNT>
+__device__ __forceinline__ void sm_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(COUNT) : "memory"); }
 
 // Whether x holds in any thread of `count` threads that meet at barrier `id`.
 __device__ __forceinline__ bool any_of(int id, int count, bool x) {
@@ -149,14 +166,16 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots,
                    const int nraw) {
   using C = TcCfg<D, NSRC, NC, Q4>;
-  constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB;
+  constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB, TS = C::TS, CS = C::CS;
+  auto sm_sync = [] { sm_barrier<C::SM>(); };
+  // Everything before the rings lies at offsets known at compile time, from a
+  // pointer that the compiler sees is shared memory: addresses cost no
+  // registers.  1024 bytes: the period of the 128-byte swizzle.
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sRing = smem;
-  uint8_t* sQ = sRing + (size_t)nslots * C::SLOT;
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  uint8_t* sQ = smem;
   uint8_t* sP = sQ + C::Q_BYTES;
-  uint8_t* sRaw = sP + NPB * C::P_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + (Q4 ? (size_t)nraw * C::RAW : 0));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sP + NPB * C::P_BYTES);
   uint64_t* empty = full + MAX_SLOTS;
   uint64_t* raw_full = empty + MAX_SLOTS;
   uint64_t* raw_empty = raw_full + MAX_RAW;
@@ -170,16 +189,17 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
   int* merge_flag = sm_issued + 1;
   int* sm_span = merge_flag + 1;                               // [2] least and largest depth
-  unsigned long long* sMask =
-      reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(sm_span + 2) + 15) & ~uintptr_t(15));
-  float* sRef = reinterpret_cast<float*>(sMask + 2 * kTreeMaxNodes);   // [NC] negated reference
-  float* sAlpha = sRef + NC;                                   // [NC] rescale, then 1 / sum
-  int* sDepth = reinterpret_cast<int*>(sAlpha + NC);           // [NC] depth of the column's node
+  float* sRef = reinterpret_cast<float*>(smem + C::REF_OFF);   // [TS][NC] negated reference
+  float* sAlpha = sRef + TS * NC;                              // [TS][NC] rescale, then weight
+  int* sDepth = reinterpret_cast<int*>(sAlpha + TS * NC);      // [NC] depth of the column's node
   int* sNode = sDepth + NC;                                    // [NC] node of the column, -1: none
-  float* sWarp = reinterpret_cast<float*>(sNode + NC);         // [4][NC]
-  int* sNodeDepth = reinterpret_cast<int*>(sWarp + 4 * NC);    // [kTreeMaxNodes]
-  uint32_t* sVis = reinterpret_cast<uint32_t*>(sNodeDepth + kTreeMaxNodes);   // [kTreeMaxNodes][NW]
+  float* sWarp = reinterpret_cast<float*>(sNode + NC);         // [TS][4][NC]
+  unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sWarp + TS * 4 * NC);   // [nodes][2]
+  int* sNodeDepth = reinterpret_cast<int*>(sMask + 2 * kTreeMaxNodes);   // [nodes]
+  uint32_t* sVis = reinterpret_cast<uint32_t*>(sNodeDepth + kTreeMaxNodes);   // [nodes][NW]
   const TreeSeqs sq = tree_seqs(reinterpret_cast<int*>(sVis + kTreeMaxNodes * NW), p.B);
+  uint8_t* sRing = smem + C::ring_off(p.B);
+  uint8_t* sRaw = sRing + (size_t)nslots * C::SLOT;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rt = blockIdx.y;
@@ -192,10 +212,10 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], DQ_GROUP / 32);
     }
-    mbar_init(q_ready, SM_THREADS);
+    mbar_init(q_ready, C::SM / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], SM_THREADS);
+      mbar_init(&p_full[i], CS * 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&o_done[i], 1);
     mbar_init(&drain[0], 1);
@@ -204,12 +224,12 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     *sm_issued = 0;
     fence_mbar_init();
   }
-  if (warp == QK_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  if (warp == C::QK_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
   for (int c = tid; c < NC; c += C::THREADS) {
     const int row = rt * NC + c;
     sNode[c] = row < p.G * p.T ? row % p.T : -1;
   }
-  if (!Q4 && warp == PRODUCER_WARP && lane < 8 && (lane & 1) < NSRC)
+  if (!Q4 && warp == C::PRODUCER_WARP && lane < 8 && (lane & 1) < NSRC)
     tma_prefetch(lane < 4 ? &maps.full[lane] : &maps.tail[lane - 4]);
   grid_dep_trigger();
   grid_dep_wait();
@@ -233,9 +253,9 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   auto products = [&](int t) { return wait(&o_done[t & 3], (uint32_t)(t >> 2) & 1u); };
   auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
 
-  if (active && warp >= 8 && warp < 12)
+  if (active && warp >= C::PRODUCER_WARP && warp < C::DQ_WARP)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
-  if (active && warp == PRODUCER_WARP) {
+  if (active && warp == C::PRODUCER_WARP) {
     // ---------------- producer ----------------
     if (lane == 0) {
       const int nring = Q4 ? nraw : nslots;
@@ -300,13 +320,13 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
       *sm_issued = g;
     }
-  } else if (Q4 && active && warp >= 12) {
+  } else if (Q4 && active && warp >= C::DQ_WARP) {
     // ---------------- dequantisation ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_DQ));
     if constexpr (Q4) {
       constexpr int GR = D / kQ4Group, RB = q4_row_bytes(D);
       constexpr int GROUPS = DQ_THREADS / DQ_GROUP;
-      const int t = (tid - 12 * 32) % DQ_GROUP;
+      const int t = (tid - C::DQ_WARP * 32) % DQ_GROUP;
       const __nv_bfloat162 bias = __floats2bfloat162_rn(-128.f, -128.f);
       const long long total = (walk.t1 - walk.t) * 2 * NSRC;
       int sl = 0, r = 0;
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       };
       // Both rings hold a multiple of GROUPS slots, so a slot stays with one
       // group and no phase of its barriers is awaited before the last is over.
-      const int first = (tid - 12 * 32) / DQ_GROUP;
+      const int first = (tid - C::DQ_WARP * 32) / DQ_GROUP;
       for (int k = 0; k < first; ++k) step();
       for (long long g = first; g < total; g += GROUPS) {
         if (!__all_sync(0xffffffffu, wait(&raw_full[r], rturn) && (g < nslots || wait(&empty[sl], turn)))) break;
@@ -363,11 +383,11 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         for (int k = 0; k < GROUPS; ++k) step();
       }
     }
-  } else if (active && (warp == QK_WARP || warp == PV_WARP)) {
+  } else if (active && (warp == C::QK_WARP || warp == C::PV_WARP)) {
     // ---------------- MMA issuers (the whole warp; one lane issues) ----------------
     constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
     constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
-    const bool qk = warp == QK_WARP;
+    const bool qk = warp == C::QK_WARP;
     auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
     // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
     const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
@@ -442,8 +462,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
             tc_fence_after();
             if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
-              const uint32_t d = tmem + (2 + src) * NC;
-              mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i > 0 ? 1u : 0u);
+              const uint32_t d = tmem + (2 + (TS == 2 ? j & 1 : 0) * NSRC + src) * NC;
+              mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i >= TS ? 1u : 0u);
               if (ks == KT / 16) {
 #pragma unroll
                 for (int k = 1; k < KT / 16; ++k)
@@ -463,12 +483,17 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
       ++piece;
     }
-  } else if (active && warp < 8) {
+  } else if (active && warp < C::PRODUCER_WARP) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ---------------- softmax ----------------
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
-    const int c0 = wg * HC;                // first column
+    const int ts = wg / CS;                // which tiles (TS == 2: those of this parity)
+    const int c0 = (wg % CS) * HC;         // first column
+    float* ref = sRef + ts * NC;
+    float* alpha = sAlpha + ts * NC;
+    float* part = sWarp + ts * 4 * NC;
+    const uint32_t t_acc = tmem + ((uint32_t)(quarter * 32) << 16) + (2 + ts * NSRC) * NC;   // its accumulators
     const int chan = Q4 ? (key & ~7) | (key & 1) << 2 | (key >> 1 & 3) : key;   // channel of row `key` of V^T
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
     auto fmaxop = [](float a, float b) { return fmaxf(a, b); };
@@ -484,7 +509,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       const int rows = min(NC, p.G * p.T - rt * NC);
 
       // the piece's queries times the key weights, in the MMA's layout
-      for (int it = tid; it < NC * (CB * 8); it += SM_THREADS) {
+      for (int it = tid; it < NC * (CB * 8); it += C::SM) {
         const int r = it / (CB * 8), ch = it - r * (CB * 8);   // 16-byte chunk of a row
         const int d = ch * 8;
         uint4 w = make_uint4(0, 0, 0, 0);
@@ -532,7 +557,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         sm_span[0] = kTreeMaxNodes;
         sm_span[1] = 0;
       }
-      if (tid < NC) sRef[tid] = FLT_MAX;
+      if (tid < TS * NC) sRef[tid] = FLT_MAX;
       sm_sync();
       if (tid < NC) {
         const int i = sNode[tid];
@@ -544,13 +569,14 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         }
       }
       {
-        // a warp takes every (8 / NW)-th drafted key, its lanes 32 columns
+        // a warp takes every STEP-th drafted key, its lanes 32 columns
+        constexpr int STEP = 4 * C::NWG / NW;
         const int w = warp % NW, c = w * 32 + lane;
         const int node = c < NC ? sNode[c] : -1;
         const bool live = node >= 0 && node < N;
         const unsigned long long m0 = live ? sMask[2 * node] : 0ull, m1 = live ? sMask[2 * node + 1] : 0ull;
         const int floor = live && p.window > 0 ? sNodeDepth[node] - p.window : -1;
-        for (int q = warp / NW; q < N; q += 8 / NW) {
+        for (int q = warp / NW; q < N; q += STEP) {
           const bool see = ((q < 64 ? m0 : m1) >> (q & 63) & 1) && sNodeDepth[q] > floor;
           const uint32_t v = __ballot_sync(0xffffffffu, see);
           if (lane == 0) sVis[q * NW + w] = v;
@@ -558,7 +584,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(q_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
       sm_sync();
       const int least = sm_span[0], most = sm_span[1];
 
@@ -571,12 +598,13 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       // threads, and all leave together at the piece's end.
       for (int i = 0; i < n; ++i) {
         const int j = jt + i;
+        if (TS == 2 && (j & 1) != ts) continue;
         const TreeTile t = tree_tile(p, s, pc.k0 + i, KT);
         if (ok && !__all_sync(0xffffffffu, wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u))) ok = false;
         tc_fence_after();
-        const uint32_t ts = t_lane + (j & 1) * NC;
+        const uint32_t t_s = t_lane + (j & 1) * NC;
         const bool edge = p.window > 0 && t.pos <= P + most - p.window;
-        const bool masked = t.cnt < KT || t.pos + t.cnt > P || edge;   // uniform over the CTA
+        const bool masked = t.cnt < KT || t.pos + t.cnt > P || edge;   // uniform over the tile's threads
         const int q = t.pos + key - P;   // >= 0: drafted node q
         bool poison = false;
         if (masked) {
@@ -617,8 +645,9 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
               }
             }
           }
-          sm_sync();   // both warpgroups have looked
-          if (wg == 0 && ok && (!seen || poison) && key < (t.cnt + 15) / 16 * 16) {
+          if (CS > 1) sm_sync();   // the other parts' warpgroups have looked too
+          else wg_sync(wg);
+          if (wg % CS == 0 && ok && (!seen || poison) && key < (t.cnt + 15) / 16 * 16) {
 #pragma unroll 1
             for (int src = 0; src < NSRC; ++src) {
               uint8_t* v = slot_ptr((g0 + src) % nslots);
@@ -631,13 +660,11 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         // this key's scores, -inf where a column does not see it
         float sv[HC];
         auto scores = [&]() {
-          if constexpr (HC == 8) {
-            tmem_ld8(ts, sv);
-          } else if constexpr (HC == 16) {
-            tmem_ld16(ts, sv);
+          if constexpr (HC == 16) {
+            tmem_ld16(t_s, sv);
           } else {
 #pragma unroll
-            for (int c = 0; c < HC; c += 32) tmem_ld32(ts + c, sv + c);
+            for (int c = 0; c < HC; c += 32) tmem_ld32(t_s + c, sv + c);
           }
           tmem_wait_ld();
           if (masked) {
@@ -658,7 +685,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < HC; c += 4) {
-            const float4 r = *reinterpret_cast<const float4*>(sRef + c0 + c);   // negated references
+            const float4 r = *reinterpret_cast<const float4*>(ref + c0 + c);   // negated references
             float x0 = r.x, x1 = r.y, x2 = r.z, x3 = r.w;
             fma2(x0, x1, sv[c], sv[c + 1], p.scale_log2, p.scale_log2);
             fma2(x2, x3, sv[c + 2], sv[c + 3], p.scale_log2, p.scale_log2);
@@ -669,12 +696,13 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
           return fmaxf(top[0], top[1]);
         };
         scores();
-        // the first tile of a piece takes its maxima as references; later ones
-        // keep the references unless a score exceeds its own by more than the slack
-        bool grow = i == 0;
+        // a warpgroup's first tile of a piece takes its maxima as references;
+        // later ones keep them unless a score exceeds its own by more than the slack
+        const bool first = i < TS;
+        bool grow = first;
         if (!grow) grow = any_of(2 + wg, 128, shift() > SLACK);
         if (grow) {
-          if (i > 0) scores();
+          if (!first) scores();
           constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
           for (int b0 = 0; b0 < HC; b0 += RN) {
@@ -682,34 +710,32 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < RN; ++c) v[c] = sv[b0 + c];
             const float m = reduce_scatter<RN>(v, lane, fmaxop);
-            if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
+            if (lane < RN) part[quarter * NC + c0 + b0 + lane] = m;
           }
           wg_sync(wg);
           if ((tid & 127) < HC) {
             const int c = c0 + (tid & 127);
-            const float m = fmaxf(fmaxf(sWarp[c], sWarp[NC + c]), fmaxf(sWarp[2 * NC + c], sWarp[3 * NC + c]));
-            const float old = -sRef[c], ref = fmaxf(old, m * p.scale_log2);
-            sAlpha[c] = fast_exp2(old - ref);
-            sRef[c] = -ref;
+            const float m = fmaxf(fmaxf(part[c], part[NC + c]), fmaxf(part[2 * NC + c], part[3 * NC + c]));
+            const float old = -ref[c], top = fmaxf(old, m * p.scale_log2);
+            alpha[c] = fast_exp2(old - top);
+            ref[c] = -top;
           }
           // O holds every product before this tile once the last one is done
-          if (i > 0 && ok &&
-              !__all_sync(0xffffffffu, products(j - 1)))
-            ok = false;
+          if (!first && ok && !__all_sync(0xffffffffu, products(j - TS))) ok = false;
           tc_fence_after();
           wg_sync(wg);
-          if (i > 0) {
+          if (!first) {
 #pragma unroll
             for (int c = 0; c < HC; c += 8) {
               float al[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                al[e] = sAlpha[c0 + c + e];
+                al[e] = alpha[c0 + c + e];
                 l[c + e] *= al[e];
               }
 #pragma unroll
               for (int src = 0; src < NSRC; ++src) {
-                const uint32_t to = t_lane + (2 + src) * NC + c;
+                const uint32_t to = t_acc + src * NC + c0 + c;
                 float o[8];
                 tmem_ld8(to, o);
                 tmem_wait_ld();
@@ -745,64 +771,93 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        if (ok) mbar_arrive(&p_full[j & 1]);
+        // one arrival a warp: 32 lanes on one barrier would be taken one by one
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&p_full[j & 1]);
       }
       // the sums of the columns over all keys, and the last products
       const int jl = jt + n - 1;
       if (ok && !__all_sync(0xffffffffu, products(jl))) ok = false;
-      if (any_of(1, SM_THREADS, !ok)) break;
+      if (any_of(1, C::SM, !ok)) break;
       tc_fence_after();
       constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
       for (int b0 = 0; b0 < HC; b0 += RN) {
         const float m = reduce_scatter<RN>(l + b0, lane, addop);
-        if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
+        if (lane < RN) part[quarter * NC + c0 + b0 + lane] = m;
       }
       sm_sync();
       const bool whole = n == pc.tiles;
       float* rec = p.ws + ((size_t)(2 * blockIdx.x + (pc.first ? 0 : 1)) * p.row_tiles + rt) *
                               tree_record_floats(NC, D);
       if (tid < NC) {
-        const float sum = (sWarp[tid] + sWarp[NC + tid]) + (sWarp[2 * NC + tid] + sWarp[3 * NC + tid]);
-        sAlpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        // the weights of the accumulators: 2^(reference - top), over the sum
+        // where the piece is its whole unit
+        float L[TS], w[TS], top = -FLT_MAX, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < TS; ++k) {
+          const float* x = sWarp + k * 4 * NC + tid;
+          L[k] = (x[0] + x[NC]) + (x[2 * NC] + x[3 * NC]);
+          top = fmaxf(top, -sRef[k * NC + tid]);
+        }
+#pragma unroll
+        for (int k = 0; k < TS; ++k) {
+          w[k] = L[k] == 0.f ? 0.f : fast_exp2(-sRef[k * NC + tid] - top);
+          sum += L[k] == 0.f ? 0.f : w[k] * L[k];
+        }
+        const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+#pragma unroll
+        for (int k = 0; k < TS; ++k) sAlpha[k * NC + tid] = w[k] * f;
         if (!whole) {
-          rec[NC * D + tid] = -sRef[tid];
+          rec[NC * D + tid] = top;
           rec[NC * D + NC + tid] = sum;
         }
       }
       sm_sync();
-      float b0w = 1.f, b1w = 0.f;
-      if (WGT && key < D) {
-        b0w = p.b[0][(size_t)pc.h * D + chan];
-        if constexpr (NSRC == 2) b1w = p.b[1][(size_t)pc.h * D + chan];
+      float bw[NSRC];
+#pragma unroll
+      for (int src = 0; src < NSRC; ++src) {
+        bw[src] = 1.f;
+        if (WGT && key < D) bw[src] = p.b[src][(size_t)pc.h * D + chan];
       }
 #pragma unroll 1
-      for (int c = 0; c < HC; c += 8) {
-        float o[8], o2[8];
-        tmem_ld8(t_lane + 2 * NC + c, o);
-        if constexpr (NSRC == 2) tmem_ld8(t_lane + 3 * NC + c, o2);
-        tmem_wait_ld();
+      for (int c = wg * C::EC; c < (wg + 1) * C::EC; c += 8) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < TS; ++k) {
+          float o[NSRC][8];
+#pragma unroll
+          for (int src = 0; src < NSRC; ++src)
+            tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + (2 + k * NSRC + src) * NC + c, o[src]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = sAlpha[k * NC + c + e];
+            float y = o[0][e];
+            if constexpr (WGT) y *= bw[0];
+            if constexpr (NSRC == 2) y = fmaf(bw[1], o[1][e], y);
+            x[e] = w == 0.f ? x[e] : fmaf(w, y, x[e]);   // an accumulator without a product is not read
+          }
+        }
         if (key < D) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float x = o[e];
-            if constexpr (WGT) x *= b0w;
-            if constexpr (NSRC == 2) x = fmaf(b1w, o2[e], x);
-            const int cc = c0 + c + e;
+            const int cc = c + e;
             if (whole) {
               const int node = sNode[cc];
-              const float inv = sAlpha[cc];
               if (node >= 0 && node < N)
                 static_cast<__nv_bfloat16*>(p.out)[(unit * p.G * p.T + rt * NC + cc) * D + chan] =
-                    __float2bfloat16_rn(inv == 0.f ? 0.f : x * inv);
+                    __float2bfloat16_rn(x[e]);
             } else {
-              rec[(size_t)cc * D + chan] = x;
+              rec[(size_t)cc * D + chan] = x[e];
             }
           }
         }
       }
       if (!whole)
-        tree_publish<__nv_bfloat16, D, NC, SM_THREADS>(p, cut, sq.pre, pc.b, pc.h, N, tid, merge_flag, sWarp,
+        tree_publish<__nv_bfloat16, D, NC, C::SM>(p, cut, sq.pre, pc.b, pc.h, N, tid, merge_flag, sWarp,
                                                        sm_sync);
       sm_sync();   // shared words are free for the next piece
       base += 2 * n * NSRC;
@@ -815,21 +870,21 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   __syncthreads();
   if (*abort_flag) {
     // no role may have awaited the last copies and products: let them finish
-    if (warp == PRODUCER_WARP && lane == 0) {
+    if (warp == C::PRODUCER_WARP && lane == 0) {
       const int issued = *sm_issued, nring = Q4 ? nraw : nslots;
       uint64_t* ring_full = Q4 ? raw_full : full;
       for (int g = max(0, issued - nring); g < issued; ++g)
         (void)mbar_wait_bounded(&ring_full[g % nring], (uint32_t)(g / nring) & 1u, kDrainLimitNs);
     }
-    if ((warp == QK_WARP || warp == PV_WARP) && elect_one()) {
-      mma_commit(&drain[warp - QK_WARP]);
-      (void)mbar_wait_bounded(&drain[warp - QK_WARP], 0, kDrainLimitNs);
+    if ((warp == C::QK_WARP || warp == C::PV_WARP) && elect_one()) {
+      mma_commit(&drain[warp - C::QK_WARP]);
+      (void)mbar_wait_bounded(&drain[warp - C::QK_WARP], 0, kDrainLimitNs);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
   }
-  if (warp == QK_WARP) {
+  if (warp == C::QK_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -839,7 +894,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
 template <int D, int NSRC, int NC, bool Q4>
 void size_tc(int B, TreePlan* plan) {
   using C = TcCfg<D, NSRC, NC, Q4>;
-  const int fixed = (int)(C::FIXED + C::NPB * C::P_BYTES + tree_seqs_bytes(B) + 64);
+  const int fixed = 1024 + C::ring_off(B) + C::OVERRUN;
   int left = SMEM_LIMIT - fixed;
   plan->raw_slots = 0;
   if (Q4) {
@@ -855,8 +910,7 @@ void size_tc(int B, TreePlan* plan) {
   int slots = left > 0 ? left / C::SLOT : 0;
   if (slots > MAX_SLOTS) slots = MAX_SLOTS;
   if (Q4) slots = slots / (DQ_THREADS / DQ_GROUP) * (DQ_THREADS / DQ_GROUP);
-  // the block past the last slot's end lies in Q and P
-  if (slots < 2 * NSRC || C::OVERRUN > C::Q_BYTES + C::NPB * C::P_BYTES) slots = 0;
+  if (slots < 2 * NSRC) slots = 0;
   plan->slots = slots;
   plan->smem_bytes = (size_t)fixed + (size_t)slots * C::SLOT + (size_t)plan->raw_slots * C::RAW;
 }
