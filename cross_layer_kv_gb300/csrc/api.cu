@@ -29,6 +29,7 @@ struct fkv_ctx {
   std::vector<int> window;                 // sliding window per layer (0: full attention)
   std::vector<char> q4;                    // layer cache holds 4-bit records
   std::vector<int> ring;                   // > 0: the layer's caches are rings of that many rows
+  std::vector<fkv::TileMaps> maps[2];      // tensor maps of the bound bf16 K, V planes (tree attention)
 };
 
 namespace {
@@ -62,6 +63,18 @@ fkv_status check_config(const fkv_config* c) {
   if (c->head_dim != 64 && c->head_dim != 80 && c->head_dim != 96 && c->head_dim != 128)
     return FKV_ERR_UNSUPPORTED;
   return FKV_OK;
+}
+
+// Tensor maps of a layer's planes, remade whenever its buffers or rows change.
+void remake_maps(fkv_ctx* c, int layer) {
+  for (int kv = 0; kv < 2; ++kv) {
+    void* ptr = kv ? c->v[layer] : c->k[layer];
+    fkv::TileMaps& m = c->maps[kv][layer];
+    m.valid = false;
+    if (!ptr || c->q4[layer] || c->cfg.dtype != FKV_BF16) continue;
+    const int rows = c->ring[layer] > 0 ? c->ring[layer] : c->cfg.max_seq;
+    fkv::tile_maps(&m, ptr, c->cfg.head_dim, rows, (long long)c->cfg.batch * c->cfg.num_kv_heads);
+  }
 }
 
 // Resolve the cache / weight sources of a call.  nsrc = 1 or 2.
@@ -120,8 +133,9 @@ fkv_status resolve_sources_impl(const fkv_ctx* c, int layer, int mode, const voi
 // FKV_ERR_UNSUPPORTED (the sources of a call are read at the same rows).
 fkv_status resolve_sources(const fkv_ctx* c, int layer, int mode, const void* k[2],
                            const void* v[2], const float* a[2], const float* b[2], int* nsrc,
-                           int* q4, int* ring) {
-  int src[4];
+                           int* q4, int* ring, int* layers = nullptr) {
+  int own[4];
+  int* src = layers ? layers : own;   // source layers: K first, K second, V first, V second
   const fkv_status s = resolve_sources_impl(c, layer, mode, k, v, a, b, nsrc, src);
   if (s != FKV_OK) return s;
   int nq = 0, nt = 0, r = -1;
@@ -169,6 +183,7 @@ fkv::TreeArgs tree_args(const fkv_ctx* c, int T) {
   t.max_seq = c->cfg.max_seq;
   t.head_dim = c->cfg.head_dim;
   t.T = T;
+  t.device = c->device;
   t.is_f32 = c->cfg.dtype == FKV_F32;
   t.num_ctas = c->cfg.decode_ctas;
   t.softmax_scale = c->scale;
@@ -279,6 +294,7 @@ fkv_status fkv_create(const fkv_config* cfg, fkv_ctx** out) {
   c->window.assign(cfg->num_layers + 1, 0);
   c->q4.assign(cfg->num_layers + 1, 0);
   c->ring.assign(cfg->num_layers + 1, 0);
+  for (auto& m : c->maps) m.assign(cfg->num_layers + 1, fkv::TileMaps{});
   c->lite_src[0].assign(cfg->num_layers + 1, c->n);  // K^n
   c->lite_src[1].assign(cfg->num_layers + 1, 1);     // V^1
   c->fused_src[0].assign(cfg->num_layers + 1, 1);
@@ -317,6 +333,7 @@ fkv_status fkv_bind_layer_cache(fkv_ctx* c, int layer, void* k, void* v) {
   c->k[layer] = k;
   c->v[layer] = v;
   c->q4[layer] = 0;
+  remake_maps(c, layer);
   return FKV_OK;
 }
 
@@ -379,6 +396,7 @@ fkv_status fkv_set_ring_rows(fkv_ctx* c, int layer, int rows) {
   if (!c || layer < 1 || layer > c->cfg.num_layers) return FKV_ERR_INVALID_ARG;
   if (rows < 0 || rows > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   c->ring[layer] = rows == c->cfg.max_seq ? 0 : rows;
+  remake_maps(c, layer);
   return FKV_OK;
 }
 
@@ -501,9 +519,13 @@ fkv_status fkv_tree_attn(fkv_ctx* c, const void* q, int layer, int mode, const i
   if (!c || !on_device(c)) return FKV_ERR_INVALID_ARG;
   if (T < 1 || T > kTreeNodes || T > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   fkv::TreeArgs t = tree_args(c, T);
-  int q4 = 0, ring = 0, nsrc = 0;
-  fkv_status s = resolve_sources(c, layer, mode, t.k, t.v, t.a, t.b, &nsrc, &q4, &ring);
+  int q4 = 0, ring = 0, nsrc = 0, src[4];
+  fkv_status s = resolve_sources(c, layer, mode, t.k, t.v, t.a, t.b, &nsrc, &q4, &ring, src);
   if (s != FKV_OK) return s;
+  for (int i = 0; i < 2; ++i) {
+    t.k_maps[i] = &c->maps[0][src[i]];   // (entry 0 where there is no second source)
+    t.v_maps[i] = &c->maps[1][src[2 + i]];
+  }
   t.window = c->window[layer];
   if (ring > 0) {
     // every position that a node may see has to be in the ring still, with
@@ -572,6 +594,7 @@ fkv_status fkv_reorder_seqs(fkv_ctx* c, const int32_t* src, const int32_t* seq_l
   a.batch = c->cfg.batch;
   a.kv_heads = c->cfg.num_kv_heads;
   a.max_seq = c->cfg.max_seq;
+  a.device = c->device;
   return for_bound_planes(c, [&](const fkv::MoveTable& tb) {
     return fkv::reorder_launch(tb, a, c->num_sms, static_cast<cudaStream_t>(stream));
   });

@@ -277,8 +277,8 @@ cudaError_t compact_launch(const MoveTable& tb, CompactArgs a, cudaStream_t stre
 
 cudaError_t reorder_launch(const MoveTable& tb, const ReorderArgs& a, int num_sms, cudaStream_t stream) {
   const size_t smem = kReorderSmem + (size_t)a.batch * 6 * sizeof(int);
-  cudaError_t e =
-      cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static KernelReady ready;
+  const cudaError_t e = ready.check(reorder_kernel, a.device, kReorderSmem + 1024 * 6 * (int)sizeof(int), 32, 0);
   if (e != cudaSuccess) return e;
   return launch_pdl(reorder_kernel, dim3(num_sms), dim3(32), smem, stream, tb, a);
 }

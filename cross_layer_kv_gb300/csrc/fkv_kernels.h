@@ -2,6 +2,7 @@
 // library; the public ABI is include/fusedkv.h).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -127,8 +128,44 @@ cudaError_t prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_wide_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_fused_wide_launch(const PrefillArgs& a, cudaStream_t stream);
 
+// What a kernel needs once per device before its first launch: its dynamic
+// shared memory raised to `smem` bytes and, for kernels that split their
+// registers by warpgroup, a launch allocation of at least `regs` registers
+// (cudaErrorNotSupported otherwise).  One object per kernel; later calls are
+// one load.
+struct KernelReady {
+  std::atomic<unsigned long long> devices{0};
+  template <typename Kern>
+  cudaError_t check(Kern kern, int device, int smem, int threads, int regs) {
+    const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
+    if (bit && (devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (regs > 0) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if ((long long)fa.numRegs * threads < regs) return cudaErrorNotSupported;
+    }
+    devices.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+  }
+};
+
+// Tensor maps of one bound bf16 plane as the tree kernels read it (boxes of a
+// whole key tile and of a ragged tile's rows), made when the buffer is bound.
+struct TileMaps {
+  alignas(128) unsigned char full[128];
+  alignas(128) unsigned char tail[128];
+  bool valid;
+};
+bool tile_maps(TileMaps* m, const void* base, int D, int rows, long long planes);
+
 // One fkv_tree_attn call, after host validation.
 struct TreeArgs {
+  const TileMaps* k_maps[2];   // of the sources (bf16 caches)
+  const TileMaps* v_maps[2];
+  int device;
   const void* k[2];          // second source null unless fused
   const void* v[2];
   const float* a[2];         // null for vanilla and lite
@@ -190,7 +227,7 @@ struct ReorderArgs {
   const int32_t* seq_lens;   // [B]
   int* status;
   const unsigned long long* wait_limit;
-  int batch, kv_heads, max_seq;
+  int batch, kv_heads, max_seq, device;
 };
 
 constexpr int kMaxAccepted = 128;   // rows a sequence may compact in one call

@@ -1,8 +1,53 @@
 // Host side of fkv_tree_attn: which kernel runs a call, its workspace, and the
 // parameters that the kernels share.
+#include "tc_device.cuh"
 #include "tree_common.cuh"
 
 namespace fkv {
+namespace {
+
+// The tensor-core kernels: bf16 and 4-bit caches.
+bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
+  if (a.is_f32) return false;
+  const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
+  plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim == 128))) plan->rows = 64;
+  plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
+  switch (a.head_dim) {
+    case 64: tree_tc_size_64(a, plan); break;
+    case 80: tree_tc_size_80(a, plan); break;
+    case 96: tree_tc_size_96(a, plan); break;
+    default: tree_tc_size_128(a, plan); break;
+  }
+  if (plan->slots == 0) return false;
+  // one CTA an SM over ranges and row tiles; the device takes fewer ranges
+  // where there are fewer key tiles
+  plan->ranges = a.num_ctas > 0 ? a.num_ctas : num_sms / plan->row_tiles > 0 ? num_sms / plan->row_tiles : 1;
+  plan->tensor = true;
+  return true;
+}
+
+cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+  switch (a.head_dim) {
+    case 64: return tree_tc_run_64(p, a, plan, stream);
+    case 80: return tree_tc_run_80(p, a, plan, stream);
+    case 96: return tree_tc_run_96(p, a, plan, stream);
+    default: return tree_tc_run_128(p, a, plan, stream);
+  }
+}
+
+}  // namespace
+
+// Tensor maps of a bf16 plane: `planes` times `rows` rows of D elements.
+bool tile_maps(TileMaps* m, const void* base, int D, int rows, long long planes) {
+  static_assert(sizeof(CUtensorMap) == sizeof(m->full) && alignof(TileMaps) >= alignof(CUtensorMap), "tensor map");
+  const size_t plane = (size_t)rows * D * 2;
+  m->valid = make_map_box(reinterpret_cast<CUtensorMap*>(m->full), base, D, rows, planes, plane, 64,
+                          kTreeKeyTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+             make_map_box(reinterpret_cast<CUtensorMap*>(m->tail), base, D, rows, planes, plane, 64,
+                          kTreeTailRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  return m->valid;
+}
 
 cudaError_t tree_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
   if (!tree_tc_plan(a, num_sms, plan)) tree_simt_plan(a, num_sms, plan);

@@ -22,11 +22,19 @@
 namespace fkv {
 
 constexpr int kTreeMaxNodes = 128;
+constexpr int kTreeKeyTile = 128;    // keys per tile of the tensor-core kernels
+constexpr int kTreeTailRows = 16;    // rows of the boxes of a ragged tile
 
 struct TreeParams;
-bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
-cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
-                           cudaStream_t stream);
+// tree_tc_impl.cuh, one unit per head dimension
+void tree_tc_size_64(const TreeArgs& a, TreePlan* plan);
+void tree_tc_size_80(const TreeArgs& a, TreePlan* plan);
+void tree_tc_size_96(const TreeArgs& a, TreePlan* plan);
+void tree_tc_size_128(const TreeArgs& a, TreePlan* plan);
+cudaError_t tree_tc_run_64(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
+cudaError_t tree_tc_run_80(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
+cudaError_t tree_tc_run_96(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
+cudaError_t tree_tc_run_128(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
 void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
 cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
                              cudaStream_t stream);

@@ -236,28 +236,30 @@ __global__ void __launch_bounds__(NT) tree_simt_kernel(const TreeParams p) {
 }
 
 template <int FMT, int D, int NSRC, bool WGT>
-cudaError_t launch_simt(const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+cudaError_t launch_simt(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
   auto kern = tree_simt_kernel<FMT, D, NSRC, WGT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)plan.smem_bytes);
+  static KernelReady ready;
+  const cudaError_t e = ready.check(kern, a.device, 232448, NT, 0);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(NT), plan.smem_bytes, stream, p);
 }
 
 template <int FMT, int D>
-cudaError_t launch_simt_src(const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
-  if (p.k[1]) return launch_simt<FMT, D, 2, true>(p, plan, stream);
-  if (p.a[0]) return launch_simt<FMT, D, 1, true>(p, plan, stream);
-  return launch_simt<FMT, D, 1, false>(p, plan, stream);
+cudaError_t launch_simt_src(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
+                            cudaStream_t stream) {
+  if (p.k[1]) return launch_simt<FMT, D, 2, true>(p, a, plan, stream);
+  if (p.a[0]) return launch_simt<FMT, D, 1, true>(p, a, plan, stream);
+  return launch_simt<FMT, D, 1, false>(p, a, plan, stream);
 }
 
 template <int FMT>
-cudaError_t launch_simt_dim(const TreeParams& p, int D, const TreePlan& plan, cudaStream_t stream) {
-  switch (D) {
-    case 64: return launch_simt_src<FMT, 64>(p, plan, stream);
-    case 80: return launch_simt_src<FMT, 80>(p, plan, stream);
-    case 96: return launch_simt_src<FMT, 96>(p, plan, stream);
-    default: return launch_simt_src<FMT, 128>(p, plan, stream);
+cudaError_t launch_simt_dim(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
+                            cudaStream_t stream) {
+  switch (a.head_dim) {
+    case 64: return launch_simt_src<FMT, 64>(p, a, plan, stream);
+    case 80: return launch_simt_src<FMT, 80>(p, a, plan, stream);
+    case 96: return launch_simt_src<FMT, 96>(p, a, plan, stream);
+    default: return launch_simt_src<FMT, 128>(p, a, plan, stream);
   }
 }
 
@@ -276,9 +278,9 @@ void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
 
 cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
                              cudaStream_t stream) {
-  if (a.is_f32) return launch_simt_dim<kTreeF32>(p, a.head_dim, plan, stream);
-  if (a.q4) return launch_simt_dim<kTreeQ4>(p, a.head_dim, plan, stream);
-  return launch_simt_dim<kTreeBf16>(p, a.head_dim, plan, stream);
+  if (a.is_f32) return launch_simt_dim<kTreeF32>(p, a, plan, stream);
+  if (a.q4) return launch_simt_dim<kTreeQ4>(p, a, plan, stream);
+  return launch_simt_dim<kTreeBf16>(p, a, plan, stream);
 }
 
 }  // namespace fkv

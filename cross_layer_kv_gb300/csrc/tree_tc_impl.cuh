@@ -26,8 +26,8 @@
 //    tensor memory), another O += V_j^T P_j: an MMA of these sizes costs its
 //    issuer 40 to 48 clocks at 16 to 64 columns (64 at 128), as long as the
 //    tensor pipe, so one issuer for both was the bound of small trees;
-//  * two or four softmax warpgroups take every second tile or a part of the
-//    columns (TcCfg): scores from tensor memory, P to shared memory as an MN-major operand (a thread writes its
+//  * two or four softmax warpgroups take a part of the columns each: scores
+//    from tensor memory, P to shared memory as an MN-major operand (a thread writes its
 //    key's columns, 16 bytes at a time, without bank conflicts).
 // 4-bit caches: the producer copies a tile's records (one contiguous run) to a
 // second ring, and two more warpgroups dequantise them into the slots, two
@@ -42,21 +42,26 @@
 // value rows that nobody sees are zeroed in shared memory, since 0 * NaN is
 // no 0.  A drafted value row that is not finite is zeroed too and its score
 // made NaN, so that it stays with the nodes that see it.
+#pragma once
+
 #include <cfloat>
 #include <cstring>
+#include <type_traits>
 
 #include "tc_device.cuh"
 #include "tree_common.cuh"
 
 namespace fkv {
+
+// (an unnamed namespace: each unit has its own head dimension's kernels)
 namespace {
 
-constexpr int KT = 128;               // keys per tile
+constexpr int KT = kTreeKeyTile;
 constexpr int DQ_THREADS = 256;       // dequantising threads (4-bit caches)
 constexpr int DQ_GROUP = 64;          // of them that share a tile: four tiles are in work at a time
 constexpr int MAX_RAW = 12;           // slots of records
 constexpr int MAX_SLOTS = 12;
-constexpr int TAIL_ROWS = 16;         // rows of the boxes of a ragged tile
+constexpr int TAIL_ROWS = kTreeTailRows;
 constexpr int SMEM_LIMIT = 232448;
 constexpr int SWB = 128;              // bytes of a swizzled row: 64 channels or columns
 constexpr int SWC = SWB / 2;
@@ -72,29 +77,29 @@ struct TcCfg {
   // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
   // past its end into what follows (rows that are not used)
   static constexpr int OVERRUN = Q4 ? 0 : (2 - CB) * KT * SWB;   // (the records follow 4-bit slots)
-  // Softmax warpgroups.  Up to 32 columns: two, each with every second tile,
-  // its own references, sums and accumulators (joined when a piece ends), so
-  // that one's waits overlap the other's work.  More columns: each warpgroup
-  // takes a part of the columns of every tile.
-  static constexpr int TS = NC <= 32 ? 2 : 1;            // tiles in work
-  static constexpr int CS = NC <= 32 ? 1 : Q4 ? 2 : 4;   // column parts
-  static constexpr int NWG = TS * CS;
+  // Softmax warpgroups, each with a part of the columns of every tile.  Four
+  // from 64 columns on, where they hide each other's waits (332M fused, T = 64:
+  // 202 us, with two 249); two below, which leaves them more registers and
+  // shorter barriers, and for 4-bit caches, whose dequantising warpgroups take
+  // the other threads.  (Two warpgroups with every second tile each, references
+  // and accumulators of their own, gained 3% at 16 columns and lost 20% over
+  // 4-bit caches.)
+  static constexpr int NWG = NC <= 32 || Q4 ? 2 : 4;
   static constexpr int SM = NWG * 128;                   // softmax threads
-  static constexpr int HC = NC / CS;                     // columns of a softmax thread
-  static constexpr int EC = NC / NWG;                    // columns a warpgroup writes out
+  static constexpr int HC = NC / NWG;                    // columns of a softmax thread
+  static constexpr int CH = HC < 16 ? HC : 16;           // of them in registers at a time
   static constexpr int PRODUCER_WARP = 4 * NWG, QK_WARP = PRODUCER_WARP + 1, PV_WARP = PRODUCER_WARP + 2;
   static constexpr int DQ_WARP = PRODUCER_WARP + 4;      // the first of the dequantising warps
-  static constexpr int TMEM_USED = (2 + TS * NSRC) * NC;
+  static constexpr int TMEM_USED = (2 + NSRC) * NC;
   static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
   static_assert(TMEM_USED <= 512, "tensor memory");
   // barriers and words, then the arrays of floats and masks
   static constexpr int BAR_BYTES = ((2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 11 * 8 + 6 * 4 + 127) / 128 * 128;
-  static constexpr int ARRAY_BYTES = NC * 4 * (2 * TS + 2 + 4 * TS) + kTreeMaxNodes * (16 + 4 + NW * 4);
-  // two P buffers where warpgroups take whole tiles, or where at least five
-  // tile slots remain beside them
+  static constexpr int ARRAY_BYTES = NC * 4 * 8 + kTreeMaxNodes * (16 + 4 + NW * 4);
+  // two P buffers where at least five tile slots remain beside them
   static constexpr int NPB =
-      TS == 2 || (SMEM_LIMIT - 3072 - Q_BYTES - BAR_BYTES - ARRAY_BYTES - OVERRUN - 2 * P_BYTES) / SLOT >= 5 ? 2 : 1;
+      (SMEM_LIMIT - 3072 - Q_BYTES - BAR_BYTES - ARRAY_BYTES - OVERRUN - 2 * P_BYTES) / SLOT >= 5 ? 2 : 1;
   static constexpr int REF_OFF = Q_BYTES + NPB * P_BYTES + BAR_BYTES;
   __host__ __device__ static constexpr int ring_off(int B) {
     return (REF_OFF + ARRAY_BYTES + (int)tree_seqs_bytes(B) + 1023) / 1024 * 1024;
@@ -154,6 +159,17 @@ __device__ __forceinline__ bool any_of(int id, int count, bool x) {
   return r != 0;
 }
 
+// A wait that did not succeed at once: until the phase completes, another role
+// gives up, or the limit passes.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                     volatile int* abort_flag, int* status) {
+  if (*abort_flag) return false;
+  if (mbar_wait_bounded(bar, parity, limit)) return true;
+  *abort_flag = 1;
+  flag_status(status, kDevTimeout);
+  return false;
+}
+
 // The 128 threads of softmax warpgroup wg.
 __device__ __forceinline__ void wg_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); }
 
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots,
                    const int nraw) {
   using C = TcCfg<D, NSRC, NC, Q4>;
-  constexpr int CB = C::CB, HC = C::HC, NW = C::NW, NPB = C::NPB, TS = C::TS, CS = C::CS;
+  constexpr int CB = C::CB, HC = C::HC, CH = C::CH, NW = C::NW, NPB = C::NPB;
   auto sm_sync = [] { sm_barrier<C::SM>(); };
   // Everything before the rings lies at offsets known at compile time, from a
   // pointer that the compiler sees is shared memory: addresses cost no
@@ -189,12 +205,12 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
   int* merge_flag = sm_issued + 1;
   int* sm_span = merge_flag + 1;                               // [2] least and largest depth
-  float* sRef = reinterpret_cast<float*>(smem + C::REF_OFF);   // [TS][NC] negated reference
-  float* sAlpha = sRef + TS * NC;                              // [TS][NC] rescale, then weight
-  int* sDepth = reinterpret_cast<int*>(sAlpha + TS * NC);      // [NC] depth of the column's node
+  float* sRef = reinterpret_cast<float*>(smem + C::REF_OFF);   // [NC] negated reference
+  float* sAlpha = sRef + NC;                                   // [NC] rescale, then weight
+  int* sDepth = reinterpret_cast<int*>(sAlpha + NC);           // [NC] depth of the column's node
   int* sNode = sDepth + NC;                                    // [NC] node of the column, -1: none
-  float* sWarp = reinterpret_cast<float*>(sNode + NC);         // [TS][4][NC]
-  unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sWarp + TS * 4 * NC);   // [nodes][2]
+  float* sWarp = reinterpret_cast<float*>(sNode + NC);         // [4][NC]
+  unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sWarp + 4 * NC);   // [nodes][2]
   int* sNodeDepth = reinterpret_cast<int*>(sMask + 2 * kTreeMaxNodes);   // [nodes]
   uint32_t* sVis = reinterpret_cast<uint32_t*>(sNodeDepth + kTreeMaxNodes);   // [nodes][NW]
   const TreeSeqs sq = tree_seqs(reinterpret_cast<int*>(sVis + kTreeMaxNodes * NW), p.B);
@@ -215,7 +231,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     mbar_init(q_ready, C::SM / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], CS * 4);
+      mbar_init(&p_full[i], C::SM / 32);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&o_done[i], 1);
     mbar_init(&drain[0], 1);
@@ -243,11 +259,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   if (active) walk.begin(cut, sq.pre, p.B, p.H, blockIdx.x);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(bar, parity, wlim)) return true;
-    *abort_flag = 1;
-    flag_status(p.status, kDevTimeout);
-    return false;
+    if (wlim != 0 && mbar_try_wait(bar, parity)) return true;
+    return wait_on(bar, parity, wlim, abort_flag, p.status);
   };
   // the value products of tile t are done
   auto products = [&](int t) { return wait(&o_done[t & 3], (uint32_t)(t >> 2) & 1u); };
@@ -462,8 +475,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
             tc_fence_after();
             if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
-              const uint32_t d = tmem + (2 + (TS == 2 ? j & 1 : 0) * NSRC + src) * NC;
-              mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i >= TS ? 1u : 0u);
+              const uint32_t d = tmem + (2 + src) * NC;
+              mma_bf16(d, a.at(0), b.at(0), IDESC_PV, i > 0 ? 1u : 0u);
               if (ks == KT / 16) {
 #pragma unroll
                 for (int k = 1; k < KT / 16; ++k)
@@ -488,12 +501,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     // ---------------- softmax ----------------
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
-    const int ts = wg / CS;                // which tiles (TS == 2: those of this parity)
-    const int c0 = (wg % CS) * HC;         // first column
-    float* ref = sRef + ts * NC;
-    float* alpha = sAlpha + ts * NC;
-    float* part = sWarp + ts * 4 * NC;
-    const uint32_t t_acc = tmem + ((uint32_t)(quarter * 32) << 16) + (2 + ts * NSRC) * NC;   // its accumulators
+    const int c0 = wg * HC;                // first column
     const int chan = Q4 ? (key & ~7) | (key & 1) << 2 | (key >> 1 & 3) : key;   // channel of row `key` of V^T
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
     auto fmaxop = [](float a, float b) { return fmaxf(a, b); };
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         sm_span[0] = kTreeMaxNodes;
         sm_span[1] = 0;
       }
-      if (tid < TS * NC) sRef[tid] = FLT_MAX;
+      if (tid < NC) sRef[tid] = FLT_MAX;
       sm_sync();
       if (tid < NC) {
         const int i = sNode[tid];
@@ -589,6 +597,16 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       sm_sync();
       const int least = sm_span[0], most = sm_span[1];
 
+      // the piece's tiles that need masks: from `tail` on (drafted rows, a ragged
+      // end), the ragged one before a ring's end, and up to `edge` (rows that the
+      // window of a deep node has left: positions up to P + most - window)
+      const int tA = (s.cntA + KT - 1) / KT;
+      const int kept = P - s.start;   // committed rows
+      const int tail = (kept < s.cntA ? kept / KT : tA + (kept - s.cntA) / KT) - pc.k0;
+      const int seam = s.cntB > 0 ? tA - 1 - pc.k0 : -1;
+      const int gone = p.window > 0 ? P + most - p.window - s.start : -1;   // last such row, from the start
+      const int edge = gone < 0 ? 0 : (gone < s.cntA ? gone / KT + 1 : tA + (gone - s.cntA) / KT + 1) - pc.k0;
+
       float l[HC];
 #pragma unroll
       for (int c = 0; c < HC; ++c) l[c] = 0.f;
@@ -598,29 +616,30 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       // threads, and all leave together at the piece's end.
       for (int i = 0; i < n; ++i) {
         const int j = jt + i;
-        if (TS == 2 && (j & 1) != ts) continue;
-        const TreeTile t = tree_tile(p, s, pc.k0 + i, KT);
-        if (ok && !__all_sync(0xffffffffu, wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u))) ok = false;
+        ok = ok && wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
+        __syncwarp();
         tc_fence_after();
         const uint32_t t_s = t_lane + (j & 1) * NC;
-        const bool edge = p.window > 0 && t.pos <= P + most - p.window;
-        const bool masked = t.cnt < KT || t.pos + t.cnt > P || edge;   // uniform over the tile's threads
-        const int q = t.pos + key - P;   // >= 0: drafted node q
+        // uniform over the CTA: rows that some column does not see
+        const bool masked = i >= tail || i == seam || i < edge;
+        TreeTile t{0, 0, KT};
+        int q = 0;   // >= 0: drafted node q; else the key's distance from the drafted rows
+        if (masked) {
+          t = tree_tile(p, s, pc.k0 + i, KT);
+          q = t.pos + key - P;
+        }
         bool poison = false;
         if (masked) {
           // wait for the tile's values: unseen rows are zeroed, rows that are
           // not finite are noted
           // (once the products of the tile before are done, the slots' phases
           // before the awaited ones are known to be over)
-          if (i > 0 && ok &&
-              !__all_sync(0xffffffffu, products(j - 1)))
-            ok = false;
+          ok = ok && (i == 0 || products(j - 1));
           const int g0 = base + v_slot(i, n) * NSRC;
 #pragma unroll
           for (int src = 0; src < NSRC; ++src) {
             const int g = g0 + src;
-            if (ok && !__all_sync(0xffffffffu, wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u)))
-              ok = false;
+            ok = ok && wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u);
           }
           bool seen = false;
           if (key < t.cnt) {
@@ -645,9 +664,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
               }
             }
           }
-          if (CS > 1) sm_sync();   // the other parts' warpgroups have looked too
-          else wg_sync(wg);
-          if (wg % CS == 0 && ok && (!seen || poison) && key < (t.cnt + 15) / 16 * 16) {
+          sm_sync();   // every warpgroup has looked
+          if (wg == 0 && ok && (!seen || poison) && key < (t.cnt + 15) / 16 * 16) {
 #pragma unroll 1
             for (int src = 0; src < NSRC; ++src) {
               uint8_t* v = slot_ptr((g0 + src) % nslots);
@@ -657,71 +675,71 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
             }
           }
         }
-        // this key's scores, -inf where a column does not see it
-        float sv[HC];
-        auto scores = [&]() {
-          if constexpr (HC == 16) {
-            tmem_ld16(t_s, sv);
-          } else {
-#pragma unroll
-            for (int c = 0; c < HC; c += 32) tmem_ld32(t_s + c, sv + c);
-          }
+        // CH of this key's scores from column c0 + c on, -inf where a column does
+        // not see it.  They are read again from tensor memory rather than kept:
+        // 32 a thread beside its 32 sums spilled.
+        float sv[CH];
+        auto scores = [&](int c) {
+          if constexpr (CH == 8) tmem_ld8(t_s + c, sv);
+          else tmem_ld16(t_s + c, sv);
           tmem_wait_ld();
           if (masked) {
-            uint32_t vis[(HC + 31) / 32];
-#pragma unroll
-            for (int w = 0; w < (HC + 31) / 32; ++w)
-              vis[w] = (key >= t.cnt ? 0u : q >= 0 ? sVis[q * NW + c0 / 32 + w] : ~0u) >> (c0 & 31);
+            const int first = c0 + c;
+            const uint32_t vis =
+                (key >= t.cnt ? 0u : q >= 0 ? sVis[q * NW + first / 32] : ~0u) >> (first & 31);
             const int reach = q < 0 && p.window > 0 ? q + p.window : kTreeMaxNodes;   // depths below it see the key
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-              const bool see = (vis[c >> 5] >> (c & 31) & 1u) && sDepth[c0 + c] < reach;
-              sv[c] = !see ? -INFINITY : poison ? NAN : sv[c];
+            for (int e = 0; e < CH; ++e) {
+              const bool see = (vis >> e & 1u) && sDepth[first + e] < reach;
+              sv[e] = !see ? -INFINITY : poison ? NAN : sv[e];
             }
           }
         };
-        // x = score * scale - reference, and the largest of them
-        auto shift = [&]() {
+        // score * scale - reference, and the largest of them
+        auto shift = [&](int c) {
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < HC; c += 4) {
-            const float4 r = *reinterpret_cast<const float4*>(ref + c0 + c);   // negated references
+          for (int e = 0; e < CH; e += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(sRef + c0 + c + e);   // negated references
             float x0 = r.x, x1 = r.y, x2 = r.z, x3 = r.w;
-            fma2(x0, x1, sv[c], sv[c + 1], p.scale_log2, p.scale_log2);
-            fma2(x2, x3, sv[c + 2], sv[c + 3], p.scale_log2, p.scale_log2);
-            sv[c] = x0; sv[c + 1] = x1; sv[c + 2] = x2; sv[c + 3] = x3;
+            fma2(x0, x1, sv[e], sv[e + 1], p.scale_log2, p.scale_log2);
+            fma2(x2, x3, sv[e + 2], sv[e + 3], p.scale_log2, p.scale_log2);
+            sv[e] = x0; sv[e + 1] = x1; sv[e + 2] = x2; sv[e + 3] = x3;
             top[0] = fmax3f(top[0], x0, x1);
             top[1] = fmax3f(top[1], x2, x3);
           }
           return fmaxf(top[0], top[1]);
         };
-        scores();
-        // a warpgroup's first tile of a piece takes its maxima as references;
-        // later ones keep them unless a score exceeds its own by more than the slack
-        const bool first = i < TS;
+        // the first tile of a piece takes its maxima as references; later ones
+        // keep them unless a score exceeds its own by more than the slack
+        const bool first = i == 0;
         bool grow = first;
-        if (!grow) grow = any_of(2 + wg, 128, shift() > SLACK);
+        if (!first) {
+          float over = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < HC; c += CH) {
+            scores(c);
+            over = fmaxf(over, shift(c));
+          }
+          grow = any_of(2 + wg, 128, over > SLACK);
+        }
         if (grow) {
-          if (!first) scores();
-          constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
-          for (int b0 = 0; b0 < HC; b0 += RN) {
-            float v[RN];
-#pragma unroll
-            for (int c = 0; c < RN; ++c) v[c] = sv[b0 + c];
-            const float m = reduce_scatter<RN>(v, lane, fmaxop);
-            if (lane < RN) part[quarter * NC + c0 + b0 + lane] = m;
+          for (int c = 0; c < HC; c += CH) {
+            scores(c);
+            const float m = reduce_scatter<CH>(sv, lane, fmaxop);
+            if (lane < CH) sWarp[quarter * NC + c0 + c + lane] = m;
           }
           wg_sync(wg);
           if ((tid & 127) < HC) {
             const int c = c0 + (tid & 127);
-            const float m = fmaxf(fmaxf(part[c], part[NC + c]), fmaxf(part[2 * NC + c], part[3 * NC + c]));
-            const float old = -ref[c], top = fmaxf(old, m * p.scale_log2);
-            alpha[c] = fast_exp2(old - top);
-            ref[c] = -top;
+            const float m = fmaxf(fmaxf(sWarp[c], sWarp[NC + c]), fmaxf(sWarp[2 * NC + c], sWarp[3 * NC + c]));
+            const float old = -sRef[c], top = fmaxf(old, m * p.scale_log2);
+            sAlpha[c] = fast_exp2(old - top);
+            sRef[c] = -top;
           }
           // O holds every product before this tile once the last one is done
-          if (!first && ok && !__all_sync(0xffffffffu, products(j - TS))) ok = false;
+          ok = ok && (first || products(j - 1));
           tc_fence_after();
           wg_sync(wg);
           if (!first) {
@@ -730,12 +748,12 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
               float al[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                al[e] = alpha[c0 + c + e];
+                al[e] = sAlpha[c0 + c + e];
                 l[c + e] *= al[e];
               }
 #pragma unroll
               for (int src = 0; src < NSRC; ++src) {
-                const uint32_t to = t_acc + src * NC + c0 + c;
+                const uint32_t to = t_lane + (2 + src) * NC + c;
                 float o[8];
                 tmem_ld8(to, o);
                 tmem_wait_ld();
@@ -746,28 +764,33 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
             }
             tmem_wait_st();
           }
-          shift();
         }
 
         // P of this key: 2^x, bf16
         const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
-        if (pj >= 0 && ok && !__all_sync(0xffffffffu, products(pj)))
-          ok = false;
+        ok = ok && (pj < 0 || products(pj));
+        __syncwarp();
         uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
 #pragma unroll
-        for (int c = 0; c < HC; c += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float e0 = fast_exp2(sv[c + e]);
-            const float e1 = fast_exp2(sv[c + e + 1]);
-            add2(l[c + e], l[c + e + 1], e0, e1);
-            const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
-            w[e / 2] = *reinterpret_cast<const uint32_t*>(&v2);
+        for (int c = 0; c < HC; c += CH) {
+          if (HC > CH || grow) {
+            scores(c);
+            shift(c);
           }
-          const int cc = c0 + c;
-          *reinterpret_cast<uint4*>(pb + (cc >> 6) * KT * SWB + swz128(key, (cc & 63) >> 3)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int h = 0; h < CH; h += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = h; e < h + 8; e += 2) {
+              const float e0 = fast_exp2(sv[e]), e1 = fast_exp2(sv[e + 1]);
+              add2(l[c + e], l[c + e + 1], e0, e1);
+              const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
+              w[(e - h) / 2] = *reinterpret_cast<const uint32_t*>(&v2);
+            }
+            const int cc = c0 + c + h;
+            *reinterpret_cast<uint4*>(pb + (cc >> 6) * KT * SWB + swz128(key, (cc & 63) >> 3)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -777,39 +800,24 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       }
       // the sums of the columns over all keys, and the last products
       const int jl = jt + n - 1;
-      if (ok && !__all_sync(0xffffffffu, products(jl))) ok = false;
+      ok = ok && products(jl);
       if (any_of(1, C::SM, !ok)) break;
       tc_fence_after();
       constexpr int RN = HC < 32 ? HC : 32;
 #pragma unroll
       for (int b0 = 0; b0 < HC; b0 += RN) {
         const float m = reduce_scatter<RN>(l + b0, lane, addop);
-        if (lane < RN) part[quarter * NC + c0 + b0 + lane] = m;
+        if (lane < RN) sWarp[quarter * NC + c0 + b0 + lane] = m;
       }
       sm_sync();
       const bool whole = n == pc.tiles;
       float* rec = p.ws + ((size_t)(2 * blockIdx.x + (pc.first ? 0 : 1)) * p.row_tiles + rt) *
                               tree_record_floats(NC, D);
       if (tid < NC) {
-        // the weights of the accumulators: 2^(reference - top), over the sum
-        // where the piece is its whole unit
-        float L[TS], w[TS], top = -FLT_MAX, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < TS; ++k) {
-          const float* x = sWarp + k * 4 * NC + tid;
-          L[k] = (x[0] + x[NC]) + (x[2 * NC] + x[3 * NC]);
-          top = fmaxf(top, -sRef[k * NC + tid]);
-        }
-#pragma unroll
-        for (int k = 0; k < TS; ++k) {
-          w[k] = L[k] == 0.f ? 0.f : fast_exp2(-sRef[k * NC + tid] - top);
-          sum += L[k] == 0.f ? 0.f : w[k] * L[k];
-        }
-        const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-#pragma unroll
-        for (int k = 0; k < TS; ++k) sAlpha[k * NC + tid] = w[k] * f;
+        const float sum = (sWarp[tid] + sWarp[NC + tid]) + (sWarp[2 * NC + tid] + sWarp[3 * NC + tid]);
+        sAlpha[tid] = sum == 0.f ? 0.f : whole ? 1.f / sum : 1.f;
         if (!whole) {
-          rec[NC * D + tid] = top;
+          rec[NC * D + tid] = -sRef[tid];
           rec[NC * D + NC + tid] = sum;
         }
       }
@@ -821,25 +829,19 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         if (WGT && key < D) bw[src] = p.b[src][(size_t)pc.h * D + chan];
       }
 #pragma unroll 1
-      for (int c = wg * C::EC; c < (wg + 1) * C::EC; c += 8) {
-        float x[8];
+      for (int c = c0; c < c0 + HC; c += 8) {
+        float o[NSRC][8], x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        for (int src = 0; src < NSRC; ++src)
+          tmem_ld8(t_lane - c0 + (2 + src) * NC + c, o[src]);
+        tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < TS; ++k) {
-          float o[NSRC][8];
-#pragma unroll
-          for (int src = 0; src < NSRC; ++src)
-            tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + (2 + k * NSRC + src) * NC + c, o[src]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float w = sAlpha[k * NC + c + e];
-            float y = o[0][e];
-            if constexpr (WGT) y *= bw[0];
-            if constexpr (NSRC == 2) y = fmaf(bw[1], o[1][e], y);
-            x[e] = w == 0.f ? x[e] : fmaf(w, y, x[e]);   // an accumulator without a product is not read
-          }
+        for (int e = 0; e < 8; ++e) {
+          const float w = sAlpha[c + e];
+          float y = o[0][e];
+          if constexpr (WGT) y *= bw[0];
+          if constexpr (NSRC == 2) y = fmaf(bw[1], o[1][e], y);
+          x[e] = w == 0.f ? 0.f : w * y;
         }
         if (key < D) {
 #pragma unroll
@@ -919,86 +921,59 @@ template <int D, int NSRC, bool WGT, int NC, bool Q4>
 cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
   TcMaps maps;
   std::memset(&maps, 0, sizeof(maps));
-  const int rows = a.ring > 0 ? a.ring : a.max_seq;
-  const long long units = (long long)a.batch * a.kv_heads;
-  bool ok = true;
   for (int i = 0; i < 4 && !Q4; ++i) {
+    const TileMaps* m = i < 2 ? a.k_maps[i & 1] : a.v_maps[i & 1];
     if ((i & 1) >= NSRC) continue;
-    const void* ptr = i < 2 ? a.k[i & 1] : a.v[i & 1];
-    ok = ok && make_map_box(&maps.full[i], ptr, D, rows, units, (size_t)rows * D * 2, SWC, KT,
-                            CU_TENSOR_MAP_SWIZZLE_128B);
-    ok = ok && make_map_box(&maps.tail[i], ptr, D, rows, units, (size_t)rows * D * 2, SWC, TAIL_ROWS,
-                            CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!m || !m->valid) return cudaErrorInvalidValue;
+    std::memcpy(&maps.full[i], m->full, sizeof(CUtensorMap));
+    std::memcpy(&maps.tail[i], m->tail, sizeof(CUtensorMap));
   }
-  if (!ok) return cudaErrorInvalidValue;
   using C = TcCfg<D, NSRC, NC, Q4>;
   auto kern = tree_tc_kernel<D, NSRC, WGT, NC, Q4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_bytes);
+  // the softmax warpgroups' larger share of the registers has to fit the launch
+  // allocation, or it would never be granted: refuse instead
+  static KernelReady ready;
+  const cudaError_t e = ready.check(kern, a.device, SMEM_LIMIT, C::THREADS, C::REGS_SPLIT);
   if (e != cudaSuccess) return e;
-  // the softmax warpgroups' larger share has to fit the launch allocation, or
-  // it would never be granted: refuse instead
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs * C::THREADS < C::REGS_SPLIT) return cudaErrorNotSupported;
   return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(C::THREADS), plan.smem_bytes, stream, maps,
                     p, plan.slots, plan.raw_slots);
 }
 
-// Call f with the plan's configuration as integral constants: head dim,
-// sources, columns and whether the caches are 4-bit.
-template <typename F>
-auto dispatch_tc(int D, int nsrc, int rows, bool q4, F f) {
-  auto fmt = [&](auto d, auto ns, auto nc) {
+// Call f with the plan's columns, its sources and whether the caches are 4-bit
+// as integral constants.
+template <int D, typename F>
+auto dispatch_tc(int nsrc, int rows, bool q4, F f) {
+  auto fmt = [&](auto ns, auto nc) {
     // 4-bit caches take at most 64 columns: 128 registers a softmax thread
     if constexpr (decltype(nc)::value <= 64) {
-      if (q4) return f(d, ns, nc, std::true_type());
+      if (q4) return f(ns, nc, std::true_type());
     }
-    return f(d, ns, nc, std::false_type());
+    return f(ns, nc, std::false_type());
   };
-  auto cols = [&](auto d, auto ns) {
+  auto cols = [&](auto ns) {
     // fused rows of 128 channels leave too little room for tiles beside 128 columns
-    constexpr bool wide = !(decltype(d)::value == 128 && decltype(ns)::value == 2);
+    constexpr bool wide = !(D == 128 && decltype(ns)::value == 2);
     switch (rows) {
-      case 16: return fmt(d, ns, std::integral_constant<int, 16>());
-      case 32: return fmt(d, ns, std::integral_constant<int, 32>());
-      case 64: return fmt(d, ns, std::integral_constant<int, 64>());
-      default: return fmt(d, ns, std::integral_constant<int, wide ? 128 : 64>());
+      case 16: return fmt(ns, std::integral_constant<int, 16>());
+      case 32: return fmt(ns, std::integral_constant<int, 32>());
+      case 64: return fmt(ns, std::integral_constant<int, 64>());
+      default: return fmt(ns, std::integral_constant<int, wide ? 128 : 64>());
     }
   };
-  auto dims = [&](auto ns) {
-    switch (D) {
-      case 64: return cols(std::integral_constant<int, 64>(), ns);
-      case 80: return cols(std::integral_constant<int, 80>(), ns);
-      case 96: return cols(std::integral_constant<int, 96>(), ns);
-      default: return cols(std::integral_constant<int, 128>(), ns);
-    }
-  };
-  return nsrc == 2 ? dims(std::integral_constant<int, 2>()) : dims(std::integral_constant<int, 1>());
+  return nsrc == 2 ? cols(std::integral_constant<int, 2>()) : cols(std::integral_constant<int, 1>());
 }
 
-}  // namespace
-
-bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
-  if (a.is_f32) return false;
-  const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
-  plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim == 128))) plan->rows = 64;
-  plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
-  dispatch_tc(a.head_dim, nsrc, plan->rows, a.q4, [&](auto d, auto ns, auto nc, auto q4) {
-    size_tc<decltype(d)::value, decltype(ns)::value, decltype(nc)::value, decltype(q4)::value>(a.batch, plan);
+template <int D>
+void tree_tc_size(const TreeArgs& a, TreePlan* plan) {
+  dispatch_tc<D>(a.k[1] ? 2 : 1, plan->rows, a.q4, [&](auto ns, auto nc, auto q4) {
+    size_tc<D, decltype(ns)::value, decltype(nc)::value, decltype(q4)::value>(a.batch, plan);
   });
-  if (plan->slots == 0) return false;
-  // one CTA an SM over ranges and row tiles; the device takes fewer ranges
-  // where there are fewer key tiles
-  plan->ranges = a.num_ctas > 0 ? a.num_ctas : num_sms / plan->row_tiles > 0 ? num_sms / plan->row_tiles : 1;
-  plan->tensor = true;
-  return true;
 }
 
-cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  return dispatch_tc(a.head_dim, a.k[1] ? 2 : 1, plan.rows, a.q4, [&](auto d, auto ns, auto nc, auto q4) {
-    constexpr int D = decltype(d)::value, NS = decltype(ns)::value, NC = decltype(nc)::value;
+template <int D>
+cudaError_t tree_tc_run(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+  return dispatch_tc<D>(a.k[1] ? 2 : 1, plan.rows, a.q4, [&](auto ns, auto nc, auto q4) {
+    constexpr int NS = decltype(ns)::value, NC = decltype(nc)::value;
     constexpr bool Q4 = decltype(q4)::value;
     if constexpr (NS == 2) {
       return launch_tc<D, 2, true, NC, Q4>(p, a, plan, stream);
@@ -1009,4 +984,5 @@ cudaError_t tree_tc_launch(const TreeParams& p, const TreeArgs& a, const TreePla
   });
 }
 
+}  // namespace
 }  // namespace fkv

@@ -140,8 +140,15 @@ def _ptr(x) -> Optional[int]:
     raise TypeError("expected a tensor, an int pointer or None, got %r" % type(x))
 
 
+# torch's current stream as a number, without the Stream object that
+# torch.cuda.current_stream() makes (2.9 us a call on a Grace host, against 0.1)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -197,7 +204,7 @@ class Context:
     def _need(self, t: torch.Tensor, shape, dtype, name):
         if not isinstance(t, torch.Tensor):
             return
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
             raise ValueError("%s: expected contiguous %s %s, got %s %s" %
                              (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
