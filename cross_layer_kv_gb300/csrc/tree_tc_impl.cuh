@@ -262,8 +262,13 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     if (wlim != 0 && mbar_try_wait(bar, parity)) return true;
     return wait_on(bar, parity, wlim, abort_flag, p.status);
   };
+  // the same by a whole warp, with one answer
+  auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (wlim != 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity, wlim, abort_flag, p.status));
+  };
   // the value products of tile t are done
-  auto products = [&](int t) { return wait(&o_done[t & 3], (uint32_t)(t >> 2) & 1u); };
+  auto products = [&](int t) { return await(&o_done[t & 3], (uint32_t)(t >> 2) & 1u); };
   auto slot_ptr = [&](int s) { return sRing + (size_t)s * C::SLOT; };
 
   if (active && warp >= C::PRODUCER_WARP && warp < C::DQ_WARP)
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       const int first = (tid - C::DQ_WARP * 32) / DQ_GROUP;
       for (int k = 0; k < first; ++k) step();
       for (long long g = first; g < total; g += GROUPS) {
-        if (!__all_sync(0xffffffffu, wait(&raw_full[r], rturn) && (g < nslots || wait(&empty[sl], turn)))) break;
+        if (!await(&raw_full[r], rturn) || (g >= nslots && !await(&empty[sl], turn))) break;
         const uint8_t* rec = sRaw + (size_t)r * C::RAW;
         uint8_t* dst = slot_ptr(sl);
 #pragma unroll 4
@@ -401,7 +406,6 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
     constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
     constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
     const bool qk = warp == C::QK_WARP;
-    auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
     // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
     const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
                            : sdesc128(smem_u32(sRing), KT * SWB, 8 * SWB);
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         for (int i = 0; ok && i < n; ++i, ++j) {
           const uint32_t d = tmem + (j & 1) * NC;
           ok = (j < 2 || await(&p_full[j & 1], (uint32_t)((j - 2) >> 1) & 1u)) &&
-               (j < 3 || __all_sync(0xffffffffu, products(j - 3)));
+               (j < 3 || products(j - 3));
 #pragma unroll
           for (int src = 0; src < NSRC; ++src) {
             if (!ok || !await(&full[sl], turn)) {
@@ -616,8 +620,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
       // threads, and all leave together at the piece's end.
       for (int i = 0; i < n; ++i) {
         const int j = jt + i;
-        ok = ok && wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
-        __syncwarp();
+        ok = ok && await(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
         tc_fence_after();
         const uint32_t t_s = t_lane + (j & 1) * NC;
         // uniform over the CTA: rows that some column does not see
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
 #pragma unroll
           for (int src = 0; src < NSRC; ++src) {
             const int g = g0 + src;
-            ok = ok && wait(&full[g % nslots], (uint32_t)(g / nslots) & 1u);
+            ok = ok && await(&full[g % nslots], (uint32_t)(g / nslots) & 1u);
           }
           bool seen = false;
           if (key < t.cnt) {
@@ -769,7 +772,6 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
         // P of this key: 2^x, bf16
         const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
         ok = ok && (pj < 0 || products(pj));
-        __syncwarp();
         uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
 #pragma unroll
         for (int c = 0; c < HC; c += CH) {
