@@ -8,18 +8,23 @@ namespace {
 
 // The tensor-core kernels: bf16 and 4-bit caches.
 bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
-  if (a.is_f32) return false;
   const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
   plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim == 128))) plan->rows = 64;
-  plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
-  switch (a.head_dim) {
-    case 64: tree_tc_size_64(a, plan); break;
-    case 80: tree_tc_size_80(a, plan); break;
-    case 96: tree_tc_size_96(a, plan); break;
-    default: tree_tc_size_128(a, plan); break;
+  // fewer columns a CTA until the tiles that the products need fit beside them
+  // (4-bit fused caches of 128 channels; batches of hundreds)
+  for (;;) {
+    plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
+    switch (a.head_dim) {
+      case 64: tree_tc_size_64(a, plan); break;
+      case 80: tree_tc_size_80(a, plan); break;
+      case 96: tree_tc_size_96(a, plan); break;
+      default: tree_tc_size_128(a, plan); break;
+    }
+    if (plan->slots > 0) break;
+    if (plan->rows == 16) return false;
+    plan->rows /= 2;
   }
-  if (plan->slots == 0) return false;
   // one CTA an SM over ranges and row tiles; the device takes fewer ranges
   // where there are fewer key tiles
   plan->ranges = a.num_ctas > 0 ? a.num_ctas : num_sms / plan->row_tiles > 0 ? num_sms / plan->row_tiles : 1;
@@ -50,7 +55,8 @@ bool tile_maps(TileMaps* m, const void* base, int D, int rows, long long planes)
 }
 
 cudaError_t tree_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
-  if (!tree_tc_plan(a, num_sms, plan)) tree_simt_plan(a, num_sms, plan);
+  if (a.is_f32) tree_f32_plan(a, num_sms, plan);
+  else if (!tree_tc_plan(a, num_sms, plan)) return cudaErrorNotSupported;
   // two partial records per range and row tile, then the arrival words
   plan->partial_bytes = (size_t)plan->ranges * 2 * plan->row_tiles *
                         tree_record_floats(plan->rows, a.head_dim) * sizeof(float);
@@ -89,7 +95,7 @@ cudaError_t tree_launch(const TreeArgs& a, const TreePlan& plan, cudaStream_t st
   // recycled workspace may hold
   p.epoch = a.epoch * 0x9E3779B1u;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-  return plan.tensor ? tree_tc_launch(p, a, plan, stream) : tree_simt_launch(p, a, plan, stream);
+  return plan.tensor ? tree_tc_launch(p, a, plan, stream) : tree_f32_launch(p, a, plan, stream);
 }
 
 }  // namespace fkv

@@ -35,9 +35,9 @@ cudaError_t tree_tc_run_64(const TreeParams&, const TreeArgs&, const TreePlan&, 
 cudaError_t tree_tc_run_80(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
 cudaError_t tree_tc_run_96(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
 cudaError_t tree_tc_run_128(const TreeParams&, const TreeArgs&, const TreePlan&, cudaStream_t);
-void tree_simt_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
-cudaError_t tree_simt_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
-                             cudaStream_t stream);
+void tree_f32_plan(const TreeArgs& a, int num_sms, TreePlan* plan);
+cudaError_t tree_f32_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan,
+                            cudaStream_t stream);
 
 struct TreeParams {
   const void* k[2];

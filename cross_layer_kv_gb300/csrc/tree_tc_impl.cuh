@@ -97,14 +97,17 @@ struct TcCfg {
   // barriers and words, then the arrays of floats and masks
   static constexpr int BAR_BYTES = ((2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 11 * 8 + 6 * 4 + 127) / 128 * 128;
   static constexpr int ARRAY_BYTES = NC * 4 * 8 + kTreeMaxNodes * (16 + 4 + NW * 4);
-  // two P buffers where at least five tile slots remain beside them
-  static constexpr int NPB =
-      (SMEM_LIMIT - 3072 - Q_BYTES - BAR_BYTES - ARRAY_BYTES - OVERRUN - 2 * P_BYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int RAW = KT * q4_row_bytes(D);       // records of a tile
+  // two P buffers where at least five tile slots remain beside them (4-bit
+  // caches: the four that the dequantising groups need, with four of records
+  // and the lengths of the largest batch)
+  static constexpr int BESIDE = 3072 + Q_BYTES + BAR_BYTES + ARRAY_BYTES + OVERRUN + 2 * P_BYTES +
+                                (Q4 ? (int)tree_seqs_bytes(1024) + 4 * RAW : 0);
+  static constexpr int NPB = (SMEM_LIMIT - BESIDE) / SLOT >= (Q4 ? 4 : 5) ? 2 : 1;
   static constexpr int REF_OFF = Q_BYTES + NPB * P_BYTES + BAR_BYTES;
   __host__ __device__ static constexpr int ring_off(int B) {
     return (REF_OFF + ARRAY_BYTES + (int)tree_seqs_bytes(B) + 1023) / 1024 * 1024;
   }
-  static constexpr int RAW = KT * q4_row_bytes(D);       // records of a tile
   static constexpr int THREADS = SM + 128 + (Q4 ? DQ_THREADS : 0);
   // registers a thread: 168 at launch with 384 threads, 96 with 640; the
   // control (and dequantising) warpgroups give some up for the softmax:

@@ -46,10 +46,20 @@ def test_node_numbers(fmt, T):
     _run("T=%d" % T, fmt=fmt, T=T, S=400, lens=(0, 130, 271), D=64, G=2, H=1)
 
 
-@pytest.mark.parametrize("T,G", [(128, 4), (96, 4), (70, 2)])
+@pytest.mark.parametrize("fmt,T,G", [("bf16", 128, 4), ("bf16", 96, 4), ("bf16", 70, 2), ("f32", 70, 4),
+                                     ("q4", 128, 2), ("q4", 40, 2)])
 @pytest.mark.parametrize("mode", ["lite", "fused"])
-def test_many_rows(T, G, mode):
-    _run("T=%d G=%d" % (T, G), T=T, G=G, mode=mode, S=420, lens=(3, 128, 290), D=128, H=2)
+def test_many_rows(fmt, T, G, mode):
+    _run("T=%d G=%d" % (T, G), fmt=fmt, T=T, G=G, mode=mode, S=420, lens=(3, 128, 290), D=128, H=2)
+
+
+@pytest.mark.parametrize("fmt,Bt", [("bf16", 300), ("f32", 300), ("q4", 300), ("bf16", 1024), ("q4", 1024)])
+def test_large_batches(fmt, Bt):
+    """The lengths of the batch take shared memory from the tiles."""
+    T = 3
+    lens = [(7 * b) % 61 for b in range(Bt)]
+    counts = [b % (T + 1) for b in range(Bt)]
+    _run("B=%d" % Bt, fmt=fmt, Bt=Bt, T=T, S=64, lens=lens, counts=counts, H=1, G=1, D=128)
 
 
 @pytest.mark.parametrize("P", [0, 1, 15, 16, 31, 63, 64, 65, 112, 119, 120, 121, 127, 128, 129, 255, 256, 1000])
