@@ -139,16 +139,23 @@ __device__ __forceinline__ int tree_depth(const TreeParams& p, int b, int i, int
 }
 
 // The cut: the tiles of all units, unit by unit, in `ranges` equal contiguous
-// ranges.  Fills sq, and zeros the output of the sequences whose lengths are
-// out of range; every thread of the CTA takes part.
+// ranges.  Where ranges would be short (six tiles and fewer), a boundary within
+// `snap` tiles of a unit's start or end moves there: on the tensor cores,
+// writing, announcing and merging a partial takes as long as four to six tiles
+// (snap = 3: 650M ring layer, 32 units of five tiles, 19.5 -> 18.1 us; other
+// short calls 25 -> 20, 35 -> 30, 20 -> 23 us).  fp32 tiles take longer than a
+// merge (snap = 0: 12.5 us a tiny call, 19.3 with 3).  Fills sq, and zeros the
+// output of the sequences whose lengths are out of range; every thread of the
+// CTA takes part.
 struct TreeCut {
   long long total;
   int ranges;
+  int snap;
 };
 
 template <typename E, int D>
 __device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, const TreeSeqs& sq, int KT,
-                                            int max_ranges) {
+                                            int max_ranges, int snap) {
   const bool first = blockIdx.x == 0 && blockIdx.y == 0;
   bool bad = false;
   for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
@@ -190,6 +197,7 @@ __device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, const TreeSeqs&
   TreeCut c;
   c.total = (long long)p.H * sq.pre[p.B];
   c.ranges = (int)min((long long)max_ranges, c.total);
+  c.snap = c.total <= 6ll * c.ranges ? snap : 0;
   return c;
 }
 
@@ -199,14 +207,31 @@ struct TreePiece {
   bool first;   // the range's first piece
 };
 
+// The first tile of a range, as cut.
+__device__ __forceinline__ long long tree_bound(const TreeCut& c, const int* pre, int B, int H,
+                                                long long range) {
+  const long long t = range * c.total / c.ranges;
+  if (c.snap == 0 || t >= c.total) return t;
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)H * pre[mid + 1] > t) hi = mid; else lo = mid + 1;
+  }
+  const int n = pre[lo + 1] - pre[lo];
+  const int k = (int)((t - (long long)H * pre[lo]) % n);   // of the unit's n tiles
+  return k <= c.snap ? t - k : n - k <= c.snap ? t + n - k : t;
+}
+
 struct TreeWalk {
   long long t, t1;
   int b, h, k;
   bool first;
 
   __device__ __forceinline__ void begin(const TreeCut& c, const int* pre, int B, int H, int range) {
-    t = range * c.total / c.ranges;
-    t1 = (range + 1) * c.total / c.ranges;
+    t = tree_bound(c, pre, B, H, range);
+    t1 = tree_bound(c, pre, B, H, range + 1);
+    first = true;
+    if (t >= t1) return;   // nothing is left of the range
     int lo = 0, hi = B - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -217,7 +242,6 @@ struct TreeWalk {
     b = lo;
     h = (int)(off / n);
     k = (int)(off - (long long)h * n);
-    first = true;
   }
   __device__ __forceinline__ bool next(const int* pre, int B, int H, TreePiece& pc) {
     if (t >= t1) return false;
@@ -251,13 +275,16 @@ struct TreeUnit {
   bool first_is_tail;      // the first range's piece is its last one
 };
 
-__device__ __forceinline__ TreeUnit tree_unit(const TreeCut& c, const int* pre, int H, int b, int h) {
+__device__ __forceinline__ TreeUnit tree_unit(const TreeCut& c, const int* pre, int B, int H, int b, int h) {
   const long long n = pre[b + 1] - pre[b];
   const long long u0 = (long long)H * pre[b] + h * n, u1 = u0 + n;
+  // boundaries r * total / ranges up to `low` fall on u0 or before, those from
+  // u1 - snap on on u1 or behind
+  const long long low = u0 + min((long long)c.snap, n - 1);
   TreeUnit u;
-  u.first = ((u0 + 1) * c.ranges - 1) / c.total;
-  u.last = (u1 * c.ranges - 1) / c.total;
-  u.first_is_tail = u.first * c.total / c.ranges < u0;
+  u.first = ((low + 1) * c.ranges + c.total - 1) / c.total - 1;
+  u.last = max(u.first, ((u1 - c.snap) * c.ranges + c.total - 1) / c.total - 1);
+  u.first_is_tail = tree_bound(c, pre, B, H, u.first) < u0;
   return u;
 }
 
@@ -280,7 +307,7 @@ template <typename E, int D, int ROWS, int NT, typename Sync>
 __device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut& c, const int* pre,
                                              int b, int h, int N, int tid, int* flag, float* scratch,
                                              Sync sync) {
-  const TreeUnit u = tree_unit(c, pre, p.H, b, h);
+  const TreeUnit u = tree_unit(c, pre, p.B, p.H, b, h);
   const int P = (int)(u.last - u.first + 1);
   const int rt = blockIdx.y;
   __threadfence();

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(NT) tree_f32_kernel(const TreeParams p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   grid_dep_trigger();
   grid_dep_wait();
-  const TreeCut cut = tree_cut<float, D>(p, sq, KT, gridDim.x);
+  const TreeCut cut = tree_cut<float, D>(p, sq, KT, gridDim.x, 0);
   if ((int)blockIdx.x >= cut.ranges) return;
   const int rt = blockIdx.y;
   const size_t plane = p.ring > 0 ? p.ring : p.S_max;

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
   grid_dep_wait();
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
   tc_fence_before();
-  const TreeCut cut = tree_cut<__nv_bfloat16, D>(p, sq, KT, gridDim.x);   // ends with a __syncthreads
+  const TreeCut cut = tree_cut<__nv_bfloat16, D>(p, sq, KT, gridDim.x, 3);   // ends with a __syncthreads
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool active = (int)blockIdx.x < cut.ranges;
