@@ -501,11 +501,13 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
 size_t fkv_tree_workspace_bytes(const fkv_ctx* c, int T) {
   if (!c || T < 1 || T > kTreeNodes) return 0;
   size_t best = 0;
-  for (int nsrc = 1; nsrc <= 2; ++nsrc)
+  for (int kind = 0; kind < 3; ++kind)   // one source, one with weights, two
     for (int q4 = 0; q4 <= 1; ++q4) {
       fkv::TreeArgs t = tree_args(c, T);
       t.q4 = q4;
-      t.k[1] = nsrc == 2 ? c : nullptr;   // only whether there is a second source counts
+      // only whether there are weights and a second source counts here
+      t.a[0] = kind >= 1 ? reinterpret_cast<const float*>(c) : nullptr;
+      t.k[1] = kind == 2 ? c : nullptr;
       fkv::TreePlan p{};
       if (fkv::tree_plan(t, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
         best = p.workspace_bytes;

@@ -10,7 +10,7 @@ namespace {
 bool tree_tc_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
   const int rows = a.group * a.T, nsrc = a.k[1] ? 2 : 1;
   plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim == 128))) plan->rows = 64;
+  if (plan->rows == 128 && (a.q4 || (nsrc == 2 && a.head_dim > 64))) plan->rows = 64;
   // fewer columns a CTA until the tiles that the products need fit beside them
   // (4-bit fused caches of 128 channels; batches of hundreds)
   for (;;) {

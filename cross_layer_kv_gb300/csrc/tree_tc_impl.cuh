@@ -13,8 +13,10 @@
 // only taken on the first tile of a piece and when the scores grow.  Fused
 // layers need no fused tile: S = K^1 (q a_1)^T + K^n (q a_n)^T accumulates in
 // one product, and O = b_1 (V^1 P) + b_n (V^n P) keeps two accumulators.
-// q a is rounded to bf16 (2^-9 of each product's term, random over channels),
-// and P to bf16 as in the prefill kernels; sums are fp32.
+// q a is split into two bf16 halves (exact to 2^-16; one half alone cost 1.5e-3
+// of relative error in the output, as much as P), which doubles the score
+// products of weighted layers, and P is rounded to bf16 as in the prefill
+// kernels; sums are fp32.
 //
 // A CTA takes a contiguous range of key tiles of 128 rows (tree_common.cuh)
 // and one tile of NC query rows:
@@ -67,11 +69,16 @@ constexpr int SWB = 128;              // bytes of a swizzled row: 64 channels or
 constexpr int SWC = SWB / 2;
 constexpr float SLACK = 8.f;          // log2 growth of a score over its reference
 
-template <int D, int NSRC, int NC, bool Q4>
+template <int D, int NSRC, bool WGT, int NC, bool Q4>
 struct TcCfg {
   static constexpr int CB = (D + SWC - 1) / SWC;         // 64-channel blocks
   static constexpr int SLOT = CB * KT * SWB;             // one K or V tile
-  static constexpr int Q_BYTES = NSRC * CB * NC * SWB;
+  // the queries, or per source the high and low halves of query times weight
+  // (the high half alone over 4-bit caches, whose keys are rounded to bf16 too:
+  // both halves took 186 us instead of 159 at 332M fused, T = 16, and the
+  // output's error from 3.5e-3 to 3.0e-3)
+  static constexpr int NQ = WGT && !Q4 ? 2 : 1;
+  static constexpr int Q_BYTES = NSRC * NQ * CB * NC * SWB;
   static constexpr int P_BYTES = (NC + SWC - 1) / SWC * KT * SWB;
   static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
   // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
@@ -181,10 +188,10 @@ __device__ __forceinline__ void wg_sync(int wg) { asm volatile("bar.sync %0, 128
 __device__ __forceinline__ int v_slot(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 + 2 * i; }
 
 template <int D, int NSRC, bool WGT, int NC, bool Q4>
-__global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
+__global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots,
                    const int nraw) {
-  using C = TcCfg<D, NSRC, NC, Q4>;
+  using C = TcCfg<D, NSRC, WGT, NC, Q4>;
   constexpr int CB = C::CB, HC = C::HC, CH = C::CH, NW = C::NW, NPB = C::NPB;
   auto sm_sync = [] { sm_barrier<C::SM>(); };
   // Everything before the rings lies at offsets known at compile time, from a
@@ -449,12 +456,14 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
             if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint64_t ad = a.at((k >> 2) * KT * SWB + (k & 3) * 32);
-                const uint64_t bd = db.at((src * CB + (k >> 2)) * NC * SWB + (k & 3) * 32);
-                if (src == 0 && k == 0) mma_bf16_t<false>(d, ad, bd, IDESC_QK);
-                else mma_bf16_t<true>(d, ad, bd, IDESC_QK);
-              }
+              for (int part = 0; part < C::NQ; ++part)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint64_t ad = a.at((k >> 2) * KT * SWB + (k & 3) * 32);
+                  const uint64_t bd = db.at(((src * C::NQ + part) * CB + (k >> 2)) * NC * SWB + (k & 3) * 32);
+                  if (src == 0 && part == 0 && k == 0) mma_bf16_t<false>(d, ad, bd, IDESC_QK);
+                  else mma_bf16_t<true>(d, ad, bd, IDESC_QK);
+                }
               if (src == NSRC - 1) mma_commit(&s_full[j & 1]);
               mma_commit(&empty[sl]);
             }
@@ -538,23 +547,29 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
                          __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
 #pragma unroll
         for (int src = 0; src < NSRC; ++src) {
-          uint4 o = w;
+          uint8_t* dst = sQ + src * C::NQ * CB * NC * SWB + (ch >> 3) * NC * SWB + swz128(r, ch & 7);
           if constexpr (WGT) {
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
             if (d < D) {
               const float4* ap = reinterpret_cast<const float4*>(p.a[src] + (size_t)pc.h * D + d);
               const float4 a0 = ap[0], a1 = ap[1];
-              uint32_t x[4];
               const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int e0 = Q4 ? e : 2 * e, e1 = Q4 ? e + 4 : 2 * e + 1;
-                const __nv_bfloat162 v2 = __floats2bfloat162_rn(f[e0] * av[e0], f[e1] * av[e1]);
-                x[e] = *reinterpret_cast<const uint32_t*>(&v2);
+                const float x0 = f[e0] * av[e0], x1 = f[e1] * av[e1];
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+                hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                const __nv_bfloat162 l2 = __floats2bfloat162_rn(x0 - bf16lo(hi[e]), x1 - bf16hi(hi[e]));
+                lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
               }
-              o = make_uint4(x[0], x[1], x[2], x[3]);
             }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (C::NQ == 2)
+              *reinterpret_cast<uint4*>(dst + CB * NC * SWB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint4*>(dst) = w;
           }
-          *reinterpret_cast<uint4*>(sQ + src * CB * NC * SWB + (ch >> 3) * NC * SWB + swz128(r, ch & 7)) = o;
         }
       }
       // the nodes' masks and depths, then per drafted key the columns that see it
@@ -898,9 +913,9 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, NC, Q4>::THREADS, 1)
 }
 
 // Tile slots and shared memory of a configuration; 0 slots if it does not fit.
-template <int D, int NSRC, int NC, bool Q4>
+template <int D, int NSRC, bool WGT, int NC, bool Q4>
 void size_tc(int B, TreePlan* plan) {
-  using C = TcCfg<D, NSRC, NC, Q4>;
+  using C = TcCfg<D, NSRC, WGT, NC, Q4>;
   const int fixed = 1024 + C::ring_off(B) + C::OVERRUN;
   int left = SMEM_LIMIT - fixed;
   plan->raw_slots = 0;
@@ -933,7 +948,7 @@ cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& pl
     std::memcpy(&maps.full[i], m->full, sizeof(CUtensorMap));
     std::memcpy(&maps.tail[i], m->tail, sizeof(CUtensorMap));
   }
-  using C = TcCfg<D, NSRC, NC, Q4>;
+  using C = TcCfg<D, NSRC, WGT, NC, Q4>;
   auto kern = tree_tc_kernel<D, NSRC, WGT, NC, Q4>;
   // the softmax warpgroups' larger share of the registers has to fit the launch
   // allocation, or it would never be granted: refuse instead
@@ -944,48 +959,45 @@ cudaError_t launch_tc(const TreeParams& p, const TreeArgs& a, const TreePlan& pl
                     p, plan.slots, plan.raw_slots);
 }
 
-// Call f with the plan's columns, its sources and whether the caches are 4-bit
-// as integral constants.
+// Call f with the plan's sources, weights and columns and whether the caches
+// are 4-bit as integral constants.
 template <int D, typename F>
-auto dispatch_tc(int nsrc, int rows, bool q4, F f) {
-  auto fmt = [&](auto ns, auto nc) {
+auto dispatch_tc(const TreeArgs& a, int rows, F f) {
+  auto fmt = [&](auto ns, auto wt, auto nc) {
     // 4-bit caches take at most 64 columns: 128 registers a softmax thread
     if constexpr (decltype(nc)::value <= 64) {
-      if (q4) return f(ns, nc, std::true_type());
+      if (a.q4) return f(ns, wt, nc, std::true_type());
     }
-    return f(ns, nc, std::false_type());
+    return f(ns, wt, nc, std::false_type());
   };
-  auto cols = [&](auto ns) {
-    // fused rows of 128 channels leave too little room for tiles beside 128 columns
-    constexpr bool wide = !(D == 128 && decltype(ns)::value == 2);
+  auto cols = [&](auto ns, auto wt) {
+    // two sources of more than 64 channels leave too little room for tiles
+    // beside 128 columns
+    constexpr bool wide = !(D > 64 && decltype(ns)::value == 2);
     switch (rows) {
-      case 16: return fmt(ns, std::integral_constant<int, 16>());
-      case 32: return fmt(ns, std::integral_constant<int, 32>());
-      case 64: return fmt(ns, std::integral_constant<int, 64>());
-      default: return fmt(ns, std::integral_constant<int, wide ? 128 : 64>());
+      case 16: return fmt(ns, wt, std::integral_constant<int, 16>());
+      case 32: return fmt(ns, wt, std::integral_constant<int, 32>());
+      case 64: return fmt(ns, wt, std::integral_constant<int, 64>());
+      default: return fmt(ns, wt, std::integral_constant<int, wide ? 128 : 64>());
     }
   };
-  return nsrc == 2 ? cols(std::integral_constant<int, 2>()) : cols(std::integral_constant<int, 1>());
+  if (a.k[1]) return cols(std::integral_constant<int, 2>(), std::true_type());
+  if (a.a[0]) return cols(std::integral_constant<int, 1>(), std::true_type());
+  return cols(std::integral_constant<int, 1>(), std::false_type());
 }
 
 template <int D>
 void tree_tc_size(const TreeArgs& a, TreePlan* plan) {
-  dispatch_tc<D>(a.k[1] ? 2 : 1, plan->rows, a.q4, [&](auto ns, auto nc, auto q4) {
-    size_tc<D, decltype(ns)::value, decltype(nc)::value, decltype(q4)::value>(a.batch, plan);
+  dispatch_tc<D>(a, plan->rows, [&](auto ns, auto wt, auto nc, auto q4) {
+    size_tc<D, decltype(ns)::value, decltype(wt)::value, decltype(nc)::value, decltype(q4)::value>(a.batch, plan);
   });
 }
 
 template <int D>
 cudaError_t tree_tc_run(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  return dispatch_tc<D>(a.k[1] ? 2 : 1, plan.rows, a.q4, [&](auto ns, auto nc, auto q4) {
-    constexpr int NS = decltype(ns)::value, NC = decltype(nc)::value;
-    constexpr bool Q4 = decltype(q4)::value;
-    if constexpr (NS == 2) {
-      return launch_tc<D, 2, true, NC, Q4>(p, a, plan, stream);
-    } else {
-      if (a.a[0]) return launch_tc<D, 1, true, NC, Q4>(p, a, plan, stream);
-      return launch_tc<D, 1, false, NC, Q4>(p, a, plan, stream);
-    }
+  return dispatch_tc<D>(a, plan.rows, [&](auto ns, auto wt, auto nc, auto q4) {
+    return launch_tc<D, decltype(ns)::value, decltype(wt)::value, decltype(nc)::value, decltype(q4)::value>(
+        p, a, plan, stream);
   });
 }
 

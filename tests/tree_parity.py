@@ -110,7 +110,8 @@ class TreeSetup:
           (u_p + 2 ds) sum_t p_t |v_t|      probabilities rounded to bf16 (u_p), scores off by ds,
           u_v sum_t p_t |v_t|               4-bit values dequantised to bf16,
         to first order, where ds = scale * sum_d (u_q |q a k| + u_k |q a k|): the query times the
-        key weights is rounded to bf16 (u_q, weighted modes), 4-bit keys to bf16 (u_k).  fp32 sums
+        key weights is held in two bf16 halves (u_q = 2^-16, weighted modes; over 4-bit caches in one,
+        2^-8), 4-bit keys in one (u_k).  fp32 sums
         of n terms add n 2^-24 of the sum of their magnitudes (D terms a score, the rows a value;
         rows above 1024 add in random order and are counted as 1024).
         """
@@ -129,7 +130,7 @@ class TreeSetup:
         weighted = self.mode in ("fused", "scaled")
         u_o = u32 * 4 if f32 else u16
         u_p = 0.0 if f32 else u16
-        u_q = u16 if weighted and not f32 else 0.0
+        u_q = (u16 if self.fmt == "q4" else u16 * u16) if weighted and not f32 else 0.0
         u_k = u_v = u16 if self.fmt == "q4" else 0.0
         bound = np.full(ref.shape, np.inf)
         for b in range(self.Bt):
