@@ -12,7 +12,8 @@
 // below 256, exact scaling), so the column maximum over the 128 threads is
 // only taken on the first tile of a piece and when the scores grow.  Fused
 // layers need no fused tile: S = K^1 (q a_1)^T + K^n (q a_n)^T accumulates in
-// one product, and O = b_1 (V^1 P) + b_n (V^n P) keeps two accumulators.
+// one product, and O = b_1 (V^1 P) + b_n (V^n P) keeps two accumulators (one of
+// 128 lanes for both at 64 channels: 332M fused, T = 64, 228 -> 207 us).
 // q a is split into two bf16 halves (exact to 2^-16; one half alone cost 1.5e-3
 // of relative error in the output, as much as P), which doubles the score
 // products of weighted layers, and P is rounded to bf16 as in the prefill
@@ -20,10 +21,9 @@
 //
 // A CTA takes a contiguous range of key tiles of 128 rows (tree_common.cuh)
 // and one tile of NC query rows:
-//  * the producer warp loads K and V tiles by TMA (boxes of 128-byte rows: with
-//    64-byte rows the copy engine itself held the kernel at 25 bytes a clock
-//    and SM, half of its share of HBM) into a ring of slots, in the order in which the MMAs read them:
-//    K_0, K_1, V_0, K_2, V_1, ...;
+//  * the producer warp loads K and V tiles by TMA (boxes of 128-byte rows) into
+//    a ring of slots, in the order in which the MMAs read them: K_0, K_1, V_0,
+//    K_2, V_1, ...;
 //  * one warp issues S_j = K_j Q^T up to two tiles ahead (S has two buffers in
 //    tensor memory), another O += V_j^T P_j: an MMA of these sizes costs its
 //    issuer 40 to 48 clocks at 16 to 64 columns (64 at 128), as long as the
@@ -39,6 +39,16 @@
 // for the tensor cores; decode keeps fp32).  The pairs that fall out of a word
 // are channels e and e + 4 of eight, so the tiles hold the channels in the
 // order 0 4 1 5 2 6 3 7 and so do the queries; the epilogue undoes it.
+//
+// What bounds it (one GB300, against 6.78 TB/s of measured copy bandwidth; bytes
+// are the cached rows once): HBM from 32 columns and 160-byte rows on (4B lite,
+// T = 16: 2.0 GB in 300 us; 1.5B fused, T = 26: 3.2 GB in 460 us).  With 128
+// columns the softmax's issue slots (332M fused, T = 64: 0.82 GB in 207 us, 44%
+// of the slots used, tensor pipe 34%); with 16 columns the end of a unit, which
+// the ring's 192 KB of tiles hides only in part (332M lite, T = 8: 0.40 GB in
+// 75 us); over 4-bit caches the dequantisation beside the softmax (332M fused,
+// T = 16: 0.30 GB in 150 us, 52% of the slots); short calls their chain of
+// prologue, first tile, merge (650M ring layer, T = 12: 18 us).
 //
 // Tiles with drafted rows, a window's edge or a ragged end are masked, and the
 // value rows that nobody sees are zeroed in shared memory, since 0 * NaN is
@@ -81,15 +91,20 @@ struct TcCfg {
   static constexpr int Q_BYTES = NSRC * NQ * CB * NC * SWB;
   static constexpr int P_BYTES = (NC + SWC - 1) / SWC * KT * SWB;
   static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
-  // V^T is read as 128 channels: the MMA reads 2 blocks from a slot on,
-  // past its end into what follows (rows that are not used)
-  static constexpr int OVERRUN = Q4 ? 0 : (2 - CB) * KT * SWB;   // (the records follow 4-bit slots)
+  // V^T is read as 128 channels, 2 blocks from a slot on.  Two sources of 64
+  // channels make one product: the blocks are their neighbouring slots, lanes
+  // 0 .. 63 of the accumulator hold V^1 P, the others V^n P.  One source of 64
+  // channels reads past its slot into what follows (rows that are not used;
+  // the records behind 4-bit slots, else a block left free).
+  static constexpr bool PAIR = NSRC == 2 && D == 64;
+  static constexpr int NACC = PAIR ? 1 : NSRC;           // accumulators
+  static constexpr int OVERRUN = Q4 || PAIR ? 0 : (2 - CB) * KT * SWB;
   // Softmax warpgroups, each with a part of the columns of every tile.  Four
-  // from 64 columns on, where they hide each other's waits (332M fused, T = 64:
-  // 202 us, with two 249); two below, which leaves them more registers and
+  // from 64 columns on, where they hide each other's waits (332M fused, T = 64,
+  // took a fifth less than with two); two below, which leaves them more registers and
   // shorter barriers, and for 4-bit caches, whose dequantising warpgroups take
   // the other threads.  (Two warpgroups with every second tile each, references
-  // and accumulators of their own, gained 3% at 16 columns and lost 20% over
+  // and accumulators of their own, gained 3% at 16 columns and lost 19% over
   // 4-bit caches.)
   static constexpr int NWG = NC <= 32 || Q4 ? 2 : 4;
   static constexpr int SM = NWG * 128;                   // softmax threads
@@ -97,7 +112,7 @@ struct TcCfg {
   static constexpr int CH = HC < 16 ? HC : 16;           // of them in registers at a time
   static constexpr int PRODUCER_WARP = 4 * NWG, QK_WARP = PRODUCER_WARP + 1, PV_WARP = PRODUCER_WARP + 2;
   static constexpr int DQ_WARP = PRODUCER_WARP + 4;      // the first of the dequantising warps
-  static constexpr int TMEM_USED = (2 + NSRC) * NC;
+  static constexpr int TMEM_USED = (2 + NACC) * NC;
   static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
   static_assert(TMEM_USED <= 512, "tensor memory");
@@ -192,7 +207,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ TcMaps maps, const TreeParams p, const int nslots,
                    const int nraw) {
   using C = TcCfg<D, NSRC, WGT, NC, Q4>;
-  constexpr int CB = C::CB, HC = C::HC, CH = C::CH, NW = C::NW, NPB = C::NPB;
+  constexpr int CB = C::CB, HC = C::HC, CH = C::CH, NACC = C::NACC, NW = C::NW, NPB = C::NPB;
   auto sm_sync = [] { sm_barrier<C::SM>(); };
   // Everything before the rings lies at offsets known at compile time, from a
   // pointer that the compiler sees is shared memory: addresses cost no
@@ -483,11 +498,10 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
           ok = await(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
           const SDesc128 b{db.lo + (NPB == 2 && (j & 1) ? C::P_BYTES >> 4 : 0), db.hi};
 #pragma unroll
-          for (int src = 0; src < NSRC; ++src) {
-            if (!ok || !await(&full[sl], turn)) {
-              ok = false;
-              break;
-            }
+          for (int src = 0; src < NACC; ++src) {
+            constexpr int SLOTS = C::PAIR ? 2 : 1;   // (a pair never wraps: both counts are even)
+            ok = ok && await(&full[sl], turn) && (SLOTS == 1 || await(&full[sl + 1], turn));
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
               const SDesc128 a{da.lo + (uint32_t)(sl * C::SLOT >> 4), da.hi};
@@ -501,11 +515,12 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
                 for (int k = 1; k < ks; ++k)
                   mma_bf16_t<true>(d, a.at(k * 16 * SWB), b.at(k * 16 * SWB), IDESC_PV);
               }
-              if (src == NSRC - 1) mma_commit(&o_done[j & 3]);
+              if (src == NACC - 1) mma_commit(&o_done[j & 3]);
               mma_commit(&empty[sl]);
+              if (SLOTS == 2) mma_commit(&empty[sl + 1]);
             }
             __syncwarp();
-            skip(1);
+            skip(SLOTS);
           }
           if (i + 2 < n) skip(NSRC);   // the keys of the tile after next
         }
@@ -518,7 +533,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // key of the tile; channel in the epilogue
     const int c0 = wg * HC;                // first column
-    const int chan = Q4 ? (key & ~7) | (key & 1) << 2 | (key >> 1 & 3) : key;   // channel of row `key` of V^T
+    const int row = C::PAIR ? key & 63 : key;   // row of V^T; its channel:
+    const int chan = Q4 ? (row & ~7) | (row & 1) << 2 | (row >> 1 & 3) : row;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
     auto fmaxop = [](float a, float b) { return fmaxf(a, b); };
     auto addop = [](float a, float b) { return a + b; };
@@ -773,7 +789,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
                 l[c + e] *= al[e];
               }
 #pragma unroll
-              for (int src = 0; src < NSRC; ++src) {
+              for (int src = 0; src < NACC; ++src) {
                 const uint32_t to = t_lane + (2 + src) * NC + c;
                 float o[8];
                 tmem_ld8(to, o);
@@ -842,17 +858,18 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
         }
       }
       sm_sync();
-      float bw[NSRC];
+      float bw[NACC];
 #pragma unroll
-      for (int src = 0; src < NSRC; ++src) {
+      for (int src = 0; src < NACC; ++src) {
         bw[src] = 1.f;
-        if (WGT && key < D) bw[src] = p.b[src][(size_t)pc.h * D + chan];
+        if (WGT && row < D) bw[src] = p.b[C::PAIR ? key >> 6 : src][(size_t)pc.h * D + chan];
       }
+      float* pair = reinterpret_cast<float*>(sP) + wg * 64 * 9;   // (P is read; 9: no bank conflicts)
 #pragma unroll 1
       for (int c = c0; c < c0 + HC; c += 8) {
-        float o[NSRC][8], x[8];
+        float o[NACC][8], x[8];
 #pragma unroll
-        for (int src = 0; src < NSRC; ++src)
+        for (int src = 0; src < NACC; ++src)
           tmem_ld8(t_lane - c0 + (2 + src) * NC + c, o[src]);
         tmem_wait_ld();
 #pragma unroll
@@ -860,8 +877,20 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
           const float w = sAlpha[c + e];
           float y = o[0][e];
           if constexpr (WGT) y *= bw[0];
-          if constexpr (NSRC == 2) y = fmaf(bw[1], o[1][e], y);
+          if constexpr (NACC == 2) y = fmaf(bw[1], o[1][e], y);
           x[e] = w == 0.f ? 0.f : w * y;
+        }
+        if constexpr (C::PAIR) {   // the second source's half joins the first's
+          if (key >= 64) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pair[row * 9 + e] = x[e];
+          }
+          wg_sync(wg);
+          if (key < 64) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += pair[row * 9 + e];
+          }
+          wg_sync(wg);
         }
         if (key < D) {
 #pragma unroll
@@ -932,6 +961,7 @@ void size_tc(int B, TreePlan* plan) {
   int slots = left > 0 ? left / C::SLOT : 0;
   if (slots > MAX_SLOTS) slots = MAX_SLOTS;
   if (Q4) slots = slots / (DQ_THREADS / DQ_GROUP) * (DQ_THREADS / DQ_GROUP);
+  if (C::PAIR) slots &= ~1;
   if (slots < 2 * NSRC) slots = 0;
   plan->slots = slots;
   plan->smem_bytes = (size_t)fixed + (size_t)slots * C::SLOT + (size_t)plan->raw_slots * C::RAW;
