@@ -499,7 +499,7 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
 }
 
 size_t fkv_tree_workspace_bytes(const fkv_ctx* c, int T) {
-  if (!c || T < 1 || T > kTreeNodes) return 0;
+  if (!c || T < 1 || T > kTreeNodes || T > c->cfg.max_seq) return 0;
   size_t best = 0;
   for (int kind = 0; kind < 3; ++kind)   // one source, one with weights, two
     for (int q4 = 0; q4 <= 1; ++q4) {

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(32) reorder_kernel(const __grid_constant__ Mov
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ uint64_t full[kReorderStages];
   __shared__ long long first_item[kMovePlanes + 1];
+  __shared__ int head_items[kMovePlanes];
   uint8_t* meta = stage_mem + kReorderSmem;
   int* src_seq = reinterpret_cast<int*>(meta);   // [B] sequence of each slot
   int* src_len = src_seq + a.batch;              // [B] rows read of each slot
@@ -175,31 +176,44 @@ __global__ void __launch_bounds__(32) reorder_kernel(const __grid_constant__ Mov
   // chunk bytes: two stages of all sources fit, and small calls still give
   // every CTA a few items
   long long bytes = 0;   // of one sequence's longest rows over all planes
-  for (int i = 0; i < tb.planes; ++i)
+  for (int i = lane; i < tb.planes; i += 32)
     bytes += (long long)a.kv_heads * min(longest, tb.rows[i]) * tb.row_bytes[i];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
   long long ch = kReorderSmem / 2 / nsrc;
   ch = min(ch, (long long)kReorderChunk);
   ch = min(ch, max(1024LL, bytes / (4LL * gridDim.x)));
   const int CH = (int)max(16LL, ch / 16 * 16);
   const int stage_bytes = nsrc * CH;
   const int NST = min(kReorderStages, kReorderSmem / stage_bytes);
-  if (lane == 0) {
-    long long run = 0;
-    for (int i = 0; i < tb.planes; ++i) {
-      first_item[i] = run;
-      const long long n = (long long)min(longest, tb.rows[i]) * tb.row_bytes[i];
-      run += a.kv_heads * ((n + CH - 1) / CH);
+  long long total = 0;   // items; each plane's first and its items a head
+  for (int base = 0; base < tb.planes; base += 32) {
+    const int i = base + lane;
+    int per = 0;
+    if (i < tb.planes) per = (int)(((long long)min(longest, tb.rows[i]) * tb.row_bytes[i] + CH - 1) / CH);
+    long long incl = (long long)per * a.kv_heads;
+    const long long own = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    first_item[tb.planes] = run;
+    if (i < tb.planes) {
+      head_items[i] = per;
+      first_item[i] = total + incl - own;
+    }
+    total += __shfl_sync(0xffffffffu, incl, 31);
   }
+  if (lane == 0) first_item[tb.planes] = total;
   __syncwarp();
-  const long long total = first_item[tb.planes];
 
   // the plane (from `pl` on), the head's rows and the byte offset of an item
   auto locate = [&](long long item, int& pl, uint8_t*& head, long long& off) {
     while (item >= first_item[pl + 1]) ++pl;
-    const long long per = (first_item[pl + 1] - first_item[pl]) / a.kv_heads;
-    const long long r = item - first_item[pl], h = r / per;
+    // (a plane's bytes are below 2^40 and its chunks, of 96 bytes at least,
+    // below 2^34 for one head: 64-bit items, 32-bit chunks of a head)
+    const long long per = head_items[pl], r = item - first_item[pl];
+    const long long h = (r >> 31) == 0 ? (uint32_t)r / (uint32_t)per : r / per;
     head = static_cast<uint8_t*>(tb.plane[pl]) + (size_t)h * tb.rows[pl] * tb.row_bytes[pl];
     off = (r - h * per) * CH;
   };

@@ -302,7 +302,8 @@ __device__ __forceinline__ void tree_store4(__nv_bfloat16* dst, const float* x) 
 // weights into the output rows.  Called by NT threads (index tid) that `sync`
 // brings together; all of them have written their part before.  scratch holds
 // 2 * ROWS floats of shared memory.  A thread's items (four channels of a row)
-// are loaded together, so a merge of P pieces takes P + 1 trips to L2.
+// are loaded together, so a merge of P pieces takes about P trips to L2 (fewer
+// where a thread has one or two items, whose loop is unrolled).
 template <typename E, int D, int ROWS, int NT, typename Sync>
 __device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut& c, const int* pre,
                                              int b, int h, int N, int tid, int* flag, float* scratch,
@@ -352,7 +353,7 @@ __device__ __forceinline__ void tree_publish(const TreeParams& p, const TreeCut&
   for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-#pragma unroll 1
+#pragma unroll(ITEMS <= 2 ? 4 : 1)
   for (int i = 0; i < P; ++i) {
     const float* m = rec(i);
     const float* o = m - ROWS * D;

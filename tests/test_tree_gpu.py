@@ -249,6 +249,31 @@ def test_other_stream_is_ordered():
     assert torch.equal(got, ref)
 
 
+def test_two_calls_at_once():
+    """Unordered streams, a workspace each, bf16 beside fp32 and 4-bit calls."""
+    sets = [TreeSetup(fmt=f, T=t, Bt=3, lens=(700, 1300, 90), S=1400, seed=i)
+            for i, (f, t) in enumerate([("bf16", 16), ("f32", 9), ("q4", 16), ("bf16", 64)])]
+    want = [s.run().clone() for s in sets]
+    for s in sets:
+        s.out.fill_(-77)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        for s, st in zip(sets, streams):
+            s.run(stream=st)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, want):
+        assert s.ctx.fkv_get_device_status() == B.FKV_OK
+        assert torch.equal(s.out, w)
+
+
+def test_workspace_of_more_nodes_serves_fewer():
+    s = TreeSetup(T=9, Bt=3, lens=(700, 1300, 90), S=1400)
+    ref = s.run().clone()
+    s.ws = s.ctx.tree_workspace(128)
+    assert torch.equal(s.run(), ref)
+
+
 def test_host_refusals():
     s = TreeSetup(T=8, fmt="bf16")
     lib, c, p = s.ctx._lib, s.ctx, lambda t: t.data_ptr()
@@ -282,6 +307,7 @@ def test_host_refusals():
             r.run()
         assert e.value.status == inv
     short = B.Context(4, 1, 4, 2, 2, 64, "bf16")                    # S_max below T
+    assert short.fkv_tree_workspace_bytes(8) == 0 and short.fkv_tree_workspace_bytes(4) > 0
     assert lib.fkv_tree_attn(short.handle, p(s.q), 1, 0, p(s.seq), None, p(s.mask), 8, p(s.out), p(s.ws),
                              n, None) == inv
     assert s.ctx.fkv_get_device_status() == B.FKV_OK
