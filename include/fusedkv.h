@@ -327,7 +327,13 @@ size_t fkv_tree_workspace_bytes(const fkv_ctx* ctx, int T);
  * sequence with P < 0, N outside [0, T] or P + N > S_max gets zeros in all its
  * T rows and FKV_ERR_DEVICE_ARG in the device status.
  * Rows behind position P + N - 1, and rows that no node of the sequence sees,
- * are not used, whatever they hold.
+ * are not used, whatever they hold; a drafted row (or one at a window's edge)
+ * whose values are not finite gives NaN in the rows of the nodes that see it
+ * and does not reach the others.
+ * Rounding: fp32 caches, fp32 throughout; bf16 caches, probabilities to bf16
+ * and query times key weight to two bf16 halves, as operands of the tensor
+ * cores; 4-bit caches also keys, values and query times weight to one bf16.
+ * Sums and softmax statistics are fp32.
  * workspace: device, 16-byte aligned, at least fkv_tree_workspace_bytes(ctx,
  * T) bytes, no initialisation, as for fkv_decode_attn (also its note on graph
  * replays that stopped early); not shared with a call that may run at the same
