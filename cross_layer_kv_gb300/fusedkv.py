@@ -358,8 +358,12 @@ class Context:
         self._need_cuda(tree_mask, (c.batch, T, (T + 63) // 64), torch.int64, "tree_mask")
         self._need_cuda(node_counts, (c.batch,), torch.int32, "node_counts")
         m = MODES[mode] if isinstance(mode, str) else int(mode)
-        nbytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) \
-            else int(getattr(workspace, "nbytes", 0))
+        nbytes = int(getattr(workspace, "nbytes", 0))
+        if isinstance(workspace, torch.Tensor):
+            if not workspace.is_cuda or not workspace.is_contiguous():
+                raise ValueError("workspace: expected a contiguous CUDA tensor, got strides %s on %s" %
+                                 (workspace.stride(), workspace.device))
+            nbytes = workspace.numel() * workspace.element_size()
         _check(self._lib.fkv_tree_attn(self.handle, _ptr(q), layer, m, _ptr(seq_lens),
                                        _ptr(node_counts), _ptr(tree_mask), T, _ptr(out),
                                        _ptr(workspace), nbytes, _stream(stream)), "fkv_tree_attn")
