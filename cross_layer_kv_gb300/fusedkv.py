@@ -143,6 +143,8 @@ def _ptr(x) -> Optional[int]:
 # torch's current stream as a number, without the Stream object that
 # torch.cuda.current_stream() makes (2.9 us a call on a Grace host, against 0.1)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# its current device, likewise
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> Optional[int]:
@@ -331,8 +333,19 @@ class Context:
 
     def _need_cuda(self, t, shape, dtype, name):
         self._need(t, shape, dtype, name)
-        if isinstance(t, torch.Tensor) and not t.is_cuda:
+        self._need_current(t, name)
+
+    @staticmethod
+    def _need_current(t, name):
+        """A tensor of the current device, the one that the library launches on."""
+        if not isinstance(t, torch.Tensor):
+            return
+        index = t.get_device()   # -1: not on a CUDA device
+        if index < 0:
             raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
+        if index != _current_device():
+            raise ValueError("%s: expected a tensor on the current device, cuda:%d, got one on cuda:%d" %
+                             (name, _current_device(), index))
 
     def fkv_tree_workspace_bytes(self, T: int) -> int:
         return int(self._lib.fkv_tree_workspace_bytes(self.handle, T))
@@ -360,9 +373,10 @@ class Context:
         m = MODES[mode] if isinstance(mode, str) else int(mode)
         nbytes = int(getattr(workspace, "nbytes", 0))
         if isinstance(workspace, torch.Tensor):
-            if not workspace.is_cuda or not workspace.is_contiguous():
-                raise ValueError("workspace: expected a contiguous CUDA tensor, got strides %s on %s" %
-                                 (workspace.stride(), workspace.device))
+            self._need_current(workspace, "workspace")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace: expected a contiguous tensor, got strides %s" %
+                                 (workspace.stride(),))
             nbytes = workspace.numel() * workspace.element_size()
         _check(self._lib.fkv_tree_attn(self.handle, _ptr(q), layer, m, _ptr(seq_lens),
                                        _ptr(node_counts), _ptr(tree_mask), T, _ptr(out),
