@@ -13,6 +13,8 @@
 // Packed FMAs (two channels an instruction) in both products.  A call of one
 // sequence over 256 rows (4 query heads, 7 nodes, fused) takes 12.5 us on the
 // device, four tiles and a merge one after another.
+#include <type_traits>
+
 #include "decode_impl.cuh"   // fma2
 #include "tree_common.cuh"
 
@@ -260,17 +262,40 @@ cudaError_t launch_f32(const TreeParams& p, const TreeArgs& a, const TreePlan& p
   return launch_pdl(kern, dim3(plan.ranges, plan.row_tiles), dim3(NT), plan.smem_bytes, stream, p);
 }
 
-template <int D, int RT>
-cudaError_t launch_f32_src(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  if (p.k[1]) return launch_f32<D, 2, true, RT>(p, a, plan, stream);
-  if (p.a[0]) return launch_f32<D, 1, true, RT>(p, a, plan, stream);
-  return launch_f32<D, 1, false, RT>(p, a, plan, stream);
+// Registers a thread of an instance, asked for once; 255 where that fails.
+template <int D, int NSRC, bool WGT, int RT>
+int f32_registers() {
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, tree_f32_kernel<D, NSRC, WGT, RT>) == cudaSuccess ? fa.numRegs : 255;
+  }();
+  return regs;
 }
 
-template <int D>
-cudaError_t launch_f32_rows(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  return plan.rows == 64 ? launch_f32_src<D, 64>(p, a, plan, stream) : launch_f32_src<D, 16>(p, a, plan, stream);
+// Call f with the call's head dimension, sources, weights and rows a CTA as
+// integral constants.
+template <typename F>
+auto dispatch_f32(const TreeArgs& a, int rows, F f) {
+  auto src = [&](auto d, auto rt) {
+    if (a.k[1]) return f(d, std::integral_constant<int, 2>(), std::true_type(), rt);
+    if (a.a[0]) return f(d, std::integral_constant<int, 1>(), std::true_type(), rt);
+    return f(d, std::integral_constant<int, 1>(), std::false_type(), rt);
+  };
+  auto row = [&](auto d) {
+    return rows == 64 ? src(d, std::integral_constant<int, 64>()) : src(d, std::integral_constant<int, 16>());
+  };
+  switch (a.head_dim) {
+    case 64: return row(std::integral_constant<int, 64>());
+    case 80: return row(std::integral_constant<int, 80>());
+    case 96: return row(std::integral_constant<int, 96>());
+    default: return row(std::integral_constant<int, 128>());
+  }
 }
+
+// What an SM holds: registers, and shared memory with 1 KB of it taken by each
+// CTA beside its own.
+constexpr int SM_REGS = 65536;
+constexpr size_t SM_SMEM = 233472, CTA_SMEM = 1024;
 
 }  // namespace
 
@@ -279,21 +304,26 @@ void tree_f32_plan(const TreeArgs& a, int num_sms, TreePlan* plan) {
   plan->tensor = false;
   plan->rows = rows <= 16 ? 16 : 64;
   plan->row_tiles = (rows + plan->rows - 1) / plan->rows;
-  // two CTAs an SM over ranges and row tiles; the device takes fewer ranges
-  // where there are fewer key tiles
-  plan->ranges = a.num_ctas > 0 ? a.num_ctas : (2 * num_sms + plan->row_tiles - 1) / plan->row_tiles;
   const int RT = plan->rows, LD = a.head_dim + 4;
   plan->smem_bytes = (size_t)(RT * LD + 2 * KT * LD + KT * RT + 2 * RT) * 4 + RT * 16 +
                      (kTreeMaxNodes + KT + 1) * 4 + tree_seqs_bytes(a.batch);
+  // One wave: ranges times row tiles are at most the CTAs that the device holds
+  // at once, two an SM or one (64 rows of 80 or 96 channels take too many
+  // registers for two, of 128 too much shared memory).  The device takes fewer
+  // ranges where there are fewer key tiles.
+  const int regs = dispatch_f32(a, plan->rows, [](auto d, auto ns, auto wt, auto rt) {
+    return f32_registers<decltype(d)::value, decltype(ns)::value, decltype(wt)::value, decltype(rt)::value>();
+  });
+  const bool two = 2 * NT * ((regs + 7) / 8 * 8) <= SM_REGS && 2 * (plan->smem_bytes + CTA_SMEM) <= SM_SMEM;
+  const int ranges = (two ? 2 : 1) * num_sms / plan->row_tiles;
+  plan->ranges = a.num_ctas > 0 ? a.num_ctas : ranges > 0 ? ranges : 1;
 }
 
 cudaError_t tree_f32_launch(const TreeParams& p, const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  switch (a.head_dim) {
-    case 64: return launch_f32_rows<64>(p, a, plan, stream);
-    case 80: return launch_f32_rows<80>(p, a, plan, stream);
-    case 96: return launch_f32_rows<96>(p, a, plan, stream);
-    default: return launch_f32_rows<128>(p, a, plan, stream);
-  }
+  return dispatch_f32(a, plan.rows, [&](auto d, auto ns, auto wt, auto rt) {
+    return launch_f32<decltype(d)::value, decltype(ns)::value, decltype(wt)::value, decltype(rt)::value>(p, a, plan,
+                                                                                                        stream);
+  });
 }
 
 }  // namespace fkv
