@@ -143,8 +143,6 @@ def _ptr(x) -> Optional[int]:
 # torch's current stream as a number, without the Stream object that
 # torch.cuda.current_stream() makes (2.9 us a call on a Grace host, against 0.1)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-# its current device, likewise
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> Optional[int]:
@@ -161,6 +159,8 @@ class Context:
     """An fkv_ctx plus references to the caller buffers bound to it (kept
     alive for as long as the context can read them)."""
 
+    _device = None   # its CUDA device, as torch counts them
+
     def __init__(self, num_layers: int, batch: int, max_seq: int, num_q_heads: int,
                  num_kv_heads: int, head_dim: int, dtype: str = "bf16", store_upper: bool = False,
                  softmax_scale: float = 0.0, decode_ctas: int = 0):
@@ -172,6 +172,8 @@ class Context:
         h = ctypes.c_void_p()
         _check(self._lib.fkv_create(ctypes.byref(self.cfg), ctypes.byref(h)), "fkv_create")
         self.handle = h
+        if torch.cuda.is_available():
+            self._device = torch.cuda.current_device()
         self._keep = {}
         self._ring = {}   # layer -> ring rows (layers with full-length caches absent)
 
@@ -332,20 +334,21 @@ class Context:
         return out
 
     def _need_cuda(self, t, shape, dtype, name):
-        self._need(t, shape, dtype, name)
-        self._need_current(t, name)
-
-    @staticmethod
-    def _need_current(t, name):
-        """A tensor of the current device, the one that the library launches on."""
         if not isinstance(t, torch.Tensor):
             return
-        index = t.get_device()   # -1: not on a CUDA device
+        # what a right tensor passes first; then the messages
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != self._device:
+            self._need(t, shape, dtype, name)
+            self._need_device(t, name)
+
+    def _need_device(self, t, name):
+        """A tensor of the context's device, which the kernels read and write."""
+        index = t.get_device()   # -1: not a CUDA tensor
         if index < 0:
             raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
-        if index != _current_device():
-            raise ValueError("%s: expected a tensor on the current device, cuda:%d, got one on cuda:%d" %
-                             (name, _current_device(), index))
+        if index != self._device:
+            raise ValueError("%s: expected a tensor on the context's device %s, got one on %d" %
+                             (name, self._device, index))
 
     def fkv_tree_workspace_bytes(self, T: int) -> int:
         return int(self._lib.fkv_tree_workspace_bytes(self.handle, T))
@@ -373,7 +376,7 @@ class Context:
         m = MODES[mode] if isinstance(mode, str) else int(mode)
         nbytes = int(getattr(workspace, "nbytes", 0))
         if isinstance(workspace, torch.Tensor):
-            self._need_current(workspace, "workspace")
+            self._need_device(workspace, "workspace")
             if not workspace.is_contiguous():
                 raise ValueError("workspace: expected a contiguous tensor, got strides %s" %
                                  (workspace.stride(),))

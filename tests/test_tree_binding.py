@@ -35,9 +35,9 @@ def _cuda(t, index=0):
 
 
 @pytest.fixture
-def ctx(monkeypatch):
-    monkeypatch.setattr(B, "_current_device", lambda: 0)
+def ctx():
     c = object.__new__(B.Context)
+    c._device = 0
     c.cfg = B.fkv_config(4, 2, 64, 4, 2, 64, B.FKV_BF16, 0, 0.0, 0)
     c.torch_dtype = torch.bfloat16
     c._keep = {}
@@ -74,10 +74,10 @@ def test_a_workspace_that_the_kernel_cannot_write_is_refused(ctx, what):
     ("seq_lens", (2,), torch.int32), ("tree_mask", (2, 5, 1), torch.int64),
     ("node_counts", (2,), torch.int32), ("workspace", (64,), torch.uint8)])
 def test_tensors_of_another_device_are_refused(ctx, name, shape, dtype):
-    """The kernel runs on the current device, whose memory theirs need not be."""
+    """The kernels run on the context's device, which need not reach their memory."""
     other = _cuda(torch.zeros(shape, dtype=dtype), index=1)
     ws = _cuda(torch.zeros(64, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="%s.*current device" % name):
+    with pytest.raises(ValueError, match="%s.*context's device" % name):
         if name == "workspace":
             _tree(ctx, other)
         else:
@@ -85,8 +85,8 @@ def test_tensors_of_another_device_are_refused(ctx, name, shape, dtype):
     i, j = (_cuda(torch.zeros(2, dtype=torch.int32), index=k) for k in (0, 1))
     idx = _cuda(torch.zeros(2, 3, dtype=torch.int32))
     for a, b in ((i, j), (j, i)):
-        with pytest.raises(ValueError, match="current device"):
+        with pytest.raises(ValueError, match="context's device"):
             ctx.fkv_reorder_seqs(a, b, stream=0)
-        with pytest.raises(ValueError, match="current device"):
+        with pytest.raises(ValueError, match="context's device"):
             ctx.fkv_compact_rows(a, idx, b, stream=0)
     assert ctx._lib.calls == []
