@@ -500,18 +500,21 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
 
 size_t fkv_tree_workspace_bytes(const fkv_ctx* c, int T) {
   if (!c || T < 1 || T > kTreeNodes || T > c->cfg.max_seq) return 0;
+  // the largest of all calls with up to T nodes: fewer nodes can have more
+  // partials, since the CTAs of an SM and of a row tile come in whole numbers
   size_t best = 0;
-  for (int kind = 0; kind < 3; ++kind)   // one source, one with weights, two
-    for (int q4 = 0; q4 <= 1; ++q4) {
-      fkv::TreeArgs t = tree_args(c, T);
-      t.q4 = q4;
-      // only whether there are weights and a second source counts here
-      t.a[0] = kind >= 1 ? reinterpret_cast<const float*>(c) : nullptr;
-      t.k[1] = kind == 2 ? c : nullptr;
-      fkv::TreePlan p{};
-      if (fkv::tree_plan(t, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
-        best = p.workspace_bytes;
-    }
+  for (int nodes = 1; nodes <= T; ++nodes)
+    for (int kind = 0; kind < 3; ++kind)   // one source, one with weights, two
+      for (int q4 = 0; q4 <= 1; ++q4) {
+        fkv::TreeArgs t = tree_args(c, nodes);
+        t.q4 = q4;
+        // only whether there are weights and a second source counts here
+        t.a[0] = kind >= 1 ? reinterpret_cast<const float*>(c) : nullptr;
+        t.k[1] = kind == 2 ? c : nullptr;
+        fkv::TreePlan p{};
+        if (fkv::tree_plan(t, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
+          best = p.workspace_bytes;
+      }
   return best;
 }
 

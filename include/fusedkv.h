@@ -299,8 +299,8 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* ctx, const void* q, int layer, int mo
  * All three are made with the context's device current
  * (FKV_ERR_INVALID_ARG otherwise) and can be captured into a CUDA graph. */
 
-/* Bytes of device workspace fkv_tree_attn needs for T nodes per sequence, in
- * any mode and cache format of this context (0 for a T that it refuses). */
+/* Bytes of device workspace fkv_tree_attn needs for up to T nodes per sequence,
+ * in any mode and cache format of this context (0 for a T that it refuses). */
 size_t fkv_tree_workspace_bytes(const fkv_ctx* ctx, int T);
 
 /* Attention of a tree of drafted tokens over a layer's cache.  Sequence b has

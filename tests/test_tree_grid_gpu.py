@@ -37,3 +37,25 @@ def test_fp32_three_row_tiles(D, T, mode):
     s.run()
     assert s.ctx.fkv_get_device_status() == B.FKV_OK
     s.check("three row tiles")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,Bt", [(64, 1, 1), (64, 4, 3), (80, 2, 3), (96, 4, 300), (128, 4, 3), (128, 2, 1024)])
+def test_workspaces_grow_with_the_nodes(dtype, D, G, Bt):
+    """A workspace for T nodes serves every call with fewer."""
+    ctx = B.Context(4, Bt, 4096, 2 * G, 2, D, dtype)
+    sizes = [ctx.fkv_tree_workspace_bytes(T) for T in range(1, 129)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("fmt,D,G,T,fewer", [("bf16", 64, 4, 80, (64, 33, 8)), ("f32", 64, 4, 112, (64, 16, 4)),
+                                             ("q4", 128, 2, 112, (96, 64, 16)), ("f32", 128, 4, 33, (32, 4))])
+def test_the_largest_tree_s_workspace_serves_smaller_ones(fmt, D, G, T, fewer):
+    big = TreeSetup(D=D, G=G, T=T, fmt=fmt, mode="lite", lens=(100, 700, 1200), S=1400)
+    for t in fewer:
+        s = TreeSetup(D=D, G=G, T=t, fmt=fmt, mode="lite", lens=(100, 700, 1200), S=1400)
+        want = s.run().clone()
+        s.ws = big.ws
+        s.out.fill_(-77)
+        assert torch.equal(s.run(), want)
+        assert s.ctx.fkv_get_device_status() == B.FKV_OK
