@@ -65,6 +65,30 @@ fkv_status check_config(const fkv_config* c) {
   return FKV_OK;
 }
 
+// The per-layer entries of a new context; false where the host has no memory
+// for them (no exception may leave a C entry).
+bool size_layers(fkv_ctx* c) {
+  const size_t rows = (size_t)c->cfg.num_layers + 1;
+  try {
+    c->k.assign(rows, nullptr);
+    c->v.assign(rows, nullptr);
+    for (auto& w : c->w) w.assign(rows, nullptr);
+    c->window.assign(rows, 0);
+    c->q4.assign(rows, 0);
+    c->ring.assign(rows, 0);
+    for (auto& m : c->maps) m.assign(rows, fkv::TileMaps{});
+    c->lite_src[0].assign(rows, c->n);  // K^n
+    c->lite_src[1].assign(rows, 1);     // V^1
+    c->fused_src[0].assign(rows, 1);
+    c->fused_src[1].assign(rows, c->n);
+    c->fused_src[2].assign(rows, 1);
+    c->fused_src[3].assign(rows, c->n);
+  } catch (...) {
+    return false;
+  }
+  return true;
+}
+
 // Tensor maps of a layer's planes, remade whenever its buffers or rows change.
 void remake_maps(fkv_ctx* c, int layer) {
   for (int kv = 0; kv < 2; ++kv) {
@@ -288,19 +312,10 @@ fkv_status fkv_create(const fkv_config* cfg, fkv_ctx** out) {
   c->n = cfg->num_layers / 2;
   c->group = cfg->num_q_heads / cfg->num_kv_heads;
   c->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt((float)cfg->head_dim);
-  c->k.assign(cfg->num_layers + 1, nullptr);
-  c->v.assign(cfg->num_layers + 1, nullptr);
-  for (auto& w : c->w) w.assign(cfg->num_layers + 1, nullptr);
-  c->window.assign(cfg->num_layers + 1, 0);
-  c->q4.assign(cfg->num_layers + 1, 0);
-  c->ring.assign(cfg->num_layers + 1, 0);
-  for (auto& m : c->maps) m.assign(cfg->num_layers + 1, fkv::TileMaps{});
-  c->lite_src[0].assign(cfg->num_layers + 1, c->n);  // K^n
-  c->lite_src[1].assign(cfg->num_layers + 1, 1);     // V^1
-  c->fused_src[0].assign(cfg->num_layers + 1, 1);
-  c->fused_src[1].assign(cfg->num_layers + 1, c->n);
-  c->fused_src[2].assign(cfg->num_layers + 1, 1);
-  c->fused_src[3].assign(cfg->num_layers + 1, c->n);
+  if (!size_layers(c)) {
+    delete c;
+    return FKV_ERR_INVALID_ARG;
+  }
   c->status = nullptr;
   c->wait_limit = nullptr;
   const unsigned long long limit = kDefaultWaitLimitNs;

@@ -91,7 +91,8 @@ typedef struct fkv_ctx fkv_ctx;
 /* Create a context for the current CUDA device.  Validates the config
  * (FKV_ERR_INVALID_ARG / FKV_ERR_UNSUPPORTED before touching CUDA), then
  * queries the device and allocates its 16 bytes of device words, the status
- * word and the wait limit (FKV_ERR_CUDA on failure, e.g. no GPU).  *out is
+ * word and the wait limit (FKV_ERR_CUDA on failure, e.g. no GPU).  Host memory
+ * that does not suffice for the layers is FKV_ERR_INVALID_ARG.  *out is
  * set to NULL on any error. */
 fkv_status fkv_create(const fkv_config* cfg, fkv_ctx** out);
 
