@@ -284,6 +284,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_tt(int M, int N) {
   return idesc_bf16(M, N, true) | (1u << 15);
 }
 
+// An instruction descriptor as above with fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_with_f16(uint32_t idesc_bf16) {
+  return idesc_bf16 & ~((1u << 7) | (1u << 10));
+}
+
 // Byte offset of the 16-byte chunk `lc` of row `r` inside one 64-byte-swizzled
 // block whose rows are 64 bytes (the pattern TMA writes and the MMA reads).
 __device__ __forceinline__ uint32_t swz64(int r, int lc) {

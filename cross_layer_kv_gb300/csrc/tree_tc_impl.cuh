@@ -33,12 +33,17 @@
 //    key's columns, 16 bytes at a time, without bank conflicts).
 // 4-bit caches: the producer copies a tile's records (one contiguous run) to a
 // second ring, and two more warpgroups dequantise them into the slots, two
-// values an instruction: a nibble pair under the exponent of 128 is 128 + code
-// in bf16, exactly; less 128, times the scale, plus the minimum in one FMA is
-// the record's value rounded once to bf16 (2^-9 of it, the library's choice
-// for the tensor cores; decode keeps fp32).  The pairs that fall out of a word
-// are channels e and e + 4 of eight, so the tiles hold the channels in the
-// order 0 4 1 5 2 6 3 7 and so do the queries; the epilogue undoes it.
+// values an instruction: a nibble pair under the exponent of 64 is 64 + code / 16
+// in fp16, exactly; less 64, times 16 * scale, plus the minimum in one FMA is
+// the record's value rounded once to fp16.  Queries and P are fp16 then too:
+// each operand is off by 2^-11 of itself, so that the output's error is its own
+// rounding's (bf16 operands gave twice that, 3.4e-3).  fp16's range is the price:
+// keys and values up to 2^14 (16 * scale stays finite), beside an error of
+// 3 * 2^-25 (scale, minimum and value, each below 2^-14); a query row that leaves
+// it is held times a power of two.
+// The pairs that fall out of a word are channels e and e + 4 of eight, so the
+// tiles hold the channels in the order 0 4 1 5 2 6 3 7 and so do the queries; the
+// epilogue undoes it.
 //
 // What bounds it (one GB300, against 6.78 TB/s of measured copy bandwidth; bytes
 // are the cached rows once): HBM from 32 columns and 160-byte rows on (4B lite,
@@ -59,6 +64,8 @@
 #include <cfloat>
 #include <cstring>
 #include <type_traits>
+
+#include <cuda_fp16.h>
 
 #include "tc_device.cuh"
 #include "tree_common.cuh"
@@ -84,10 +91,11 @@ struct TcCfg {
   static constexpr int CB = (D + SWC - 1) / SWC;         // 64-channel blocks
   static constexpr int SLOT = CB * KT * SWB;             // one K or V tile
   // the queries, or per source the high and low halves of query times weight
-  // (the high half alone over 4-bit caches, whose keys are rounded to bf16 too:
-  // both halves took 186 us instead of 159 at 332M fused, T = 16, and the
-  // output's error from 3.5e-3 to 3.0e-3)
+  // (over 4-bit caches one fp16, whose rounding is an eighth of bf16's)
   static constexpr int NQ = WGT && !Q4 ? 2 : 1;
+  // How far the probabilities' exponents are raised (4-bit caches): 2^4 at the
+  // reference, so that what fp16 loses below 2^-25 is below 2^-29 of a column's sum.
+  static constexpr float RAISE = Q4 ? 4.f : 0.f;
   static constexpr int Q_BYTES = NSRC * NQ * CB * NC * SWB;
   static constexpr int P_BYTES = (NC + SWC - 1) / SWC * KT * SWB;
   static constexpr int NW = (NC + 31) / 32;              // 32-bit words of a column mask
@@ -117,8 +125,8 @@ struct TcCfg {
                                    : TMEM_USED <= 256 ? 256 : 512;
   static_assert(TMEM_USED <= 512, "tensor memory");
   // barriers and words, then the arrays of floats and masks
-  static constexpr int BAR_BYTES = ((2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 11 * 8 + 6 * 4 + 127) / 128 * 128;
-  static constexpr int ARRAY_BYTES = NC * 4 * 8 + kTreeMaxNodes * (16 + 4 + NW * 4);
+  static constexpr int BAR_BYTES = ((2 * MAX_SLOTS + 2 * MAX_RAW) * 8 + 11 * 8 + 7 * 4 + 127) / 128 * 128;
+  static constexpr int ARRAY_BYTES = NC * 4 * 8 + kTreeMaxNodes * (16 + 4 + NW * 4) + (Q4 ? NC * 4 : 0);
   static constexpr int RAW = KT * q4_row_bytes(D);       // records of a tile
   // two P buffers where at least five tile slots remain beside them (4-bit
   // caches: the four that the dequantising groups need, with four of records
@@ -198,6 +206,21 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, unsigned
 // The 128 threads of softmax warpgroup wg.
 __device__ __forceinline__ void wg_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); }
 
+// Two floats as fp16 or bf16.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (F16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// 2^n, |n| <= 126.
+__device__ __forceinline__ float exp2_int(int n) { return __int_as_float((127 + n) << 23); }
+
 // Slot (counted from a piece's first, in tiles of one tensor) of the values of
 // tile i of a piece's n: the order is K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
 __device__ __forceinline__ int v_slot(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 + 2 * i; }
@@ -230,6 +253,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
   int* sm_issued = reinterpret_cast<int*>(tmem_slot + 2);
   int* merge_flag = sm_issued + 1;
   int* sm_span = merge_flag + 1;                               // [2] least and largest depth
+  volatile int* sm_scaled = sm_span + 2;                       // one of them is not 1 (sCol)
   float* sRef = reinterpret_cast<float*>(smem + C::REF_OFF);   // [NC] negated reference
   float* sAlpha = sRef + NC;                                   // [NC] rescale, then weight
   int* sDepth = reinterpret_cast<int*>(sAlpha + NC);           // [NC] depth of the column's node
@@ -238,7 +262,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
   unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sWarp + 4 * NC);   // [nodes][2]
   int* sNodeDepth = reinterpret_cast<int*>(sMask + 2 * kTreeMaxNodes);   // [nodes]
   uint32_t* sVis = reinterpret_cast<uint32_t*>(sNodeDepth + kTreeMaxNodes);   // [nodes][NW]
-  const TreeSeqs sq = tree_seqs(reinterpret_cast<int*>(sVis + kTreeMaxNodes * NW), p.B);
+  float* sCol = reinterpret_cast<float*>(sVis + kTreeMaxNodes * NW);   // [NC] powers of two of the query rows (4-bit)
+  const TreeSeqs sq = tree_seqs(reinterpret_cast<int*>(sCol + (Q4 ? NC : 0)), p.B);
   uint8_t* sRing = smem + C::ring_off(p.B);
   uint8_t* sRaw = sRing + (size_t)nslots * C::SLOT;
 
@@ -263,6 +288,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
     *sm_issued = 0;
+    *sm_scaled = 0;
     fence_mbar_init();
   }
   if (warp == C::QK_WARP) tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -370,7 +396,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
       constexpr int GR = D / kQ4Group, RB = q4_row_bytes(D);
       constexpr int GROUPS = DQ_THREADS / DQ_GROUP;
       const int t = (tid - C::DQ_WARP * 32) % DQ_GROUP;
-      const __nv_bfloat162 bias = __floats2bfloat162_rn(-128.f, -128.f);
+      const __half2 bias = __floats2half2_rn(-64.f, -64.f);
       const long long total = (walk.t1 - walk.t) * 2 * NSRC;
       int sl = 0, r = 0;
       uint32_t turn = 1, rturn = 0;   // parities of the slot's last release and of the records' filling
@@ -392,30 +418,29 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
         if (!await(&raw_full[r], rturn) || (g >= nslots && !await(&empty[sl], turn))) break;
         const uint8_t* rec = sRaw + (size_t)r * C::RAW;
         uint8_t* dst = slot_ptr(sl);
-#pragma unroll 4
+        auto eight = [&](int row, int ch, uint32_t w, __half2 sc, __half2 lo) {   // channels of a row
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = ((w >> (4 * e)) & 0x000f000fu) | 0x54005400u;
+            const __half2 v = __hfma2(__hadd2(*reinterpret_cast<const __half2*>(&x), bias), sc, lo);
+            o[e] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * KT * SWB + swz128(row, ch & 7)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        };
+        // Four roles' loops share the instruction cache: 332M fused, T = 16, took
+        // 137 us unrolled twice, 141 not at all, 152 four times, 169 eight times.
+#pragma unroll 2
         for (int k = 0; k < KT * GR / DQ_GROUP; ++k) {   // a multiple: KT = 2 * DQ_GROUP
           const int it = t + k * DQ_GROUP;
           const int row = it / GR, gr = it - row * GR;
           const uint2 codes = *reinterpret_cast<const uint2*>(rec + row * RB + gr * 8);
           const uint32_t prm = *reinterpret_cast<const uint32_t*>(rec + row * RB + D / 2 + gr * 4);
-          const uint32_t s2 = __byte_perm(prm, 0, 0x1010), m2 = __byte_perm(prm, 0, 0x3232);
-          const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-          const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&m2);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = h ? codes.y : codes.x;
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t x = ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u;
-              const __nv_bfloat162 v =
-                  __hfma2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), bias), sc, lo);
-              o[e] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            const int ch = gr * 2 + h;
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * KT * SWB + swz128(row, ch & 7)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          const __half2 both = __floats2half2_rn(bf16lo(prm) * 16.f, bf16hi(prm));
+          const __half2 sc = __low2half2(both), lo = __high2half2(both);
+          eight(row, gr * 2, codes.x, sc, lo);
+          eight(row, gr * 2 + 1, codes.y, sc, lo);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -428,8 +453,8 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
     }
   } else if (active && (warp == C::QK_WARP || warp == C::PV_WARP)) {
     // ---------------- MMA issuers (the whole warp; one lane issues) ----------------
-    constexpr uint32_t IDESC_QK = idesc_bf16(KT, NC, false);
-    constexpr uint32_t IDESC_PV = idesc_bf16_tt(128, NC);
+    constexpr uint32_t IDESC_QK = Q4 ? idesc_with_f16(idesc_bf16(KT, NC, false)) : idesc_bf16(KT, NC, false);
+    constexpr uint32_t IDESC_PV = Q4 ? idesc_with_f16(idesc_bf16_tt(128, NC)) : idesc_bf16_tt(128, NC);
     const bool qk = warp == C::QK_WARP;
     // descriptors of slot 0 as K (K-major) and as V^T (MN-major), of Q and P
     const SDesc128 da = qk ? sdesc128(smem_u32(sRing), 16, 8 * SWB)
@@ -553,38 +578,64 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
         const int r = it / (CB * 8), ch = it - r * (CB * 8);   // 16-byte chunk of a row
         const int d = ch * 8;
         uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < rows && d < D)
+        if (r < rows && d < D && (!Q4 || sNode[r] < N))
           w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                               (unit * p.G * p.T + rt * NC + r) * D + d);
         float f[8];
         unpack16<__nv_bfloat16>(w, f);
-        if constexpr (Q4)   // the order of the tiles' channels: 0 4 1 5 2 6 3 7
-          w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
-                         __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+        auto place = [&](int src) { return sQ + src * C::NQ * CB * NC * SWB + (ch >> 3) * NC * SWB + swz128(r, ch & 7); };
+        if constexpr (Q4) {
+          // fp16, times a power of two where the row does not lie in its range
+          float x[NSRC][8], top = 0.f;
 #pragma unroll
-        for (int src = 0; src < NSRC; ++src) {
-          uint8_t* dst = sQ + src * C::NQ * CB * NC * SWB + (ch >> 3) * NC * SWB + swz128(r, ch & 7);
-          if constexpr (WGT) {
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-            if (d < D) {
-              const float4* ap = reinterpret_cast<const float4*>(p.a[src] + (size_t)pc.h * D + d);
-              const float4 a0 = ap[0], a1 = ap[1];
-              const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          for (int src = 0; src < NSRC; ++src)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int e0 = Q4 ? e : 2 * e, e1 = Q4 ? e + 4 : 2 * e + 1;
-                const float x0 = f[e0] * av[e0], x1 = f[e1] * av[e1];
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
-                hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
-                const __nv_bfloat162 l2 = __floats2bfloat162_rn(x0 - bf16lo(hi[e]), x1 - bf16hi(hi[e]));
-                lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
-              }
+            for (int e = 0; e < 8; ++e) {
+              x[src][e] = f[e];
+              if (WGT && d < D) x[src][e] *= p.a[src][(size_t)pc.h * D + d + e];
+              top = fmaxf(top, fabsf(x[src][e]));
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (C::NQ == 2)
+#pragma unroll
+          for (int o = 1; o < CB * 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // the row's largest is left in 2^-6 .. 2^14, else brought to 1 .. 2
+          int ex = 0;
+          if (top > 0.f && top < INFINITY && !(top >= 0.015625f && top <= 16384.f))
+            ex = min(max((__float_as_int(top) >> 23) - 127, -126), 126);
+          if (ch == 0) sCol[r] = exp2_int(ex);
+          if (ex != 0) *sm_scaled = 1;
+          const float down = exp2_int(-ex);
+#pragma unroll
+          for (int src = 0; src < NSRC; ++src) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)   // the order of the tiles' channels: 0 4 1 5 2 6 3 7
+              o[e] = pack2<true>(x[src][e] * down, x[src][e + 4] * down);
+            *reinterpret_cast<uint4*>(place(src)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        } else {
+#pragma unroll
+          for (int src = 0; src < NSRC; ++src) {
+            uint8_t* dst = place(src);
+            if constexpr (WGT) {
+              uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+              if (d < D) {
+                const float4* ap = reinterpret_cast<const float4*>(p.a[src] + (size_t)pc.h * D + d);
+                const float4 a0 = ap[0], a1 = ap[1];
+                const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float x0 = f[2 * e] * av[2 * e], x1 = f[2 * e + 1] * av[2 * e + 1];
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+                  hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                  const __nv_bfloat162 l2 = __floats2bfloat162_rn(x0 - bf16lo(hi[e]), x1 - bf16hi(hi[e]));
+                  lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
+                }
+              }
+              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
               *reinterpret_cast<uint4*>(dst + CB * NC * SWB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint4*>(dst) = w;
+            } else {
+              *reinterpret_cast<uint4*>(dst) = w;
+            }
           }
         }
       }
@@ -634,6 +685,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
       if (lane == 0) mbar_arrive(q_ready);
       sm_sync();
       const int least = sm_span[0], most = sm_span[1];
+      const bool scaled = Q4 && *sm_scaled;
 
       // the piece's tiles that need masks: from `tail` on (drafted rows, a ragged
       // end), the ragged one before a ring's end, and up to `edge` (rows that the
@@ -657,6 +709,18 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
         ok = ok && await(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
         tc_fence_after();
         const uint32_t t_s = t_lane + (j & 1) * NC;
+        if (Q4 && scaled) {
+#pragma unroll 1
+          for (int c = 0; c < HC; c += 8) {
+            float v[8];
+            tmem_ld8(t_s + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= sCol[c0 + c + e];
+            tmem_st8(t_s + c, v);
+          }
+          tmem_wait_st();
+        }
         // uniform over the CTA: rows that some column does not see
         const bool masked = i >= tail || i == seam || i < edge;
         TreeTile t{0, 0, KT};
@@ -679,6 +743,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
             ok = ok && await(&full[g % nslots], (uint32_t)(g / nslots) & 1u);
           }
           bool seen = false;
+          constexpr uint32_t INF16 = Q4 ? 0x7c00u : 0x7f80u;   // exponents of fp16, bf16
           if (key < t.cnt) {
             if (q < 0) {
               seen = p.window == 0 || least < q + p.window;
@@ -696,7 +761,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
                   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
-                    poison |= (xs[e] & 0x7f80u) == 0x7f80u || (xs[e] & 0x7f800000u) == 0x7f800000u;
+                    poison |= (xs[e] & INF16) == INF16 || (xs[e] & INF16 << 16) == INF16 << 16;
                 }
               }
             }
@@ -771,7 +836,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
           if ((tid & 127) < HC) {
             const int c = c0 + (tid & 127);
             const float m = fmaxf(fmaxf(sWarp[c], sWarp[NC + c]), fmaxf(sWarp[2 * NC + c], sWarp[3 * NC + c]));
-            const float old = -sRef[c], top = fmaxf(old, m * p.scale_log2);
+            const float old = -sRef[c], top = fmaxf(old, m * p.scale_log2 - C::RAISE);
             sAlpha[c] = fast_exp2(old - top);
             sRef[c] = -top;
           }
@@ -803,7 +868,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
           }
         }
 
-        // P of this key: 2^x, bf16
+        // P of this key: 2^x, 16 bits
         const int pj = NPB == 2 ? j - 2 : j - 1;   // the tile whose products read the buffer last
         ok = ok && (pj < 0 || products(pj));
         uint8_t* pb = sP + (NPB == 2 ? (j & 1) * C::P_BYTES : 0);
@@ -820,8 +885,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
             for (int e = h; e < h + 8; e += 2) {
               const float e0 = fast_exp2(sv[e]), e1 = fast_exp2(sv[e + 1]);
               add2(l[c + e], l[c + e + 1], e0, e1);
-              const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
-              w[(e - h) / 2] = *reinterpret_cast<const uint32_t*>(&v2);
+              w[(e - h) / 2] = pack2<Q4>(e0, e1);
             }
             const int cc = c0 + c + h;
             *reinterpret_cast<uint4*>(pb + (cc >> 6) * KT * SWB + swz128(key, (cc & 63) >> 3)) =
@@ -910,6 +974,7 @@ __global__ void __launch_bounds__(TcCfg<D, NSRC, WGT, NC, Q4>::THREADS, 1)
       if (!whole)
         tree_publish<__nv_bfloat16, D, NC, C::SM>(p, cut, sq.pre, pc.b, pc.h, N, tid, merge_flag, sWarp,
                                                        sm_sync);
+      if (tid == 0) *sm_scaled = 0;
       sm_sync();   // shared words are free for the next piece
       base += 2 * n * NSRC;
       jt += n;

@@ -311,7 +311,8 @@ size_t fkv_tree_workspace_bytes(const fkv_ctx* ctx, int T);
  * row of node j where bit j % 64 of tree_mask[b][i][j / 64] is set: for a tree,
  * its ancestors and itself, though any mask is taken (bits of nodes that do
  * not exist are ignored).  A node that sees nothing (P = 0 and no bit) gets
- * zeros.  T = 1 with bit 0 set is fkv_decode_attn with length P + 1.
+ * zeros.  T = 1 with bit 0 set computes what fkv_decode_attn does with length
+ * P + 1, up to the roundings below.
  * Modes and sources are those of fkv_decode_attn, over bf16, fp32 and 4-bit
  * caches.  Sliding windows: the depth of a node is the number of its set bits
  * less one (0 where none or one is set), its position P + depth, and with a
@@ -333,8 +334,11 @@ size_t fkv_tree_workspace_bytes(const fkv_ctx* ctx, int T);
  * and does not reach the others.
  * Rounding: fp32 caches, fp32 throughout; bf16 caches, probabilities to bf16
  * and query times key weight to two bf16 halves, as operands of the tensor
- * cores; 4-bit caches also keys, values and query times weight to one bf16.
- * Sums and softmax statistics are fp32.
+ * cores; 4-bit caches, keys, values, probabilities and query times weight to
+ * one fp16 (a query row outside its range times a power of two; keys and values
+ * above 2^14 in magnitude may count as not finite, and an error of 2^-23 stays
+ * in them however small they are).  Sums and softmax statistics are fp32; scores
+ * of 2^27 and more are not resolved over bf16 and 4-bit caches.
  * workspace: device, 16-byte aligned, at least fkv_tree_workspace_bytes(ctx,
  * T) bytes, no initialisation, as for fkv_decode_attn (also its note on graph
  * replays that stopped early); not shared with a call that may run at the same
