@@ -20,8 +20,8 @@ namespace {
 // chunks fit 8 a lane, else a CTA of 128 threads that splits wide rows by
 // columns (a move keeps the column, so columns are independent).  Measured:
 // 332M, 32 sequences, up to 5 rows 3.8 us on the device; 4B, 8 sequences, up
-// to 12 rows of 18 layers 5.3 us; a call from Python 7.4 and 7.9 us, of which
-// the host takes 6.
+// to 12 rows of 18 layers 5.3 us; calls from Python one after another 6 to 7 us,
+// the host's time.
 
 constexpr int kMoveThreads = 128;
 constexpr int kMoveItems = 8;   // chunks a thread holds
@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
 // copies).  Items touch disjoint bytes, so cycles need no scratch memory, each
 // source is read once and each destination written once: HBM traffic is the
 // floor.  One warp per SM keeps the copy engines busy: 332M, 8 prompts of 4
-// beams, up to 2048 rows 99 us, 4B, one prompt forked over 8192 rows 334 us,
-// both within a tenth of the measured copy bandwidth.
+// beams, up to 2048 rows 96 us (88% of the measured copy bandwidth), 4B, one
+// prompt forked over 8192 rows 334 to 347 us (91 to 95%; 364 and 427 us on two other
+// devices of the same kind).
 
 constexpr int kReorderSmem = 200 * 1024;
 constexpr int kReorderStages = 8;

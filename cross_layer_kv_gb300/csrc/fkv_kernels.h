@@ -188,7 +188,7 @@ struct TreeArgs {
 
 // Launch configuration of a tree attention call.
 struct TreePlan {
-  bool tensor;      // the tensor-core kernel (tree_tc.cu), else tree_f32.cu
+  bool tensor;      // the tensor-core kernel (tree_tc_impl.cuh), else tree_f32.cu
   int slots;        // its key / value tile slots
   int raw_slots;    // its slots of 4-bit records
   int ranges;       // key ranges (grid.x)

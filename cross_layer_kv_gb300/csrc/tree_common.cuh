@@ -141,10 +141,15 @@ __device__ __forceinline__ int tree_depth(const TreeParams& p, int b, int i, int
 // The cut: the tiles of all units, unit by unit, in `ranges` equal contiguous
 // ranges.  Where ranges would be short (six tiles and fewer), a boundary within
 // `snap` tiles of a unit's start or end moves there: on the tensor cores,
-// writing, announcing and merging a partial takes as long as four to six tiles
-// (snap = 3: 650M ring layer, 32 units of five tiles, 19.5 -> 18.1 us; other
-// short calls 25 -> 20, 35 -> 30, 20 -> 23 us).  fp32 tiles take longer than a
-// merge (snap = 0: 12.5 us a tiny call, 19.3 with 3).  Fills sq, and zeros the
+// writing, announcing and merging a partial takes as long as four to six tiles.
+// Measured with snap = 0 and 3 (lite unless said): 32 units of 5 tiles 14.1 and
+// 12.1 us, 64 of 6 19.5 and 11.5, 256 of 3 23.3 and 17.2, 32 of 12 27.2 and 18.6
+// (fused 34.7 and 27.8), fused 128 of 7 25.4 and 16.3.  It loses where few units
+// of dear tiles leave most CTAs without work: fused 16 units of 17 tiles 17.5 and
+// 20.0 us, 16 of 10 19.6 and 20.8; lite units like these still gain (8 of 32
+// tiles 20.6 and 18.7, 16 of 9 13.9 and 13.5), so the rule asks for neither the
+// units nor the sources.  fp32 tiles take longer than a merge (snap = 0: 12.5 us
+// a tiny call, 19.3 with 3).  Fills sq, and zeros the
 // output of the sequences whose lengths are out of range; every thread of the
 // CTA takes part.
 struct TreeCut {

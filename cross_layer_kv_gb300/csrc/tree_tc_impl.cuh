@@ -48,12 +48,14 @@
 // What bounds it (one GB300, against 6.78 TB/s of measured copy bandwidth; bytes
 // are the cached rows once): HBM from 32 columns and 160-byte rows on (4B lite,
 // T = 16: 2.0 GB in 300 us; 1.5B fused, T = 26: 3.2 GB in 460 us).  With 128
-// columns the softmax's issue slots (332M fused, T = 64: 0.82 GB in 207 us, 44%
-// of the slots used, tensor pipe 34%); with 16 columns the end of a unit, which
+// columns the softmax's chain of short dependent steps (tensor-memory loads, a
+// vote, exponentials, shared stores) beside instruction fetch: no pipe is near its
+// limit (332M fused, T = 64: 0.82 GB in 206 us, 44% of the issue slots, 34% of
+// the tensor pipe).  With 16 columns the end of a unit, which
 // the ring's 192 KB of tiles hides only in part (332M lite, T = 8: 0.40 GB in
-// 75 us); over 4-bit caches the dequantisation beside the softmax (332M fused,
-// T = 16: 0.30 GB in 150 us, 52% of the slots); short calls their chain of
-// prologue, first tile, merge (650M ring layer, T = 12: 18 us).
+// 75 us, 26% of the slots); over 4-bit caches the dequantisation beside the
+// softmax (332M fused, T = 16: 0.30 GB in 137 us, 54% of the slots); short calls
+// their chain of prologue, first tile, merge (650M ring layer, T = 12: 18 us).
 //
 // Tiles with drafted rows, a window's edge or a ragged end are masked, and the
 // value rows that nobody sees are zeroed in shared memory, since 0 * NaN is
