@@ -27,7 +27,8 @@ struct fkv_ctx {
   std::vector<int> lite_src[2];            // lite / scaled sources: K, V
   std::vector<int> fused_src[4];           // fused sources: K first, K second, V first, V second
   std::vector<int> window;                 // sliding window per layer (0: full attention)
-  std::vector<char> q4;                    // layer cache holds 4-bit records
+  std::vector<char> format;                // fkv::CacheFormat of the layer's cache
+  std::vector<float*> ks, vs;              // scales of 8-bit caches
   std::vector<int> ring;                   // > 0: the layer's caches are rings of that many rows
   std::vector<fkv::TileMaps> maps[2];      // tensor maps of the bound bf16 K, V planes (tree attention)
 };
@@ -74,7 +75,9 @@ bool size_layers(fkv_ctx* c) {
     c->v.assign(rows, nullptr);
     for (auto& w : c->w) w.assign(rows, nullptr);
     c->window.assign(rows, 0);
-    c->q4.assign(rows, 0);
+    c->format.assign(rows, fkv::kCachePlain);
+    c->ks.assign(rows, nullptr);
+    c->vs.assign(rows, nullptr);
     c->ring.assign(rows, 0);
     for (auto& m : c->maps) m.assign(rows, fkv::TileMaps{});
     c->lite_src[0].assign(rows, c->n);  // K^n
@@ -95,7 +98,7 @@ void remake_maps(fkv_ctx* c, int layer) {
     void* ptr = kv ? c->v[layer] : c->k[layer];
     fkv::TileMaps& m = c->maps[kv][layer];
     m.valid = false;
-    if (!ptr || c->q4[layer] || c->cfg.dtype != FKV_BF16) continue;
+    if (!ptr || c->format[layer] != fkv::kCachePlain || c->cfg.dtype != FKV_BF16) continue;
     const int rows = c->ring[layer] > 0 ? c->ring[layer] : c->cfg.max_seq;
     fkv::tile_maps(&m, ptr, c->cfg.head_dim, rows, (long long)c->cfg.batch * c->cfg.num_kv_heads);
   }
@@ -151,30 +154,44 @@ fkv_status resolve_sources_impl(const fkv_ctx* c, int layer, int mode, const voi
   return FKV_OK;
 }
 
-// Sources and their storage format: *q4 = 1 if every source layer holds
-// 4-bit records, 0 if none does; *ring = the row count of the sources' ring
-// caches, 0 if they are full-length.  A mix of formats or of ring sizes is
-// FKV_ERR_UNSUPPORTED (the sources of a call are read at the same rows).
+// Sources and their storage format (*format, one of fkv::CacheFormat); *ring =
+// the row count of the sources' ring caches, 0 if they are full-length.  A mix
+// of formats or of ring sizes is FKV_ERR_UNSUPPORTED (the sources of a call
+// are read at the same rows), and so are 8-bit rings that are not whole blocks.
 fkv_status resolve_sources(const fkv_ctx* c, int layer, int mode, const void* k[2],
                            const void* v[2], const float* a[2], const float* b[2], int* nsrc,
-                           int* q4, int* ring, int* layers = nullptr) {
+                           int* format, int* ring, int* layers = nullptr) {
   int own[4];
   int* src = layers ? layers : own;   // source layers: K first, K second, V first, V second
   const fkv_status s = resolve_sources_impl(c, layer, mode, k, v, a, b, nsrc, src);
   if (s != FKV_OK) return s;
-  int nq = 0, nt = 0, r = -1;
+  int f = -1, r = -1;
   for (int i = 0; i < 4; ++i) {
     if (src[i] <= 0) continue;
-    ++nt;
-    nq += c->q4[src[i]] ? 1 : 0;
+    if (f >= 0 && c->format[src[i]] != f) return FKV_ERR_UNSUPPORTED;
     if (r >= 0 && c->ring[src[i]] != r) return FKV_ERR_UNSUPPORTED;
+    f = c->format[src[i]];
     r = c->ring[src[i]];
   }
-  if (nq != 0 && nq != nt) return FKV_ERR_UNSUPPORTED;
-  *q4 = nq ? 1 : 0;
+  if (f == fkv::kCacheQ8 && r % fkv::kQ8Block != 0) return FKV_ERR_UNSUPPORTED;
+  *format = f;
   *ring = r > 0 ? r : 0;
   return FKV_OK;
 }
+
+// Scales of the source layers of a call over 8-bit caches (as resolve_sources
+// gives them; entry 0 of a context's layers is null).
+void source_scales(const fkv_ctx* c, const int src[4], const float* ks[2], const float* vs[2]) {
+  for (int i = 0; i < 2; ++i) {
+    ks[i] = c->ks[src[i]];
+    vs[i] = c->vs[src[2 + i]];
+  }
+}
+
+// An append that goes round a ring starts the scale of the block it comes to,
+// and up to kQ8Block - 1 older rows of that block are lost with it: positions
+// that a call still sees must not be among them.
+constexpr int kQ8Lost = fkv::kQ8Block - 1;
 
 fkv::DecodeArgs decode_args(const fkv_ctx* c) {
   fkv::DecodeArgs d{};
@@ -235,7 +252,7 @@ fkv_status for_bound_planes(const fkv_ctx* c, Launch launch) {
       any = true;
       tb.plane[tb.planes] = ptr;
       tb.rows[tb.planes] = c->ring[l] > 0 ? c->ring[l] : c->cfg.max_seq;
-      tb.row_bytes[tb.planes] = c->q4[l] ? fkv::q4_row_bytes(c->cfg.head_dim)
+      tb.row_bytes[tb.planes] = c->format[l] == fkv::kCacheQ4 ? fkv::q4_row_bytes(c->cfg.head_dim)
                                          : c->cfg.head_dim * elem_bytes(c->cfg);
       if (++tb.planes == fkv::kMovePlanes) {
         if (launch(tb) != cudaSuccess) return FKV_ERR_CUDA;
@@ -244,6 +261,14 @@ fkv_status for_bound_planes(const fkv_ctx* c, Launch launch) {
     }
   if (tb.planes > 0 && launch(tb) != cudaSuccess) return FKV_ERR_CUDA;
   return any ? FKV_OK : FKV_ERR_INVALID_ARG;
+}
+
+// Whether a layer with bound caches holds 8-bit codes (whose rows share scales
+// and so cannot be moved one by one).
+bool any_q8(const fkv_ctx* c) {
+  for (int l = 1; l <= c->cfg.num_layers; ++l)
+    if (c->k[l] && c->format[l] == fkv::kCacheQ8) return true;
+  return false;
 }
 
 // Whether the context's device is the calling thread's current one.
@@ -265,17 +290,20 @@ fkv_status decode_attn_impl(fkv_ctx* c, const void* q, int layer, int mode,
                             size_t workspace_bytes, void* stream, bool clear_counts) {
   if (!c) return FKV_ERR_INVALID_ARG;
   fkv::DecodeArgs d = decode_args(c);
-  int q4 = 0, ring = 0;
-  fkv_status s = resolve_sources(c, layer, mode, d.k, d.v, d.a, d.b, &d.nsrc, &q4, &ring);
+  int format = 0, ring = 0, src[4];
+  fkv_status s = resolve_sources(c, layer, mode, d.k, d.v, d.a, d.b, &d.nsrc, &format, &ring, src);
   if (s != FKV_OK) return s;
   // ring caches hold the last `ring` positions: the layer must attend within them
   if (ring > 0 && (c->window[layer] < 1 || c->window[layer] > ring)) return FKV_ERR_INVALID_ARG;
+  if (ring > 0 && format == fkv::kCacheQ8 && c->window[layer] > ring - kQ8Lost) return FKV_ERR_UNSUPPORTED;
   if (!q || !out || !seq_lens || !aligned16(q) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
     return FKV_ERR_INVALID_ARG;
   fkv::DecodePlan plan{};
-  const cudaError_t pe = q4 ? fkv::decode_q4_plan(d, c->num_sms, &plan)
-                            : fkv::decode_plan(d, c->num_sms, &plan);
+  const bool q4 = format == fkv::kCacheQ4, q8 = format == fkv::kCacheQ8;
+  const cudaError_t pe = q8   ? fkv::decode_q8_plan(d, c->num_sms, &plan)
+                         : q4 ? fkv::decode_q4_plan(d, c->num_sms, &plan)
+                              : fkv::decode_plan(d, c->num_sms, &plan);
   if (pe != cudaSuccess) return FKV_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) || workspace_bytes < plan.workspace_bytes)
     return FKV_ERR_WORKSPACE;
@@ -286,6 +314,7 @@ fkv_status decode_attn_impl(fkv_ctx* c, const void* q, int layer, int mode,
   d.window = c->window[layer];
   d.ring = ring;
   d.epoch = next_epoch();
+  source_scales(c, src, d.k_scale, d.v_scale);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_counts &&
       cudaMemsetAsync(static_cast<char*>(workspace) + plan.partial_bytes, 0,
@@ -293,7 +322,9 @@ fkv_status decode_attn_impl(fkv_ctx* c, const void* q, int layer, int mode,
     cudaGetLastError();
     return FKV_ERR_CUDA;
   }
-  const cudaError_t e = q4 ? fkv::decode_q4_launch(d, plan, st) : fkv::decode_launch(d, plan, st);
+  const cudaError_t e = q8   ? fkv::decode_q8_launch(d, plan, st)
+                        : q4 ? fkv::decode_q4_launch(d, plan, st)
+                             : fkv::decode_launch(d, plan, st);
   return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
@@ -347,7 +378,7 @@ fkv_status fkv_bind_layer_cache(fkv_ctx* c, int layer, void* k, void* v) {
   if (!k || !v || !aligned16(k) || !aligned16(v)) return FKV_ERR_INVALID_ARG;
   c->k[layer] = k;
   c->v[layer] = v;
-  c->q4[layer] = 0;
+  c->format[layer] = fkv::kCachePlain;
   remake_maps(c, layer);
   return FKV_OK;
 }
@@ -364,7 +395,24 @@ fkv_status fkv_bind_layer_cache_q4(fkv_ctx* c, int layer, void* k_rec, void* v_r
   if (!k_rec || !v_rec || !aligned16(k_rec) || !aligned16(v_rec)) return FKV_ERR_INVALID_ARG;
   c->k[layer] = k_rec;
   c->v[layer] = v_rec;
-  c->q4[layer] = 1;
+  c->format[layer] = fkv::kCacheQ4;
+  return FKV_OK;
+}
+
+int fkv_q8_scale_cols(int rows) { return rows > 0 ? fkv::q8_scale_cols(rows) : 0; }
+
+fkv_status fkv_bind_layer_cache_q8(fkv_ctx* c, int layer, void* k_codes, void* v_codes,
+                                   float* k_scales, float* v_scales) {
+  if (!c || layer < 1 || layer > c->cfg.num_layers) return FKV_ERR_INVALID_ARG;
+  if (layer > c->n && !c->cfg.store_upper) return FKV_ERR_UNSUPPORTED;
+  if (!k_codes || !v_codes || !aligned16(k_codes) || !aligned16(v_codes) || !k_scales || !v_scales ||
+      !aligned16(k_scales) || !aligned16(v_scales))
+    return FKV_ERR_INVALID_ARG;
+  c->k[layer] = k_codes;
+  c->v[layer] = v_codes;
+  c->ks[layer] = k_scales;
+  c->vs[layer] = v_scales;
+  c->format[layer] = fkv::kCacheQ8;
   return FKV_OK;
 }
 
@@ -422,6 +470,12 @@ fkv_status fkv_append_kv(fkv_ctx* c, int layer, const void* k_new, const void* v
   if (T < 0 || T > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   if (c->ring[layer] > 0 && T > c->ring[layer]) return FKV_ERR_INVALID_ARG;
   if (!c->k[layer] || !c->v[layer]) return FKV_ERR_INVALID_ARG;
+  const int format = c->format[layer];
+  if (format == fkv::kCacheQ8 && c->ring[layer] > 0) {
+    if (c->ring[layer] % fkv::kQ8Block != 0) return FKV_ERR_UNSUPPORTED;
+    // the rows may not come round to the block that they start in
+    if ((long long)T + kQ8Lost > c->ring[layer]) return FKV_ERR_INVALID_ARG;
+  }
   if (T == 0) return FKV_OK;
   if (!k_new || !v_new || !pos || !aligned16(k_new) || !aligned16(v_new) ||
       (reinterpret_cast<uintptr_t>(pos) & 3u))
@@ -440,8 +494,40 @@ fkv_status fkv_append_kv(fkv_ctx* c, int layer, const void* k_new, const void* v
   a.T = T;
   a.elem_bytes = elem_bytes(c->cfg);
   a.ring = c->ring[layer];
-  const cudaError_t e = c->q4[layer] ? fkv::append_q4_launch(a, static_cast<cudaStream_t>(stream))
-                                     : fkv::append_launch(a, static_cast<cudaStream_t>(stream));
+  a.k_scale = c->ks[layer];
+  a.v_scale = c->vs[layer];
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = format == fkv::kCacheQ8   ? fkv::append_q8_launch(a, st)
+                        : format == fkv::kCacheQ4 ? fkv::append_q4_launch(a, st)
+                                                  : fkv::append_launch(a, st);
+  return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+fkv_status fkv_read_kv(fkv_ctx* c, int layer, int mode, const int32_t* pos, int T, void* k_out,
+                       void* v_out, void* stream) {
+  if (!c || !on_device(c)) return FKV_ERR_INVALID_ARG;
+  fkv::ReadArgs r{};
+  int src[4];
+  const fkv_status s =
+      resolve_sources(c, layer, mode, r.k, r.v, r.a, r.b, &r.nsrc, &r.format, &r.ring, src);
+  if (s != FKV_OK) return s;
+  if (T < 0 || T > (r.ring > 0 ? r.ring : c->cfg.max_seq)) return FKV_ERR_INVALID_ARG;
+  if (T == 0) return FKV_OK;
+  if (!pos || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return FKV_ERR_INVALID_ARG;
+  source_scales(c, src, r.k_scale, r.v_scale);
+  r.pos = pos;
+  r.k_out = k_out;
+  r.v_out = v_out;
+  r.status = c->status;
+  r.batch = c->cfg.batch;
+  r.kv_heads = c->cfg.num_kv_heads;
+  r.max_seq = c->cfg.max_seq;
+  r.head_dim = c->cfg.head_dim;
+  r.T = T;
+  r.is_f32 = c->cfg.dtype == FKV_F32;
+  const cudaError_t e = fkv::read_launch(r, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
@@ -455,6 +541,8 @@ size_t fkv_decode_workspace_bytes(const fkv_ctx* c) {
     if (fkv::decode_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
       best = p.workspace_bytes;
     if (fkv::decode_q4_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
+      best = p.workspace_bytes;
+    if (fkv::decode_q8_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
       best = p.workspace_bytes;
   }
   return best;
@@ -477,10 +565,10 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   if (!c) return FKV_ERR_INVALID_ARG;
   const int S = C;
   fkv::PrefillArgs p{};
-  int q4 = 0, ring = 0;
-  fkv_status s = resolve_sources(c, layer, mode, p.k, p.v, p.a, p.b, &p.nsrc, &q4, &ring);
+  int format = 0, ring = 0;
+  fkv_status s = resolve_sources(c, layer, mode, p.k, p.v, p.a, p.b, &p.nsrc, &format, &ring);
   if (s != FKV_OK) return s;
-  if (q4) return FKV_ERR_UNSUPPORTED;   // prefill reads bf16 caches
+  if (format != fkv::kCachePlain) return FKV_ERR_UNSUPPORTED;   // prefill reads bf16 caches
   if (c->cfg.dtype != FKV_BF16) return FKV_ERR_UNSUPPORTED;
   if (S < 1 || q_start < 0 || (long long)q_start + S > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   // Over ring caches whose positions have wrapped, every key a query of the
@@ -539,9 +627,10 @@ fkv_status fkv_tree_attn(fkv_ctx* c, const void* q, int layer, int mode, const i
   if (!c || !on_device(c)) return FKV_ERR_INVALID_ARG;
   if (T < 1 || T > kTreeNodes || T > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   fkv::TreeArgs t = tree_args(c, T);
-  int q4 = 0, ring = 0, nsrc = 0, src[4];
-  fkv_status s = resolve_sources(c, layer, mode, t.k, t.v, t.a, t.b, &nsrc, &q4, &ring, src);
+  int format = 0, ring = 0, nsrc = 0, src[4];
+  fkv_status s = resolve_sources(c, layer, mode, t.k, t.v, t.a, t.b, &nsrc, &format, &ring, src);
   if (s != FKV_OK) return s;
+  if (format == fkv::kCacheQ8) return FKV_ERR_UNSUPPORTED;   // trees read plain and 4-bit caches
   for (int i = 0; i < 2; ++i) {
     t.k_maps[i] = &c->maps[0][src[i]];   // (entry 0 where there is no second source)
     t.v_maps[i] = &c->maps[1][src[2 + i]];
@@ -557,7 +646,7 @@ fkv_status fkv_tree_attn(fkv_ctx* c, const void* q, int layer, int mode, const i
       (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(node_counts) & 3u) ||
       (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
     return FKV_ERR_INVALID_ARG;
-  t.q4 = q4;
+  t.q4 = format == fkv::kCacheQ4;
   t.ring = ring;
   fkv::TreePlan plan{};
   if (fkv::tree_plan(t, c->num_sms, &plan) != cudaSuccess) return FKV_ERR_UNSUPPORTED;
@@ -584,6 +673,7 @@ fkv_status fkv_compact_rows(fkv_ctx* c, const int32_t* pos, const int32_t* idx,
       ((reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(idx) |
         reinterpret_cast<uintptr_t>(counts)) & 3u))
     return FKV_ERR_INVALID_ARG;
+  if (any_q8(c)) return FKV_ERR_UNSUPPORTED;
   fkv::CompactArgs a{};
   a.pos = pos;
   a.idx = idx;
@@ -606,6 +696,7 @@ fkv_status fkv_reorder_seqs(fkv_ctx* c, const int32_t* src, const int32_t* seq_l
   if (!c || !on_device(c) || !src || !seq_lens ||
       ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u))
     return FKV_ERR_INVALID_ARG;
+  if (any_q8(c)) return FKV_ERR_UNSUPPORTED;
   fkv::ReorderArgs a{};
   a.src = src;
   a.seq_lens = seq_lens;

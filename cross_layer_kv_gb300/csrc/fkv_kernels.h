@@ -38,6 +38,8 @@ struct DecodeArgs {
   int ring;                  // > 0: the source caches are rings of this many rows per
                              // unit (position t at row t % ring); 0: S_max rows, row = position
   unsigned epoch;            // distinct per call (tags the unit arrival counts)
+  const float* k_scale[2];   // scales of 8-bit sources
+  const float* v_scale[2];
 };
 
 // Launch configuration the library picks for a decode call shape.
@@ -84,6 +86,8 @@ struct AppendArgs {
   int* status;
   int batch, kv_heads, max_seq, head_dim, T, elem_bytes;
   int ring;        // > 0: the cache is a ring of this many rows per unit (row = position % ring)
+  float* k_scale;  // scales of an 8-bit cache
+  float* v_scale;
 };
 
 cudaError_t append_launch(const AppendArgs& a, cudaStream_t stream);
@@ -97,6 +101,40 @@ __host__ __device__ constexpr int q4_row_bytes(int head_dim) {
 cudaError_t append_q4_launch(const AppendArgs& a, cudaStream_t stream);
 cudaError_t decode_q4_launch(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
 cudaError_t decode_q4_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan);
+
+// How a layer's cache holds its rows: elements of the context's type, 4-bit
+// records, or 8-bit codes with scales.
+enum CacheFormat { kCachePlain = 0, kCacheQ4 = 1, kCacheQ8 = 2 };
+
+// 8-bit caches: e4m3 codes, and one fp32 scale per kQ8Block rows of a
+// (sequence, KV head); a unit's scales are padded to whole 16-byte pieces.
+constexpr int kQ8Block = 32;
+constexpr int kQ8MinExp = -100, kQ8MaxExp = 119;   // of the scales that the append chooses
+__host__ __device__ constexpr int q8_scale_cols(int rows) {
+  return (rows / kQ8Block + (rows % kQ8Block ? 1 : 0) + 3) / 4 * 4;
+}
+cudaError_t append_q8_launch(const AppendArgs& a, cudaStream_t stream);
+cudaError_t decode_q8_launch(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
+cudaError_t decode_q8_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan);
+
+// One fkv_read_kv call, after host validation: sources and weights as in
+// DecodeArgs.
+struct ReadArgs {
+  const void* k[2];
+  const void* v[2];
+  const float* a[2];
+  const float* b[2];
+  const float* k_scale[2];
+  const float* v_scale[2];
+  const int32_t* pos;   // [B]
+  void* k_out;          // [B, H_kv, T, D]
+  void* v_out;
+  int* status;
+  int batch, kv_heads, max_seq, head_dim, T;
+  int nsrc, is_f32, format;
+  int ring;
+};
+cudaError_t read_launch(const ReadArgs& a, cudaStream_t stream);
 
 constexpr int kDevTimeoutBit = 2;  // must match kDevTimeout
 

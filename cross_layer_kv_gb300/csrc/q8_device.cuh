@@ -1,0 +1,52 @@
+// 8-bit caches: the format and its conversions.
+//
+// A plane (the K or V cache of a layer) is e4m3 codes [B, H_kv, rows, D] and
+// fp32 scales [B, H_kv, q8_scale_cols(rows)], one per kQ8Block consecutive
+// rows of a (sequence, KV head); an element's value is code * scale.  e4m3 has
+// 4 significant bits at every exponent from 2^-6 on (below it, steps of 2^-9),
+// so a block's scale only has to place the block's largest value below 448:
+// the append takes the power of two that does.  A later, larger row of the
+// same block then moves the codes before it by whole exponents, which rounds
+// nothing but what falls below 2^-6 (an error of at most 2^-10 scales, 2^-18
+// of the block's largest value).
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fkv_device.cuh"
+
+namespace fkv {
+
+// Two e4m3 codes (the low one first) -> fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+
+// Two fp32 -> e4m3 codes (x in the low byte): nearest even, above 448 to 448,
+// NaN to NaN.
+__device__ __forceinline__ uint32_t e4m3x2_of(float x, float y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(x), "f"(y));
+  return r;
+}
+
+// Four codes in a word -> fp32, exactly.
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
+  const uint32_t h0 = e4m3x2_to_f16x2(w), h1 = e4m3x2_to_f16x2(w >> 16);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+  f[0] = a.x;
+  f[1] = a.y;
+  f[2] = b.x;
+  f[3] = b.y;
+}
+
+}  // namespace fkv

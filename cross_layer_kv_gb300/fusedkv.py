@@ -67,12 +67,15 @@ _SIGS = {
     "fkv_bind_layer_cache": (ctypes.c_int, [_P, ctypes.c_int, _P, _P]),
     "fkv_q4_row_bytes": (ctypes.c_size_t, [ctypes.c_int]),
     "fkv_bind_layer_cache_q4": (ctypes.c_int, [_P, ctypes.c_int, _P, _P]),
+    "fkv_q8_scale_cols": (ctypes.c_int, [ctypes.c_int]),
+    "fkv_bind_layer_cache_q8": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P]),
     "fkv_set_fusion_weights": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P]),
     "fkv_set_sources": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                        ctypes.c_int, ctypes.c_int]),
     "fkv_set_window": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int]),
     "fkv_set_ring_rows": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int]),
     "fkv_append_kv": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P]),
+    "fkv_read_kv": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P]),
     "fkv_decode_workspace_bytes": (ctypes.c_size_t, [_P]),
     "fkv_decode_attn": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P,
                                        ctypes.c_size_t, _P]),
@@ -238,6 +241,33 @@ class Context:
                "fkv_bind_layer_cache_q4")
         self._keep[("kv", layer)] = (k_rec, v_rec)
 
+    def fkv_q8_scale_cols(self, rows: Optional[int] = None) -> int:
+        return int(self._lib.fkv_q8_scale_cols(rows or self.cfg.max_seq))
+
+    def q8_cache(self, device="cuda", rows: Optional[int] = None):
+        """Zeroed codes [B, H_kv, rows (default S_max), D] (float8_e4m3fn) and
+        scales [B, H_kv, fkv_q8_scale_cols(rows)] (fp32) of one K or V cache."""
+        c = self.cfg
+        rows = rows or c.max_seq
+        return (torch.zeros((c.batch, c.num_kv_heads, rows, c.head_dim), dtype=torch.float8_e4m3fn,
+                            device=device),
+                torch.zeros((c.batch, c.num_kv_heads, self.fkv_q8_scale_cols(rows)), device=device))
+
+    def fkv_bind_layer_cache_q8(self, layer: int, k_codes, v_codes, k_scales, v_scales):
+        """Codes as float8_e4m3fn or uint8 tensors; scales as fp32 ones."""
+        c = self.cfg
+        for name, t in (("k codes", k_codes), ("v codes", v_codes)):
+            dtype = getattr(t, "dtype", None)
+            self._need_cuda(t, self._cache_shape(layer),
+                            torch.uint8 if dtype == torch.uint8 else torch.float8_e4m3fn, name)
+        shape = (c.batch, c.num_kv_heads, self.fkv_q8_scale_cols(self._rows(layer)))
+        self._need_cuda(k_scales, shape, torch.float32, "k scales")
+        self._need_cuda(v_scales, shape, torch.float32, "v scales")
+        _check(self._lib.fkv_bind_layer_cache_q8(self.handle, layer, _ptr(k_codes), _ptr(v_codes),
+                                                 _ptr(k_scales), _ptr(v_scales)),
+               "fkv_bind_layer_cache_q8")
+        self._keep[("kv", layer)] = (k_codes, v_codes, k_scales, v_scales)
+
     def fkv_set_fusion_weights(self, layer: int, a_first, a_second, b_first, b_second):
         shape = (self.cfg.num_kv_heads, self.cfg.head_dim)
         for n, t in zip(("a_first", "a_second", "b_first", "b_second"),
@@ -276,6 +306,21 @@ class Context:
         self._need(pos, (c.batch,), torch.int32, "pos")
         _check(self._lib.fkv_append_kv(self.handle, layer, _ptr(k_new), _ptr(v_new), _ptr(pos), T,
                                        _stream(stream)), "fkv_append_kv")
+
+    def fkv_read_kv(self, layer: int, mode, pos, k_out, v_out, T: Optional[int] = None, stream=None):
+        """Positions pos[b] .. pos[b] + T - 1 of every sequence, as `layer` sees
+        them in `mode`, into k_out and v_out [B, H_kv, T, D]."""
+        c = self.cfg
+        if T is None:
+            T = k_out.shape[2]
+        shape = (c.batch, c.num_kv_heads, T, c.head_dim)
+        self._need_cuda(pos, (c.batch,), torch.int32, "pos")
+        self._need_cuda(k_out, shape, self.torch_dtype, "k_out")
+        self._need_cuda(v_out, shape, self.torch_dtype, "v_out")
+        m = MODES[mode] if isinstance(mode, str) else int(mode)
+        _check(self._lib.fkv_read_kv(self.handle, layer, m, _ptr(pos), T, _ptr(k_out), _ptr(v_out),
+                                     _stream(stream)), "fkv_read_kv")
+        return k_out, v_out
 
     def fkv_decode_workspace_bytes(self) -> int:
         return int(self._lib.fkv_decode_workspace_bytes(self.handle))

@@ -126,6 +126,47 @@ size_t fkv_q4_row_bytes(int head_dim);
  * FKV_ERR_UNSUPPORTED).  Needs dtype FKV_BF16 and H_q / H_kv <= 2. */
 fkv_status fkv_bind_layer_cache_q4(fkv_ctx* ctx, int layer, void* k_rec, void* v_rec);
 
+/* Scales of one (sequence, KV head) of an 8-bit cache of `rows` rows: one for
+ * every 32 rows, padded to a multiple of 4 (0 for rows < 1). */
+int fkv_q8_scale_cols(int rows);
+
+/* Register 8-bit K and V caches of a layer (half the bytes of bf16; the pages
+ * quantise to 4 bits, this format is the library's).  Contexts of either dtype
+ * and any group size.
+ * k_codes, v_codes: device, [B, H_kv, R, D] e4m3 codes (8-bit floats: sign, 4
+ * exponent bits, 3 fraction bits, 0x7F and 0xFF not a number); k_scales,
+ * v_scales: device fp32 [B, H_kv, fkv_q8_scale_cols(R)]; R = S_max, or the
+ * layer's ring rows.  All 16-byte aligned.  Row r's values are its codes times
+ * scale r / 32 of its (sequence, KV head), in K and V apart.  Scales are
+ * positive and finite; fkv_append_kv makes them powers of two, and scales that
+ * a caller fills in may be others.
+ * fkv_append_kv quantises new rows as they are written: with amax the largest
+ * finite magnitude of the rows that a call writes into a block of 32, and need
+ * = 2^e the smallest power of two with amax <= 448 * 2^e (e clamped to [-100,
+ * 119]; all zeros: 2^-100),
+ *   - the block's scale becomes need where the call writes the block's first
+ *     row, and the larger of need and the scale it had otherwise;
+ *   - a new value's code is the nearest e4m3 value of x / scale (ties to even,
+ *     magnitudes above 448 to 448), infinities and NaN the code 0x7F;
+ *   - rows of the block before the new ones keep their values: where the scale
+ *     grew, their codes become the nearest of code * old scale / new scale,
+ *     which is exact but for values below 2^-6 new scales (off by at most 2^-10
+ *     new scales);
+ *   - rows of the block behind the new ones are lost.
+ * So rows are appended in order, as for a ring; rows taken back (a shorter
+ * length, then an append there) are fine, and leave a scale that they raised.
+ * Calls over 8-bit caches: fkv_append_kv, fkv_read_kv, fkv_decode_attn
+ * (_noalloc), where every source of the call is 8-bit (a mix of formats is
+ * FKV_ERR_UNSUPPORTED).  fkv_prefill_attn (_chunk) and fkv_tree_attn over them,
+ * and fkv_compact_rows and fkv_reorder_seqs while a layer holds them, are
+ * FKV_ERR_UNSUPPORTED.
+ * Rings: R a multiple of 32 (FKV_ERR_UNSUPPORTED otherwise, from the calls);
+ * an append that comes round to a block loses the up to 31 older rows behind
+ * the new ones in it, so fkv_append_kv needs T + 31 <= R (FKV_ERR_INVALID_ARG)
+ * and fkv_decode_attn a window with window + 31 <= R (FKV_ERR_UNSUPPORTED). */
+fkv_status fkv_bind_layer_cache_q8(fkv_ctx* ctx, int layer, void* k_codes, void* v_codes,
+                                   float* k_scales, float* v_scales);
+
 /* Register the fusion weights of reconstruction layer n < layer <= L
  * (FusedKV slides, Eqs.(4)-(5)): a_first/a_second scale K^1/K^n, b_first/
  * b_second scale V^1/V^n.  Each is a device fp32 [H_kv, D] buffer owned by the
@@ -193,6 +234,25 @@ fkv_status fkv_set_ring_rows(fkv_ctx* ctx, int layer, int rows);
  * device status.  The layer must have a bound cache. */
 fkv_status fkv_append_kv(fkv_ctx* ctx, int layer, const void* k_new, const void* v_new,
                          const int32_t* pos, int T, void* stream);
+
+/* Read rows back: the keys and values of positions pos[b] .. pos[b] + T - 1 of
+ * every sequence as the attention of `layer` sees them, in the context dtype --
+ * an 8-bit or 4-bit prefix handed on to something that wants plain rows, or a
+ * reconstruction layer's rows, which no cache holds.  Modes and sources as for
+ * fkv_decode_attn: the layer's own rows, K^s and V^t (Lite, Eq.(6)), those
+ * scaled, or a_1 (.) K^s1 + a_2 (.) K^s2 and b_1 (.) V^t1 + b_2 (.) V^t2
+ * (Eqs.(4)-(5)), over caches of any format (all sources of a call of one).
+ * fp32 arithmetic, rounded once to the context dtype; plain rows come back as
+ * they are.
+ * pos: device int32 [B]; k_out, v_out: device [B, H_kv, T, D], 16-byte aligned,
+ * none of the caches read.  0 <= T <= S_max, or the rows of ring caches, of
+ * which the row of position t, t % rows, is read whatever position it holds
+ * (FKV_ERR_INVALID_ARG otherwise).  A sequence whose positions fall outside
+ * [0, S_max) is skipped, its outputs left as they were, and flagged as
+ * FKV_ERR_DEVICE_ARG in the device status.  Made with the context's device
+ * current (FKV_ERR_INVALID_ARG otherwise); can be captured. */
+fkv_status fkv_read_kv(fkv_ctx* ctx, int layer, int mode, const int32_t* pos, int T, void* k_out,
+                       void* v_out, void* stream);
 
 /* Bytes of device workspace fkv_decode_attn needs for this context (split-K
  * partial results).  The caller allocates it; its contents need no

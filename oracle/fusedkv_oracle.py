@@ -439,6 +439,89 @@ def q4_dequantize_records(rec: np.ndarray, head_dim: int) -> np.ndarray:
 
 
 # ---------------------------------------------------------------------------
+# 8-bit caches (no counterpart on the pages): the definitions that
+# include/fusedkv.h states for fkv_bind_layer_cache_q8
+# ---------------------------------------------------------------------------
+
+Q8_BLOCK = 32
+
+
+def e4m3_table() -> np.ndarray:
+    """The 256 values of an e4m3 code: sign, 4 exponent bits (bias 7), 3
+    fraction bits; exponent 0 is subnormal, all ones in both fields is NaN."""
+    out = np.empty(256)
+    for c in range(256):
+        e, f = (c >> 3) & 15, c & 7
+        x = f * 2.0 ** -9 if e == 0 else (8 + f) * 2.0 ** (e - 10)
+        if e == 15 and f == 7:
+            x = np.nan
+        out[c] = -x if c & 128 else x
+    return out
+
+
+def e4m3_encode(x: np.ndarray) -> np.ndarray:
+    """Nearest code, ties to the even one; magnitudes above 448 to 448; what is
+    not finite to 0x7F."""
+    x = np.asarray(x, dtype=np.float64)
+    grid = e4m3_table()[:127]                        # 0 .. 448, ascending
+    a = np.minimum(np.abs(np.where(np.isfinite(x), x, 0.0)), 448.0)
+    hi = np.clip(np.searchsorted(grid, a), 1, 126)   # grid[hi - 1] < a <= grid[hi]
+    lo = hi - 1
+    up, down = grid[hi] - a, a - grid[lo]
+    pick = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where(np.signbit(x), pick + 128, pick)
+    return np.where(np.isfinite(x), code, 0x7F).astype(np.uint8)
+
+
+def q8_need(amax: float) -> float:
+    """The smallest power of two whose 448-fold reaches amax, from 2^-100 to 2^119."""
+    e = -100
+    while e < 119 and amax > 448.0 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def q8_scale_cols(rows: int) -> int:
+    return (rows + 127) // 128 * 4
+
+
+def q8_append(codes: np.ndarray, scales: np.ndarray, new: np.ndarray, pos: Sequence[int]):
+    """Append new ``[B, H, T, D]`` at positions pos[b].. of a cache of codes
+    uint8 ``[B, H, R, D]`` and scales ``[B, H, cols]``; position t lives at row
+    t % R.  Returns updated copies and a mask of the rows that still hold
+    something (False: lost)."""
+    codes, scales = codes.copy(), np.array(scales, dtype=np.float64)
+    table = e4m3_table()
+    B, H, R, D = codes.shape
+    T = new.shape[2]
+    kept = np.ones((B, R), dtype=bool)
+    for b in range(B):
+        p = int(pos[b])
+        for g in range(p // Q8_BLOCK, (p + T - 1) // Q8_BLOCK + 1):
+            first, last = max(g * Q8_BLOCK, p), min((g + 1) * Q8_BLOCK, p + T)   # new positions
+            row = g * Q8_BLOCK % R
+            n0, n1 = first - g * Q8_BLOCK, last - g * Q8_BLOCK
+            kept[b, row + n1:row + Q8_BLOCK] = False
+            for h in range(H):
+                x = np.asarray(new[b, h, first - p:last - p], dtype=np.float64)
+                s = q8_need(np.max(np.abs(x[np.isfinite(x)]), initial=0.0))
+                if n0 > 0:
+                    old = scales[b, h, row // Q8_BLOCK]
+                    s = max(s, old)
+                    if s != old:
+                        c = codes[b, h, row:row + n0]
+                        codes[b, h, row:row + n0] = e4m3_encode(table[c] * (old / s))
+                codes[b, h, row + n0:row + n1] = e4m3_encode(x / s)
+                scales[b, h, row // Q8_BLOCK] = s
+    return codes, scales, kept
+
+
+def q8_values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    R = codes.shape[2]
+    return e4m3_table()[codes] * np.repeat(np.asarray(scales, np.float64), Q8_BLOCK, axis=2)[:, :, :R, None]
+
+
+# ---------------------------------------------------------------------------
 # RoPE and the pair-tying property ([Slides] "Post-RoPE fusion needs paired key
 # weights", Eqs.(7)-(8); [Notes] §2.4)
 # ---------------------------------------------------------------------------

@@ -1,0 +1,134 @@
+"""Shared helpers of the 8-bit cache tests: caches, a float64 reference, and error bounds
+derived from the arithmetic.  Test infrastructure only."""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from cross_layer_kv_gb300 import fusedkv as B
+
+BLOCK = 32
+
+
+def cols(rows):
+    return (rows + 127) // 128 * 4
+
+
+def make_plane(gen, batch, heads, rows, D, spread=1.0, device="cuda", powers=True):
+    """Random codes and scales of one plane: values of about unit size, times a
+    factor 2^k, |k| <= 3 * spread, that changes from block to block."""
+    x = torch.randn(batch, heads, rows, D, generator=gen, device=device) * 64
+    codes = x.clamp(-448, 448).to(torch.float8_e4m3fn)
+    k = torch.randn(batch, heads, cols(rows), generator=gen, device=device).clamp(-3, 3) * spread
+    if powers:
+        k = k.round()
+    return codes, torch.exp2(k - 6)
+
+
+def values(plane):
+    """A plane in float64."""
+    codes, scales = plane
+    rows = codes.shape[2]
+    at = torch.arange(rows, device=codes.device) // BLOCK
+    return codes.double() * scales[:, :, at, None].double()
+
+
+def reconstruct(mode, w, k, v):
+    """K^i, V^i in float64 of the sources' values (lists of one or two)."""
+    if mode in ("vanilla", "lite"):
+        return k[0], v[0]
+    w = [x.double()[None, :, None, :] for x in w]
+    if mode == "scaled":
+        return w[0] * k[0], w[2] * v[0]
+    return w[0] * k[0] + w[1] * k[1], w[2] * v[0] + w[3] * v[1]
+
+
+def attend(q, K, V, scale, see):
+    """softmax(scale q K^T) V in float64 with the visible keys `see` [T, S]; q [T, D].  Also the
+    largest sum of absolute products of a score, and sum p |V|."""
+    s = (q @ K.T) * scale
+    s = s.masked_fill(~see, -math.inf)
+    top = s.amax(-1, keepdim=True)
+    p = (s - torch.where(top == -math.inf, 0.0, top)).exp()
+    p = p / p.sum(-1, keepdim=True).clamp(min=1e-300)
+    size = (q.abs() @ K.abs().T * abs(scale)).masked_fill(~see, 0.0).amax(-1, keepdim=True)
+    return p @ V, size, p @ V.abs()
+
+
+def decode_bound(ref, size, pv, D, n, dtype):
+    """How far fp32 arithmetic may be off: a score is a sum of 2 D products with prescaled queries
+    (three roundings each) and their scales, the exponential and its base add 2^-21, a softmax
+    weight is off by twice a score's error, and n weighted values are added up in fp32; then one
+    rounding of the output."""
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    score = (2 * D + 8) * 2.0 ** -24 * size + 2.0 ** -21
+    return (2 * score + (n + 64) * 2.0 ** -24) * pv + u * ref.abs()
+
+
+class Setup:
+    """A context over 8-bit caches: the storage layers that a layer's mode reads."""
+
+    def __init__(self, mode, batch, seq, heads, group, D, dtype="bf16", layers=6, window=0, ring=0, seed=0,
+                 spread=1.0, powers=True, decode_ctas=0, softmax_scale=0.0):
+        self.mode, self.D, self.G, self.H, self.batch, self.seq = mode, D, group, heads, batch, seq
+        self.window, self.ring, self.dtype = window, ring, dtype
+        self.scale = softmax_scale or 1.0 / math.sqrt(D)
+        n = layers // 2
+        rows = ring or seq
+        g = self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.ctx = B.Context(layers, batch, seq, heads * group, heads, D, dtype, decode_ctas=decode_ctas,
+                             softmax_scale=softmax_scale)
+        two = mode == "fused"
+        self.layer = 2 if mode == "vanilla" else layers
+        read = [2] if mode == "vanilla" else [1, n]
+        self.planes = {l: tuple(make_plane(g, batch, heads, rows, D, spread, powers=powers) for _ in range(2))
+                       for l in read}
+        for l, (k, v) in self.planes.items():
+            if ring:
+                self.ctx.fkv_set_ring_rows(l, ring)
+            self.ctx.fkv_bind_layer_cache_q8(l, k[0], v[0], k[1], v[1])
+        if window:
+            self.ctx.fkv_set_window(self.layer, window)
+        self.w = [(torch.randn(heads, D, generator=g, device="cuda") * 0.3 + 0.5) for _ in range(4)]
+        if mode in ("scaled", "fused"):
+            self.ctx.fkv_set_fusion_weights(self.layer, *self.w)
+        if mode == "vanilla":
+            self.k, self.v = [self.planes[2][0]], [self.planes[2][1]]
+        elif two:
+            self.k, self.v = [self.planes[1][0], self.planes[n][0]], [self.planes[1][1], self.planes[n][1]]
+        else:
+            self.k, self.v = [self.planes[n][0]], [self.planes[1][1]]
+        self.torch_dtype = torch.float32 if dtype == "f32" else torch.bfloat16
+
+    def rows(self):
+        return reconstruct(self.mode, self.w, [values(x) for x in self.k], [values(x) for x in self.v])
+
+    def query(self, *shape):
+        return torch.randn(*shape, generator=self.gen, device="cuda").to(self.torch_dtype)
+
+    def close(self):
+        self.ctx.close()
+
+
+def check_decode(s, lens, q=None, what=""):
+    """One decode call against the reference, element by element."""
+    q = s.query(s.batch, s.H * s.G, s.D) if q is None else q
+    out = torch.full_like(q, float("nan"))
+    s.ctx.fkv_decode_attn(q, s.layer, s.mode, torch.tensor(lens, dtype=torch.int32, device="cuda"), out,
+                          s.ctx.workspace())
+    assert s.ctx.fkv_get_device_status() == B.FKV_OK
+    K, V = s.rows()
+    worst = 0.0
+    for b, L in enumerate(lens):
+        pos = torch.arange(max(0, L - s.window) if s.window else 0, L, device="cuda")
+        at = pos % s.ring if s.ring else pos
+        for h in range(s.H):
+            see = torch.ones(s.G, len(pos), dtype=torch.bool, device="cuda")
+            ref, size, pv = attend(q[b, h * s.G:(h + 1) * s.G].double(), K[b, h, at], V[b, h, at], s.scale, see)
+            err = (out[b, h * s.G:(h + 1) * s.G].double() - ref).abs()
+            bound = decode_bound(ref, size, pv, s.D, len(pos), s.dtype)
+            worst = max(worst, float((err / bound).max()))
+            assert bool((err <= bound).all()), "%s b=%d h=%d: %.2f of the bound" % (what, b, h, worst)
+    return out, worst
