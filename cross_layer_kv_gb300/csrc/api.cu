@@ -565,10 +565,11 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   if (!c) return FKV_ERR_INVALID_ARG;
   const int S = C;
   fkv::PrefillArgs p{};
-  int format = 0, ring = 0;
-  fkv_status s = resolve_sources(c, layer, mode, p.k, p.v, p.a, p.b, &p.nsrc, &format, &ring);
+  int format = 0, ring = 0, src[4];
+  fkv_status s = resolve_sources(c, layer, mode, p.k, p.v, p.a, p.b, &p.nsrc, &format, &ring, src);
   if (s != FKV_OK) return s;
-  if (format != fkv::kCachePlain) return FKV_ERR_UNSUPPORTED;   // prefill reads bf16 caches
+  if (format == fkv::kCacheQ4) return FKV_ERR_UNSUPPORTED;   // prefill reads bf16 and 8-bit caches
+  const bool q8 = format == fkv::kCacheQ8;
   if (c->cfg.dtype != FKV_BF16) return FKV_ERR_UNSUPPORTED;
   if (S < 1 || q_start < 0 || (long long)q_start + S > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   // Over ring caches whose positions have wrapped, every key a query of the
@@ -578,7 +579,7 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   if (ring > 0 && (long long)q_start + S > ring) {
     const int W = c->window[layer];
     if (W < 1 || W > ring) return FKV_ERR_INVALID_ARG;
-    if ((long long)S + W - 1 > ring) return FKV_ERR_UNSUPPORTED;
+    if ((long long)S + W - 1 > ring - (q8 ? kQ8Lost : 0)) return FKV_ERR_UNSUPPORTED;
   }
   p.plane_rows = ring > 0 ? ring : c->cfg.max_seq;
   p.ring = ring;
@@ -596,7 +597,9 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   p.head_dim = c->cfg.head_dim;
   p.S = S;
   p.softmax_scale = c->scale;
-  const cudaError_t e = fkv::prefill_launch(p, static_cast<cudaStream_t>(stream));
+  source_scales(c, src, p.k_scale, p.v_scale);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = q8 ? fkv::prefill_q8_launch(p, st) : fkv::prefill_launch(p, st);
   if (e == cudaErrorNotSupported) return FKV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }

@@ -155,6 +155,8 @@ struct PrefillArgs {
                    // t % ring), a multiple of the kernel's key tile once positions wrap
   int nsrc;
   float softmax_scale;
+  const float* k_scale[2];   // scales of 8-bit sources
+  const float* v_scale[2];
 };
 
 // Returns cudaErrorNotSupported for shapes the tensor-core kernels do not
@@ -165,6 +167,8 @@ struct PrefillArgs {
 cudaError_t prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_wide_launch(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t prefill_fused_wide_launch(const PrefillArgs& a, cudaStream_t stream);
+// Prefill over 8-bit caches, one source or two (prefill_q8_impl.cuh).
+cudaError_t prefill_q8_launch(const PrefillArgs& a, cudaStream_t stream);
 
 // What a kernel needs once per device before its first launch: its dynamic
 // shared memory raised to `smem` bytes and, for kernels that split their

@@ -1,0 +1,768 @@
+// Causal prefill attention over 8-bit caches (e4m3 codes, one scale per 32
+// rows of a KV head; q8_device.cuh) on the tcgen05 tensor cores of sm_103a:
+// one source (vanilla, Lite, scaled) or two (fused: FusedKV slides,
+// Eqs.(4)-(5)), rebuilt tile by tile in shared memory.
+//
+// What one call computes: for every sequence b, query head h (KV head
+// kh = h / G) and query position m of the chunk
+//     o_{h,m} = sum_{t <= m, t > m - W} softmax_t(scale * q_{h,m} . K_t) V_t.
+//
+// The operands are fp16, which holds every e4m3 code exactly, and the scales
+// stay outside the products.  With K_t = s_t k_t and V_t = r_t v_t (k, v the
+// tile's fp16 elements; s, r the same for 16 keys in a row of a tile),
+//     o = sum_t p_t r_t v_t / sum_t p_t,
+//     p_t r_t = 2^(c s_t (q . k_t) + log2 r_t),   c = scale * log2 e,
+// so a key scale multiplies the score and a value scale's logarithm is added
+// to it: the running maximum is that of the sum, and P' = p r, at most
+// 2^(kBias + kSlack) in its frame, is rounded to fp16 (2^-12) whatever the
+// scales are.  The softmax's sum takes p = P' / r.  A row of Q (times its key
+// weights in the scaled mode) is brought to fp16 with a power of two that
+// places its largest element below 2^15.  Two sources are combined as
+//     w0 c0 (s0 / s) + w1 c1 (s1 / s),  s = max(s0, s1),
+// in packed fp16 arithmetic, with the head's weights brought below 1 by one
+// power of two.
+//
+// Structure (as prefill_fused_wide.cu): a CTA owns two groups of 128 query
+// rows over the same keys (two heads of a KV head, or two row tiles of one
+// head), each with a softmax warpgroup and an MMA-issuing warp that takes
+// turns with the other's; Q, S / P and O live in tensor memory.  Two warps
+// bring tiles of codes by cp.async.bulk (a tile's rows are contiguous, in two
+// pieces where a ring wraps, so no ring size is excluded), and a conversion
+// warpgroup writes the fp16 tiles in the swizzled layout that the MMAs read.
+// Its step k makes V_{k-1} and K_k, what MMA step k reads.
+//
+// Key rows that a query may not see do not reach it, whatever they hold:
+// scores are masked by position, and a value that is not a number is 0 in the
+// tile and makes NaN of the rows that see it at the end.
+//
+// Every wait is bounded; a wait that runs out sets an abort flag that each
+// role checks, flags the device status, and the CTA frees its tensor memory.
+#pragma once
+
+#include <cfloat>
+#include <climits>
+#include <cstdint>
+
+#include "fkv_kernels.h"
+#include "q8_device.cuh"
+#include "tc_device.cuh"
+
+namespace fkv {
+namespace q8p {
+
+constexpr int BM = 128;            // query rows per group
+constexpr int NG = 2;              // groups per CTA
+constexpr int GROUP_COLS = 256;    // TMEM columns per group: S/P, O, Q
+constexpr int SMEM_LIMIT = 232448; // opt-in dynamic shared memory per CTA (227 KB)
+constexpr float kSlack = 8.f;      // log2 growth of the running max tolerated before O is rescaled
+constexpr float kBias = 7.f;       // P' <= 2^(7 + 8) < 65504, and is not flushed above 2^-31
+constexpr int NSR = 8;             // conversion-step barriers and scale records
+constexpr int NR = 2;              // slots of codes
+
+constexpr int cap4(int x) { return x > 4 ? 4 : x; }
+
+template <int D, int NSRC>
+struct Cfg {
+  static constexpr int BN = D <= 96 ? 112 : 64;        // keys per tile: S, O and Q fill 256 columns
+  static constexpr int NGRP = BN / 16;                  // key groups of one scale
+  static constexpr int CB = (D + kSWE - 1) / kSWE;      // 32-element column blocks
+  static constexpr int KV_BYTES = CB * BN * kSW;        // one fp16 tile
+  static constexpr int RAW_BYTES = BN * D;              // one tile of codes of one source
+  static constexpr int O_COL = BN;
+  static constexpr int Q_COLS = (D / 2 + 15) / 16 * 16;
+  static constexpr int Q_COL = GROUP_COLS - Q_COLS;
+  static_assert(O_COL + D <= Q_COL, "S, O and Q do not fit a group's 256 columns");
+  // fp16 weights [4][D], scale records [NSR][NGRP] float4, ratios [NSR][2][NGRP] half2, barriers and words
+  static constexpr int FIXED = 4 * D * 2 + NSR * NGRP * 16 + NSR * 2 * NGRP * 8 + 1024;
+  static constexpr int RAW = NR * 2 * NSRC * RAW_BYTES;
+  static constexpr int NS = cap4((SMEM_LIMIT - 512 - FIXED - RAW) / (2 * KV_BYTES));   // K and V slots
+  static_assert(NS >= 2, "shared memory too small for the tiles");
+  static_assert(NSR > NS + 1, "step barriers must outnumber the tile slots");
+  static constexpr size_t SMEM = 512 + (size_t)FIXED + RAW + (size_t)2 * NS * KV_BYTES;
+  static constexpr int SOFTMAX_WARPS = 4 * NG;
+  static constexpr int K_PRODUCER_WARP = SOFTMAX_WARPS;
+  static constexpr int MMA_WARP = K_PRODUCER_WARP + 1;   // + g for group g
+  static constexpr int V_PRODUCER_WARP = MMA_WARP + NG;
+  static constexpr int CONV_WARP = SOFTMAX_WARPS + 4;
+  static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 8);
+  // registers: 128 per thread at launch (65536 / 512)
+  static constexpr int REGS_CONTROL = 48, REGS_CONV = 88, REGS_SOFTMAX = 184;
+  static constexpr long long REGS_SPLIT =
+      (long long)NG * 128 * REGS_SOFTMAX + 128LL * REGS_CONTROL + 128LL * REGS_CONV;
+  static_assert(REGS_SPLIT <= (long long)THREADS * 128, "register split above the launch allocation");
+};
+
+struct Params {
+  const uint8_t* k[2];
+  const uint8_t* v[2];
+  const float* ks[2];
+  const float* vs[2];
+  const float* a[2];   // key weights [H_kv, D] of the sources (null: none)
+  const float* b[2];
+  const void* q;       // [B, H_q, S, D] bf16
+  void* out;           // [B, H_q, S, D] bf16
+  int* status;
+  const unsigned long long* wait_limit;
+  int H_kv, G;
+  int S;               // query rows of this call (the chunk length C)
+  int q_start;         // cache position of query row 0
+  int S_kv;            // key positions: q_start + C
+  int window;
+  int rows;            // rows of a (sequence, KV head) in the caches
+  int ring;            // > 0: position t at row t % ring
+  float scale_log2;
+};
+
+// All of the warpgroup's 128 threads arrive; true where all were ok.
+__device__ __forceinline__ bool group_and(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            *reinterpret_cast<__half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
+  const __half2 r = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Whether one of four codes is not a number.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// 2^e with 2^e <= x < 2^(e+1) for a normal x > 0 (0 for what is smaller).
+__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+__device__ __forceinline__ float power_of_two(int e) {   // e clamped to the normal range
+  e = e < -126 ? -126 : (e > 127 ? 127 : e);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+template <int D, int NSRC>
+__global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(const Params p) {
+  using C = Cfg<D, NSRC>;
+  constexpr int BN = C::BN, NS = C::NS, NGRP = C::NGRP;
+  extern __shared__ uint8_t smem_raw[];
+  // 512-byte alignment: the period of the 64-byte swizzle pattern
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~uintptr_t(511));
+  uint8_t* sK = smem;                                   // fp16 tiles
+  uint8_t* sV = sK + NS * C::KV_BYTES;
+  uint8_t* sRawK = sV + NS * C::KV_BYTES;               // codes, the sources of a slot side by side
+  uint8_t* sRawV = sRawK + NR * NSRC * C::RAW_BYTES;
+  float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s, log2 r, 1 / r, -}
+  // (s0 / s, s1 / s) of K and V, each as two equal halves
+  uint2* sRatio = reinterpret_cast<uint2*>(sScale + NSR * NGRP);
+  uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + NSR * 2 * NGRP);            // fp16 a0, a1, b0, b1
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sW + 4 * D);
+  uint64_t* q_ready = bars;
+  uint64_t* k_empty = q_ready + 1;        // [4]
+  uint64_t* v_empty = k_empty + 4;        // [4]
+  uint64_t* rk_full = v_empty + 4;        // [NR]
+  uint64_t* rk_empty = rk_full + NR;
+  uint64_t* rv_full = rk_empty + NR;
+  uint64_t* rv_empty = rv_full + NR;
+  uint64_t* step_ready = rv_empty + NR;   // [NSR]
+  uint64_t* s_full = step_ready + NSR;    // [NG]
+  uint64_t* p_full = s_full + NG;         // [NG]
+  uint64_t* mma_drain = p_full + NG;      // [NG]
+  uint32_t* words = reinterpret_cast<uint32_t*>(mma_drain + NG);
+  uint32_t* tmem_slot = words;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  int* sm_issued = reinterpret_cast<int*>(words + 2);   // [2] tiles each producer issued
+  uint32_t* w_top = words + 4;                          // [2] largest key / value weight (bits)
+  uint32_t* bad = words + 6;       // [1 + 8 + 8] values that are not numbers: seen by all; near the
+                                   // diagonal; near the window's start (bits of positions)
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  int ux, mt;
+  prefill_cta_tile(ux, mt);   // longest query tiles first
+  const bool two_heads = p.G % 2 == 0;
+  const int pairs = two_heads ? p.G / 2 : p.G;   // CTAs of a unit's heads
+  const int unit = ux / pairs, pair = ux % pairs;
+  const int H_q = p.H_kv * p.G;
+  const int b = unit / p.H_kv, kh = unit % p.H_kv;
+  // group g: query head and first query row (within the chunk)
+  auto g_head = [&](int g) { return kh * p.G + (two_heads ? pair * 2 + g : pair); };
+  auto g_row0 = [&](int g) { return two_heads ? mt * BM : mt * (NG * BM) + g * BM; };
+  const int S_kv = p.S_kv;
+  const int W = p.window;
+  // key tiles of positions pos0 + j * BN: from the first group's window start
+  // (down to 16 keys, which have one scale) to each group's last position
+  const int pos_first = p.q_start + g_row0(0);
+  const int pos0 = W > 0 ? max(0, pos_first - W + 1) / 16 * 16 : 0;
+  auto n_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) - pos0 + BN - 1) / BN; };
+  const int n_max = max(n_tiles(0), n_tiles(1));
+
+  auto tile_k = [&](int j) { return sK + (size_t)(j % NS) * C::KV_BYTES; };
+  auto tile_v = [&](int j) { return sV + (size_t)(j % NS) * C::KV_BYTES; };
+
+  if (tid == 0) {
+    mbar_init(q_ready, 128 * NG);
+    for (int s = 0; s < NSR; ++s) mbar_init(&step_ready[s], 128);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&k_empty[s], NG);    // one commit per group that reads the tile
+      mbar_init(&v_empty[s], NG);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&rk_full[s], 1);
+      mbar_init(&rk_empty[s], 128);  // the conversion threads, once they have read it
+      mbar_init(&rv_full[s], 1);
+      mbar_init(&rv_empty[s], 128);
+    }
+    for (int g = 0; g < NG; ++g) {
+      mbar_init(&s_full[g], 1);
+      // the group's 128 softmax threads, plus the other group's issuer once
+      // its previous step's PV products are queued (the turn)
+      mbar_init(&p_full[g], 129);
+      mbar_init(&mma_drain[g], 1);
+    }
+    *abort_flag = 0;
+    sm_issued[0] = sm_issued[1] = 0;
+    w_top[0] = w_top[1] = 0;
+    for (int i = 0; i < 17; ++i) bad[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::MMA_WARP) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const unsigned long long wlim = wait_limit_ns(p.wait_limit);
+  if constexpr (NSRC == 2) {
+    // the head's weights below 1: one power of two for keys, one for values
+    for (int i = tid; i < 4 * D; i += C::THREADS) {
+      const int v = i / D;
+      const float w = fabsf((v < 2 ? p.a[v] : p.b[v - 2])[kh * D + i % D]);
+      if (w < INFINITY) atomicMax(&w_top[v >> 1], __float_as_uint(w));
+    }
+    __syncthreads();
+    for (int i = tid; i < 4 * D; i += C::THREADS) {
+      const int v = i / D;
+      const float top = __uint_as_float(w_top[v >> 1]);
+      const float w = (v < 2 ? p.a[v] : p.b[v - 2])[kh * D + i % D];
+      const __half h = __float2half_rn(w * power_of_two(-exponent_of(top) - 1));
+      sW[i] = *reinterpret_cast<const uint16_t*>(&h);
+    }
+    __syncthreads();
+  }
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(bar, parity, wlim)) return true;
+    *abort_flag = 1;
+    flag_status(p.status, kDevTimeout);
+    return false;
+  };
+
+  if (warp >= C::CONV_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+    // ---------------- conversion warpgroup ----------------
+    const int ft = tid - 32 * C::CONV_WARP;   // 0..127
+    const size_t scols = (size_t)q8_scale_cols(p.rows);
+    // Scale records of tile j, one thread per group of 16 keys.
+    float ns[2 * NSRC];
+    auto load_scales = [&](int j) {
+      const int pos = pos0 + j * BN + ft * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * NSRC; ++i) ns[i] = 1.f;   // (groups behind the last key: any finite one)
+      if (ft < NGRP && j < n_max && pos < S_kv) {
+        const size_t at = (size_t)unit * scols + (p.ring > 0 ? pos % p.ring : pos) / kQ8Block;
+#pragma unroll
+        for (int i = 0; i < NSRC; ++i) {
+          ns[i] = __ldg(p.ks[i] + at);
+          ns[NSRC + i] = __ldg(p.vs[i] + at);
+        }
+      }
+    };
+    auto store_scales = [&](int j) {
+      if (ft >= NGRP) return;
+      float s = ns[0], r = ns[NSRC];
+      if constexpr (NSRC == 2) {
+        s = fmaxf(ns[0], ns[1]);
+        r = fmaxf(ns[2], ns[3]);
+        const float is = 1.f / s, ir = 1.f / r;
+        uint2* rec = sRatio + (size_t)(j % NSR) * 2 * NGRP;
+        rec[ft] = make_uint2(f16x2_of(ns[0] * is, ns[0] * is), f16x2_of(ns[1] * is, ns[1] * is));
+        rec[NGRP + ft] = make_uint2(f16x2_of(ns[2] * ir, ns[2] * ir), f16x2_of(ns[3] * ir, ns[3] * ir));
+      }
+      sScale[(j % NSR) * NGRP + ft] = make_float4(s, log2f(r), 1.f / r, 0.f);
+    };
+    // A value that is not a number: noted for the rows that see it, 0 in the tile.
+    auto note_bad = [&](int pos) {
+      const int q0 = pos_first, q1 = min(p.q_start + g_row0(NG - 1) + BM, S_kv) - 1;   // the CTA's query positions
+      if (pos >= S_kv) return;
+      const int hi = pos - q0, lo = pos - (q0 - W + 1);
+      if (hi <= 0 && (W == 0 || pos > q1 - W))
+        bad[0] = 1;
+      else {
+        if (hi > 0 && hi < NG * BM) atomicOr(&bad[1 + (hi >> 5)], 1u << (hi & 31));
+        if (W > 0 && hi <= 0 && lo >= 0 && lo < NG * BM) atomicOr(&bad[9 + (lo >> 5)], 1u << (lo & 31));
+      }
+    };
+    constexpr int CPR = D / 16;                      // 16-byte runs of codes per row
+    constexpr int RUNS = BN * CPR;
+    constexpr int PER = (RUNS + 127) / 128;
+    // Tile j of codes -> fp16 in the swizzled layout.
+    auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, bool value) {
+      const int n0 = pos0 + j * BN;
+      const int nv = min(BN, S_kv - n0);
+      const uint2* ratio = sRatio + (size_t)(j % NSR) * 2 * NGRP + (value ? NGRP : 0);
+      const uint16_t* w = sW + (value ? 2 * D : 0);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int run = ft + 128 * i;
+        if (run >= RUNS) break;
+        const int row = run / CPR, c = run - row * CPR;
+        uint32_t o[8];
+        uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
+        if (row < nv) {
+          x = *reinterpret_cast<const uint4*>(raw + run * 16);
+          if constexpr (NSRC == 2) y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + run * 16);
+        }
+        uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        if (value) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) any |= nan_codes(xw[e]) | (NSRC == 2 ? nan_codes(yw[e]) : 0u);
+          if (any) {
+            note_bad(n0 + row);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              xw[e] &= ~((nan_codes(xw[e]) >> 7) * 255u);
+              yw[e] &= ~((nan_codes(yw[e]) >> 7) * 255u);
+            }
+          }
+        }
+        if constexpr (NSRC == 2) {
+          const uint2 rr = ratio[row >> 4];
+          const uint4 wa = *reinterpret_cast<const uint4*>(w + c * 16), wb = *reinterpret_cast<const uint4*>(w + c * 16 + 8);
+          const uint4 wc = *reinterpret_cast<const uint4*>(w + D + c * 16), wd = *reinterpret_cast<const uint4*>(w + D + c * 16 + 8);
+          const uint32_t w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+          const uint32_t w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t cx = e4m3x2_to_f16x2(xw[e >> 1] >> (16 * (e & 1)));
+            const uint32_t cy = e4m3x2_to_f16x2(yw[e >> 1] >> (16 * (e & 1)));
+            o[e] = hfma2u(hmul2u(cx, rr.x), w0[e], hmul2u(hmul2u(cy, rr.y), w1[e]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(xw[e >> 1] >> (16 * (e & 1)));
+        }
+        uint8_t* blk = dst + (size_t)(c >> 1) * BN * kSW;
+        *reinterpret_cast<uint4*>(blk + swz64(row, (c & 1) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(blk + swz64(row, (c & 1) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    };
+    load_scales(0);
+    store_scales(0);
+    // step 0 makes K_0; step k > 0 makes V_{k-1}, then K_k (k < n_max)
+    for (int k = 0; k <= n_max; ++k) {
+      const int t = k - 1;
+      load_scales(k + 1);
+      bool ok = true;
+      if (k > 0) {
+        ok = wait(&rv_full[t % NR], (uint32_t)(t / NR) & 1u);
+        if (ok && t >= NS) ok = wait(&v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u);
+      }
+      if (ok && k < n_max) {
+        ok = wait(&rk_full[k % NR], (uint32_t)(k / NR) & 1u);
+        if (ok && k >= NS) ok = wait(&k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u);
+      }
+      // one decision for all; and the records of this step's tiles are in place
+      if (!group_and(ok)) break;
+      if (k > 0) {
+        convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, true);
+        mbar_arrive(&rv_empty[t % NR]);
+      }
+      if (k < n_max) {
+        convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, false);
+        mbar_arrive(&rk_empty[k % NR]);
+      }
+      store_scales(k + 1);
+      // the tiles are read by the tensor cores (async proxy)
+      fence_proxy_async_smem();
+      mbar_arrive(&step_ready[k % NSR]);
+    }
+  } else if (warp >= C::SOFTMAX_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
+    if ((warp == C::K_PRODUCER_WARP || warp == C::V_PRODUCER_WARP) && lane == 0) {
+      // ---------------- producers: K codes, V codes ----------------
+      const bool is_k = warp == C::K_PRODUCER_WARP;
+      uint64_t* full = is_k ? rk_full : rv_full;
+      uint64_t* empty = is_k ? rk_empty : rv_empty;
+      uint8_t* ring = is_k ? sRawK : sRawV;
+      uint64_t policy;   // the CTAs of a unit read the same tiles
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+      int issued = 0;
+      for (int j = 0; j < n_max; ++j) {
+        if (j >= NR && !wait(&empty[j % NR], (uint32_t)(j / NR - 1) & 1u)) break;
+        const int n0 = pos0 + j * BN;
+        const int nv = min(BN, S_kv - n0);
+        const int row0 = p.ring > 0 ? n0 % p.ring : n0;
+        const int n1 = p.ring > 0 ? min(nv, p.ring - row0) : nv;
+        const uint32_t b1 = (uint32_t)n1 * D, b2 = (uint32_t)(nv - n1) * D;
+        mbar_arrive_expect_tx(&full[j % NR], (b1 + b2) * NSRC);
+#pragma unroll
+        for (int i = 0; i < NSRC; ++i) {
+          uint8_t* dst = ring + ((size_t)(j % NR) * NSRC + i) * C::RAW_BYTES;
+          const uint8_t* src = (is_k ? p.k[i] : p.v[i]) + (size_t)unit * p.rows * D;
+          bulk_g2s(dst, src + (size_t)row0 * D, b1, &full[j % NR], policy);
+          if (b2) bulk_g2s(dst + b1, src, b2, &full[j % NR], policy);
+        }
+        issued = j + 1;
+      }
+      sm_issued[is_k ? 0 : 1] = issued;
+    } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NG && lane == 0) {
+      // ---------------- MMA issuer of group g ----------------
+      const int g = warp - C::MMA_WARP;
+      constexpr uint32_t IDESC_QK = idesc_with_f16(idesc_bf16(BM, BN, false));
+      constexpr uint32_t IDESC_PV = idesc_with_f16(idesc_bf16(BM, D, true));
+      const uint32_t t_g = tmem + g * GROUP_COLS;
+      // S_g = Q_g K_j^T: A = Q_g from tensor memory (8 columns per step of 16
+      // channels), B = K_j (K-major), N = BN keys
+      auto issue_qk = [&](int j) {
+        const uint32_t kbase = smem_u32(tile_k(j));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)(k & 1) * 32;
+          const uint64_t bd = sdesc(kbase + (k >> 1) * BN * kSW + off, 16, 8 * kSW);
+          mma_bf16_ts(t_g, t_g + C::Q_COL + k * 8, bd, IDESC_QK, k > 0);
+        }
+      };
+      // O_g += P_g V_j: A = P_g (two per column, in the first BN/2 columns of
+      // S_g), B = V_j as an MN-major operand, K = BN keys
+      auto issue_pv = [&](int j) {
+        const uint32_t vbase = smem_u32(tile_v(j));
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k) {
+          const uint64_t bd = sdesc(vbase + k * 16 * kSW, BN * kSW, 8 * kSW);
+          mma_bf16_ts(t_g + C::O_COL, t_g + k * 8, bd, IDESC_PV, (j > 0 || k > 0) ? 1u : 0u);
+        }
+      };
+      // Step k of group g issues PV_g(k-1) (k > 0) and QK_g(k) (k < n_g), once
+      // conversion step k has put V_{k-1} and K_k in place.  The two issuers
+      // take turns, group 0's step k before group 1's: the turn is one more
+      // arrival on the other group's p_full, passed once a step's PV products
+      // are issued, so that each group's softmax overlaps the other group's
+      // products.  Group 1 of a one-head CTA may read up to two tiles more
+      // than group 0: group 0 then passes the turn for them, and their slots
+      // are never refilled (NS >= 2), so their empty phases are never awaited.
+      const int ng = n_tiles(g);
+      auto pass_turn = [&]() { mbar_arrive(&p_full[1 - g]); };
+      auto step_operands = [&](int k) {
+        return wait(&step_ready[k % NSR], (uint32_t)(k / NSR) & 1u);
+      };
+      bool ok = wait(q_ready, 0) && step_operands(0);
+      if (ok) {
+        tc_fence_after();
+        issue_qk(0);
+        mma_commit(&s_full[g]);
+        if (g == 1) pass_turn();   // group 0's step 1 follows group 1's step 0
+      }
+      for (int j = 0; ok && j < ng; ++j) {
+        const bool more = j + 1 < ng;
+        // every wait comes before the step's first product
+        if (!wait(&p_full[g], (uint32_t)j & 1u) || !step_operands(j + 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_pv(j);
+        pass_turn();
+        if (more) issue_qk(j + 1);
+        mma_commit(&s_full[g]);
+        // V_j was read by this step's PV products, K_j by the previous step's
+        mma_commit(&v_empty[j % NS]);
+        mma_commit(&k_empty[j % NS]);
+      }
+      // pass group 1's extra turns once the phase before has completed (an
+      // early arrival would count towards that phase)
+      if (g == 0)
+        for (int j = ng; ok && j < n_tiles(1); ++j) {
+          ok = wait(&p_full[1], (uint32_t)(j - 1) & 1u);
+          if (ok) pass_turn();
+        }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    // ---------------- softmax warpgroup of group g ----------------
+    const int g = warp >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int m_row = g_row0(g) + row;       // query row within the chunk
+    const int qpos = p.q_start + m_row;      // its cache position
+    const int pos_g = p.q_start + g_row0(g);
+    const int ng = n_tiles(g);
+    const bool row_valid = m_row < p.S;
+    const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + g * GROUP_COLS;
+    const uint32_t t_o = t_s + C::O_COL;
+    float c_row;   // what a raw score times its key scale is multiplied by
+    {
+      // this thread's Q row (times its key weights where one source has some)
+      // into tensor memory as D/2 packed fp16 pairs, its largest element in
+      // [2^14, 2^15); rows beyond the chunk, and the columns past D/2, are zero
+      const uint4* qrow = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(p.q) + (((size_t)b * H_q + g_head(g)) * p.S + m_row) * D);
+      const float* wa = NSRC == 1 && p.a[0] ? p.a[0] + (size_t)kh * D : nullptr;
+      float top = 0.f;
+      for (int i = 0; i < D / 8; ++i) {
+        float f[8];
+        unpack16<__nv_bfloat16>(row_valid ? qrow[i] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(wa ? f[e] * wa[i * 8 + e] : f[e]));
+      }
+      const int eq = top > 0.f && top < INFINITY ? 14 - exponent_of(top) : 0;
+      // two factors, since 2^eq alone may lie outside the normal range
+      const float f0 = power_of_two(eq / 2), f1 = power_of_two(eq - eq / 2);
+      c_row = p.scale_log2 / f0 / f1;
+      for (int c = 0; c < C::Q_COLS; c += 8) {
+        float qw[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ch = c / 4 + i;      // 16-byte chunk of Q
+          float f[8];
+          unpack16<__nv_bfloat16>(row_valid && ch < D / 8 ? qrow[ch] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (wa && ch < D / 8) f[e] *= wa[ch * 8 + e];
+            f[e] = f[e] * f0 * f1;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qw[4 * i + e] = __uint_as_float(f16x2_of(f[2 * e], f[2 * e + 1]));
+        }
+        tmem_st8(t_s + C::Q_COL + c, qw);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(q_ready);
+    }
+    if constexpr (NSRC == 2)   // the head's power of two of the key weights
+      c_row *= power_of_two(exponent_of(__uint_as_float(w_top[0])) + 1);
+    float m_run = -FLT_MAX, l_run = 0.f;
+    bool ok = true;
+    for (int j = 0; ok && j < ng; ++j) {
+      const int n0 = pos0 + j * BN;
+      // waits are made warp-uniform: tcgen05.ld/st below are warp-collective
+      // (the step's barrier, long since passed, orders the scale records)
+      if (!__all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)j & 1u) &&
+                                       wait(&step_ready[j % NSR], (uint32_t)(j / NSR) & 1u))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float sv[BN];
+#pragma unroll
+      for (int c = 0; c + 32 <= BN; c += 32) tmem_ld32(t_s + c, sv + c);
+      if constexpr (BN % 32 != 0) tmem_ld16(t_s + BN / 32 * 32, sv + BN / 32 * 32);
+      tmem_wait_ld();
+      // masking needed: the causal diagonal, the key extent, or (window) the
+      // lowest row-window start of the tile (warp-uniform)
+      const bool diag = n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W);
+      if (diag) {
+        // visible keys of this row, as tile columns: lo <= c < hi
+        const int hi = min(qpos + 1, S_kv) - n0;
+        const int lo = W > 0 ? qpos - W + 1 - n0 : INT_MIN;
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          if (c >= hi || c < lo) sv[c] = -INFINITY;
+      }
+      const float4* rec = sScale + (j % NSR) * NGRP;
+      // row max of score + log2 value scale: per group of 16 keys the raw
+      // scores' (the factors are positive, so it commutes)
+      float mt_row = -INFINITY;
+#pragma unroll
+      for (int gr = 0; gr < NGRP; ++gr) {
+        const float* x = sv + gr * 16;
+        const float m0 = fmax3f(fmaxf(x[0], x[1]), x[2], x[3]), m1 = fmax3f(fmaxf(x[4], x[5]), x[6], x[7]);
+        const float m2 = fmax3f(fmaxf(x[8], x[9]), x[10], x[11]), m3 = fmax3f(fmaxf(x[12], x[13]), x[14], x[15]);
+        const float4 sc = rec[gr];
+        const float f = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
+        mt_row = fmaxf(mt_row, fmaf(fmax3f(fmaxf(m0, m1), m2, m3), f, sc.y));
+      }
+      // Keep a stale max until it is exceeded by more than 2^8: P' stays below
+      // 2^15 and O needs no rescaling.
+      const float m_new = mt_row > m_run + kSlack ? mt_row : m_run;
+      const float alpha = fast_exp2(m_run - m_new);
+      const float neg_m = kBias - m_new;
+      float psum = 0.f;
+      // P' over the S tile just read: BN / 2 packed columns, 8 a group
+#pragma unroll
+      for (int gr = 0; gr < NGRP; ++gr) {
+        const float4 sc = rec[gr];
+        const float f = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
+        const float add = sc.y + neg_m;
+        float pk[8], ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int cc = gr * 16 + 2 * c;
+          // x = s * f + log2 r - m for two scores with one packed FMA; exp2(-inf) = 0
+          float x0 = add, x1 = add;
+          fma2(x0, x1, sv[cc], sv[cc + 1], f, f);
+          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+          add2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], e0, e1);
+          pk[c] = __uint_as_float(f16x2_of(e0, e1));
+        }
+        psum = fmaf((ps[0] + ps[1]) + (ps[2] + ps[3]), sc.z, psum);
+        tmem_st8(t_s + gr * 8, pk);
+      }
+      if (j > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
+        // O_g holds every PV product up to tile j-1 (s_full of tile j); the
+        // next one is issued only after p_full below
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float ov[16];
+          tmem_ld16(t_o + c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+          tmem_st16(t_o + c, ov);
+        }
+      }
+      l_run = l_run * alpha + psum;
+      m_run = m_new;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[g]);
+    }
+    // the commit after the last PV product is phase ng of s_full[g]
+    if (ok && __all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)ng & 1u) &&
+                                          wait(&step_ready[ng % NSR], (uint32_t)(ng / NSR) & 1u))) {
+      tc_fence_after();
+      // values that are not numbers among the keys that this row sees
+      bool nan = bad[0] != 0;
+      {
+        const int q0 = pos_first;
+        const int lo0 = q0 - W + 1;
+        for (int i = 0; i < 8; ++i) {
+          uint32_t x = *const_cast<volatile uint32_t*>(&bad[1 + i]);
+          while (x) {
+            const int pos = q0 + i * 32 + __ffs((int)x) - 1;
+            x &= x - 1;
+            nan = nan || (pos <= qpos && (W == 0 || pos > qpos - W));
+          }
+          x = *const_cast<volatile uint32_t*>(&bad[9 + i]);
+          while (x) {
+            const int pos = lo0 + i * 32 + __ffs((int)x) - 1;
+            x &= x - 1;
+            nan = nan || (pos <= qpos && pos > qpos - W);
+          }
+        }
+      }
+      float inv = nan ? __uint_as_float(0x7fffffffu) : 1.f / l_run;
+      if constexpr (NSRC == 2) inv *= power_of_two(exponent_of(__uint_as_float(w_top[1])) + 1);
+      const float* wb = NSRC == 1 && p.b[0] && p.a[0] ? p.b[0] + (size_t)kh * D : nullptr;
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
+                            (((size_t)b * H_q + g_head(g)) * p.S + m_row) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        float ov[16];
+        tmem_ld16(t_o + c, ov);
+        tmem_wait_ld();
+        if (wb) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ov[e] *= wb[c + e];
+        }
+        uint32_t o8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          __nv_bfloat162 v2 = __floats2bfloat162_rn(ov[2 * e] * inv, ov[2 * e + 1] * inv);
+          o8[e] = *reinterpret_cast<uint32_t*>(&v2);
+        }
+        if (row_valid) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c);
+          dst[0] = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+          dst[1] = make_uint4(o8[4], o8[5], o8[6], o8[7]);
+        }
+      }
+    }
+  }
+
+  // (a producer that stopped early has let its copies in flight land)
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out somewhere, so no role may have awaited the last copies
+    // and products: each producer lets its copies in flight land (the last NR
+    // tiles; an older one was consumed before its slot was refilled) and each
+    // issuer lets its own products finish, before the CTA frees tensor memory
+    // and exits.
+    if ((warp == C::K_PRODUCER_WARP || warp == C::V_PRODUCER_WARP) && lane == 0) {
+      const bool is_k = warp == C::K_PRODUCER_WARP;
+      const int issued = sm_issued[is_k ? 0 : 1];
+      for (int j = max(0, issued - NR); j < issued; ++j)
+        (void)mbar_wait_bounded(&(is_k ? rk_full : rv_full)[j % NR], (uint32_t)(j / NR) & 1u, kDrainLimitNs);
+    }
+    if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NG && lane == 0) {
+      mma_commit(&mma_drain[warp - C::MMA_WARP]);
+      (void)mbar_wait_bounded(&mma_drain[warp - C::MMA_WARP], 0, kDrainLimitNs);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == C::MMA_WARP) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int NSRC>
+cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, NSRC>;
+  Params p;
+  for (int i = 0; i < 2; ++i) {
+    p.k[i] = static_cast<const uint8_t*>(a.k[i]);
+    p.v[i] = static_cast<const uint8_t*>(a.v[i]);
+    p.ks[i] = a.k_scale[i];
+    p.vs[i] = a.v_scale[i];
+    p.a[i] = a.a[i];
+    p.b[i] = a.b[i];
+  }
+  p.q = a.q;
+  p.out = a.out;
+  p.status = a.status;
+  p.wait_limit = a.wait_limit;
+  p.H_kv = a.kv_heads;
+  p.G = a.group;
+  p.S = a.S;
+  p.q_start = a.q_start;
+  p.S_kv = a.q_start + a.S;
+  p.window = a.window;
+  p.rows = a.plane_rows;
+  p.ring = a.ring;
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  auto kern = prefill_q8_kernel<D, NSRC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  // The register split inside the kernel must fit the launch allocation, or
+  // the softmax warpgroups' increase would never be granted: refuse instead.
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if ((long long)fa.numRegs * C::THREADS < C::REGS_SPLIT) return cudaErrorNotSupported;
+  // one CTA per (unit, 128 query rows of two heads, or 256 of one)
+  const bool two_heads = a.group % 2 == 0;
+  const int rows_per_cta = two_heads ? BM : NG * BM;
+  const long long units = (long long)a.batch * a.kv_heads * (two_heads ? a.group / 2 : a.group);
+  const long long tiles = (a.S + rows_per_cta - 1) / rows_per_cta;
+  if (tiles > 65535 || units * tiles > INT_MAX) return cudaErrorNotSupported;
+  kern<<<dim3((unsigned)units, (unsigned)tiles), C::THREADS, C::SMEM, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace q8p
+}  // namespace fkv

@@ -156,14 +156,15 @@ int fkv_q8_scale_cols(int rows);
  * So rows are appended in order, as for a ring; rows taken back (a shorter
  * length, then an append there) are fine, and leave a scale that they raised.
  * Calls over 8-bit caches: fkv_append_kv, fkv_read_kv, fkv_decode_attn
- * (_noalloc), where every source of the call is 8-bit (a mix of formats is
- * FKV_ERR_UNSUPPORTED).  fkv_prefill_attn (_chunk) and fkv_tree_attn over them,
- * and fkv_compact_rows and fkv_reorder_seqs while a layer holds them, are
- * FKV_ERR_UNSUPPORTED.
+ * (_noalloc) and, in bf16 contexts, fkv_prefill_attn (_chunk), where every
+ * source of the call is 8-bit (a mix of formats is FKV_ERR_UNSUPPORTED).
+ * fkv_tree_attn over them, and fkv_compact_rows and fkv_reorder_seqs while a
+ * layer holds them, are FKV_ERR_UNSUPPORTED.
  * Rings: R a multiple of 32 (FKV_ERR_UNSUPPORTED otherwise, from the calls);
  * an append that comes round to a block loses the up to 31 older rows behind
- * the new ones in it, so fkv_append_kv needs T + 31 <= R (FKV_ERR_INVALID_ARG)
- * and fkv_decode_attn a window with window + 31 <= R (FKV_ERR_UNSUPPORTED). */
+ * the new ones in it, so fkv_append_kv needs T + 31 <= R (FKV_ERR_INVALID_ARG),
+ * fkv_decode_attn a window with window + 31 <= R, and fkv_prefill_attn_chunk,
+ * once positions have wrapped, C + window + 30 <= R (FKV_ERR_UNSUPPORTED). */
 fkv_status fkv_bind_layer_cache_q8(fkv_ctx* ctx, int layer, void* k_codes, void* v_codes,
                                    float* k_scales, float* v_scales);
 
@@ -326,7 +327,13 @@ fkv_status fkv_decode_attn_noalloc(fkv_ctx* ctx, const void* q, int layer, int m
  * q: device [B, H_q, S, D]; out: device [B, H_q, S, D]; context dtype.
  * Query row m sees key rows t <= m.  Modes and sources as for decode; fused
  * K/V tiles are built while staging them for the tensor cores.
- * Requires dtype FKV_BF16 (FKV_ERR_UNSUPPORTED otherwise); 1 <= S <= S_max. */
+ * Requires dtype FKV_BF16 (FKV_ERR_UNSUPPORTED otherwise); 1 <= S <= S_max.
+ * Over 8-bit caches H_q / H_kv may be 4 too, rings of any number of blocks
+ * serve (no key tile to be a multiple of), scores and values take fp16
+ * operands (the codes are exact in them; queries times key weights, fused rows
+ * and probabilities are rounded to 2^-11 or better, fused weights likewise),
+ * and a stored value that is not a number gives NaN in the rows that see it
+ * and does not reach the others. */
 fkv_status fkv_prefill_attn(fkv_ctx* ctx, const void* q, int layer, int mode, int S,
                             void* out, void* stream);
 

@@ -132,3 +132,45 @@ def check_decode(s, lens, q=None, what=""):
             worst = max(worst, float((err / bound).max()))
             assert bool((err <= bound).all()), "%s b=%d h=%d: %.2f of the bound" % (what, b, h, worst)
     return out, worst
+
+
+def check_prefill(s, q_start, C, q=None, what="", rows=None):
+    """One chunk against the reference, element by element (`rows`: of these chunk rows only)."""
+    q = s.query(s.batch, s.H * s.G, C, s.D) if q is None else q
+    out = torch.full_like(q, float("nan"))
+    s.ctx.fkv_prefill_attn_chunk(q, s.layer, s.mode, q_start, C, out)
+    assert s.ctx.fkv_get_device_status() == B.FKV_OK
+    K, V = s.rows()
+    w = [x.abs() for x in s.w]
+    Ka, Va = reconstruct(s.mode, w, [values(x).abs() for x in s.k], [values(x).abs() for x in s.v])
+    lo = max(0, q_start - s.window + 1) if s.window else 0
+    pos = torch.arange(lo, q_start + C, device="cuda")
+    at = pos % s.ring if s.ring else pos
+    sel = torch.arange(C, device="cuda") if rows is None else torch.tensor(rows, device="cuda")
+    mine = (q_start + sel)[:, None]
+    see = pos <= mine
+    if s.window:
+        see = see & (pos > mine - s.window)
+    # fp16 operands, 2^-11 a rounding.  Two sources: a weight, a ratio of scales and a product
+    # each round once, and their sum; a scaled query once.  P rounds once.
+    h = 2.0 ** -11
+    k_round = {"fused": 4, "scaled": 1}.get(s.mode, 0) * h
+    v_round = (1 + (4 if s.mode == "fused" else 0)) * h
+    n, worst = len(pos), 0.0
+    for b in range(s.batch):
+        for kh in range(s.H):
+            for g in range(kh * s.G, (kh + 1) * s.G):
+                qq = q[b, g, sel].double()
+                ref, _, _ = attend(qq, K[b, kh, at], V[b, kh, at], s.scale, see)
+                sc = (qq @ K[b, kh, at].T * s.scale).masked_fill(~see, -math.inf)
+                p = torch.softmax(sc, -1)
+                size = (qq.abs() @ Ka[b, kh, at].T * s.scale).masked_fill(~see, 0.0).amax(-1, keepdim=True)
+                pv = p @ Va[b, kh, at]
+                score = (k_round + (2 * s.D + 8) * 2.0 ** -23) * size + 2.0 ** -21
+                top = Va[b, kh, at].max()
+                # P below 2^-32 of its frame may vanish
+                bound = (2 * score + v_round + (n + 64) * 2.0 ** -23) * pv + n * 2.0 ** -31 * top + 2.0 ** -8 * ref.abs()
+                err = (out[b, g, sel].double() - ref).abs()
+                worst = max(worst, float((err / bound).max()))
+                assert bool((err <= bound).all()), "%s b=%d h=%d: %.2f of the bound" % (what, b, g, worst)
+    return out, worst
