@@ -8,25 +8,11 @@ cudaError_t decode_q8_launch_f32(const DecodeArgs& a, const DecodePlan& plan, cu
 
 namespace {
 
-template <int D, int NSRC, int G, bool F32>
-void q8_shape(int B, size_t* smem, int* warps) {
-  *smem = q8_smem_bytes<D, NSRC, G, F32>(B);
-  *warps = Q8Shape<NSRC, G, F32>::W;
-}
-
-template <int D, int NSRC, bool F32>
-void q8_shape_g(const DecodeArgs& a, size_t* smem, int* warps) {
-  if (a.group == 1) q8_shape<D, NSRC, 1, F32>(a.batch, smem, warps);
-  if (a.group == 2) q8_shape<D, NSRC, 2, F32>(a.batch, smem, warps);
-  if (a.group == 4) q8_shape<D, NSRC, 4, F32>(a.batch, smem, warps);
-}
-
 template <int D>
-void q8_shape_d(const DecodeArgs& a, size_t* smem, int* warps) {
-  if (a.is_f32)
-    a.nsrc == 2 ? q8_shape_g<D, 2, true>(a, smem, warps) : q8_shape_g<D, 1, true>(a, smem, warps);
-  else
-    a.nsrc == 2 ? q8_shape_g<D, 2, false>(a, smem, warps) : q8_shape_g<D, 1, false>(a, smem, warps);
+size_t q8_shape(const DecodeArgs& a, int* warps) {
+  *warps = a.nsrc == 2 ? Q8Shape<D, 2>::W : Q8Shape<D, 1>::W;
+  return a.nsrc == 2 ? q8_smem_bytes<D, 2>(a.batch, a.group)
+                     : q8_smem_bytes<D, 1>(a.batch, a.group);
 }
 
 }  // namespace
@@ -34,14 +20,14 @@ void q8_shape_d(const DecodeArgs& a, size_t* smem, int* warps) {
 cudaError_t decode_q8_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan) {
   size_t smem = 0;
   int W = 0;
+  if (a.group != 1 && a.group != 2 && a.group != 4) return cudaErrorNotSupported;
   switch (a.head_dim) {
-    case 64: q8_shape_d<64>(a, &smem, &W); break;
-    case 80: q8_shape_d<80>(a, &smem, &W); break;
-    case 96: q8_shape_d<96>(a, &smem, &W); break;
-    case 128: q8_shape_d<128>(a, &smem, &W); break;
+    case 64: smem = q8_shape<64>(a, &W); break;
+    case 80: smem = q8_shape<80>(a, &W); break;
+    case 96: smem = q8_shape<96>(a, &W); break;
+    case 128: smem = q8_shape<128>(a, &W); break;
     default: return cudaErrorNotSupported;
   }
-  if (W == 0) return cudaErrorNotSupported;
   const long long rows = (long long)a.batch * a.kv_heads * a.max_seq;
   long long ctas = a.num_ctas > 0 ? a.num_ctas : num_sms;
   const long long by_rows = (rows + 64LL * W - 1) / (64LL * W);
@@ -51,7 +37,7 @@ cudaError_t decode_q8_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan) {
   plan->warps_per_cta = W;
   plan->smem_bytes = smem;
   const size_t units = (size_t)a.batch * a.kv_heads;
-  const size_t slots = (size_t)ctas * W + units;
+  const size_t slots = (size_t)ctas + units;   // a CTA's partial of unit u: slot CTA + u
   plan->partial_bytes = (slots * a.group * partial_stride(a.head_dim) * sizeof(float) + 15) / 16 * 16;
   plan->workspace_bytes = plan->partial_bytes + units * sizeof(unsigned long long);
   return cudaSuccess;
