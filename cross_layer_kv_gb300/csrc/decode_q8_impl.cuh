@@ -23,28 +23,34 @@
 // share of a byte permute, for values) where scalar fp32 arithmetic costs
 // three to five.  Nothing goes back to shared memory, which is why these are
 // not tcgen05 products: their operands would have to be written there as fp16,
-// twice the bytes that arrive.  Scalar arithmetic measured 78 us on the 332M
-// Lite call and 515 us on the 4B fused one; see below for these.
+// twice the bytes that arrive.  332M Lite call (0.27 GB, 40 us at the measured
+// copy rate): 78 us with scalar arithmetic, 50 with these; 4B fused call of
+// full length (2.69 GB, 402 us): 549 us with 16 rows of values' products, 442
+// with the transposed ones below, which take half the registers and products.
 //
 // Scores: S [16 x 8 keys] = Q [16 x 16 channels] . K^T.  Row g < G of Q is
 // query head g of the group (times the key weights and a power of two), to
 // fp16; row g + 8 is what that rounding left, to fp16 again: 22 bits of the
 // query, at no cost, since the rows are there.
-// Values: O [16 x 8 channels] += P [16 x 16 keys] . V, where row g holds P'
-// rounded to fp16 and row g + 8 the rest.  With the value scale r in the
-// exponent, P' = p r = 2^(s + log2 r - M), no scale can take P' out of fp16's
-// range (M is the running maximum of that sum, with a slack of 2^8 before O is
-// rescaled); the softmax's sum takes P' / r.  Two value sources have one
+// Values: O^T [16 channels x 8] += V^T [16 x 16 keys] . P^T, whose column g is
+// head g (a score's place in the first product is its weight's place in the
+// second).  With the value scale r in the exponent, P' = p r = 2^(s + log2 r
+// - M), no scale can take P' out of fp16's range (M is the running maximum of
+// that sum, with a slack of 2^8 before O is rescaled); the softmax's sum takes
+// P' / r.  P' is rounded to fp16, 2^-12, for bf16 outputs; fp32 contexts add a
+// second product with what the rounding left.  Two value sources have one
 // exponent, of the larger scale, and two P with the factors r_i / r.
 //
 // Fragment layout: lane 4 n + q holds channels [q D/4, (q + 1) D/4) of key n
 // for the scores: contiguous bytes of a row, in which a step of 16 channels
 // takes 4 of each lane (the channels' order is the same in Q, so any will do).
 // For values, lane 4 n + q holds keys 2q, 2q+1, 2q+8, 2q+9 of the group and
-// the channels of column n, contiguous bytes again; a byte permute pairs two
-// keys' codes.  Which row of the group a key index stands for is free too, and
-// chosen so that the lanes of a load meet in few banks.
+// D/8 channels, contiguous bytes again, two to a product; a byte permute pairs
+// two keys' codes.  Which row of the group a key index stands for is free too,
+// and chosen so that the lanes of a load meet in few banks.
 #pragma once
+
+#include <type_traits>
 
 #include "decode_impl.cuh"
 #include "q8_device.cuh"
@@ -91,6 +97,11 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // (x, y) = hi + lo in fp16 pairs.
@@ -143,29 +154,26 @@ __device__ __forceinline__ void load_value(const uint8_t* row, int n, uint32_t* 
   }
 }
 
-// This lane's channels of head n8 as contiguous runs: kMain of them from
-// q4 * kMain, and the rest from 64 + q4 * kRest (D = 80, 96).
+// The channels of lane 4 n + q in the value products, in order: 8 (D = 128: 16)
+// from n * 8 (n * 16) on, then D = 80, 96: 2 or 4 of those behind the 64th.
 template <int D>
-struct Q8Runs {
-  static constexpr int kMain = D == 128 ? 32 : 16;
-  static constexpr int kRest = D / 4 - kMain;
-  // where column 2 q4 + e of value tile i lies in them
-  __device__ static constexpr int at(int e, int i) {
-    if (D == 128) return e * 16 + i;
-    return i < 8 ? e * 8 + i : kMain + e * (kRest / 2) + (i - 8);
-  }
-  __device__ static __forceinline__ int channel(int q4, int k) {
-    return k < kMain ? q4 * kMain + k : 64 + q4 * kRest + (k - kMain);
-  }
-};
-
-__device__ __forceinline__ void store4(float* dst, const float* x) {
-  *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ int value_channel(int n, int k) {
+  constexpr int main = D == 128 ? 16 : 8, rest = D / 8 - main;
+  return k < main ? n * main + k : 64 + n * rest + (k - main);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* x) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+
+__device__ __forceinline__ void store2(float* dst, float x, float y) {
+  *reinterpret_cast<float2*>(dst) = make_float2(x, y);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* dst, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(x, y);
+}
+
+// log2, within 2^-22 (exact for powers of two).
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Count one arrival on a unit's word for call `epoch`; the count with this one
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   constexpr int NS = S::NS, W = S::W;
   constexpr int PS = partial_stride(D);
   constexpr int KW = D / 16;          // words of codes a lane holds of a key; steps of 16 channels
-  constexpr int VT = D / 8;           // value tiles of 8 channels
+  constexpr int VT = D / 16;          // value tiles of 16 channels, 2 of a lane's
   constexpr int VW = (D + 31) / 32;   // words of codes a lane holds of a value row
   const int G = prm.G;
 
@@ -534,7 +542,9 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   const int vrow = 2 * q4 + (q4 & 1), vrow2 = vrow ^ 1;   // key_row(2q), key_row(2q + 1)
 
   uint32_t qf[NSRC][KW][4];    // Q fragments per source and step
-  float o[NSRC][VT][4];        // O fragments: rows g and g + 8
+  // O^T fragments: this lane's channels 2 i, 2 i + 1 of heads 2 q4 (elements
+  // 0, 2) and 2 q4 + 1 (1, 3)
+  float o[NSRC][VT][4];
   float c_row = 0.f;           // 2^-e of the head's query
   float m = -FLT_MAX, l = 0.f; // of head n8, this lane's keys
   bool fresh = true;
@@ -594,16 +604,6 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       fresh = false;
     }
 
-    int row0, nrows, n1;
-    tile_rows(b, t0, n, row0, nrows, n1);
-    const int skip = t0 == 0 ? first[b] % 16 : 0;   // rows of the first group before the first attended
-    const bool ragged = skip != 0 || nrows != 16 * GROUPS;
-    const int sc0 = row0 / (4 * kQ8Block) * 4;
-    // where the scale of the tile's group gr lies in a plane's run of scales
-    auto scale_at = [&](int gr) {
-      return 16 * gr < n1 ? (row0 + 16 * gr) / kQ8Block - sc0 : SCW + (16 * gr - n1) / kQ8Block;
-    };
-
     // warp-uniform: every lane leaves, or none does (shuffles follow)
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&wbars[stage], parity, wlim))) {
       flag_status(p.status, kDevTimeout);
@@ -614,118 +614,151 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       break;
     }
 
+    int row0, nrows, n1;
+    tile_rows(b, t0, n, row0, nrows, n1);
+    const int skip = t0 == 0 ? first[b] % 16 : 0;   // rows of the first group before the first attended
     const uint8_t* st = wring + (size_t)stage * STAGE;
     const float* scales = reinterpret_cast<const float*>(st + Cfg::CODE_BYTES);
 
-    // scores in base 2 plus the group's value exponent: s[gr][2 half + e] is
-    // key 2 q4 + e of the half
-    float s[GROUPS][4], lv[GROUPS];
-    float mt = -INFINITY;
+    // One tile.  EDGE: rows before `skip` or from nrows on are not attended, or
+    // the tile wraps in a ring.
+    auto tile = [&](auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+      // where the scale of the tile's group gr lies in a plane's run of scales
+      const int sc0 = row0 & (4 * kQ8Block - 1);
+      auto scale_at = [&](int gr) {
+        if (EDGE && 16 * gr >= n1) return SCW + (16 * gr - n1) / kQ8Block;
+        return (sc0 + 16 * gr) / kQ8Block;
+      };
+      // scores in base 2 plus the group's value exponent: s[gr][2 half + e] is
+      // key 2 q4 + e of the half
+      float s[GROUPS][4], lv[GROUPS];
+      float mt = -INFINITY;
 #pragma unroll
-    for (int gr = 0; gr < GROUPS; ++gr) {
-      if (ragged && 16 * gr >= nrows) {   // no such group in this tile
-        s[gr][0] = s[gr][1] = s[gr][2] = s[gr][3] = -INFINITY;
-        lv[gr] = 0.f;
-        continue;
-      }
-      const int at = scale_at(gr);
-      float vs = scales[NSRC * 2 * SCW + at];
-      if constexpr (NSRC == 2) vs = fmaxf(vs, scales[(NSRC + 1) * 2 * SCW + at]);
-      lv[gr] = log2f(vs);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[gr][e] = lv[gr];
-#pragma unroll
-      for (int sidx = 0; sidx < NSRC; ++sidx) {
-        const float f = scales[sidx * 2 * SCW + at] * c_row;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t kw[KW];
-          load_words<D / 4>(st + sidx * TILE + (16 * gr + 8 * half + krow) * D + q4 * (D / 4), kw);
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < KW; ++j)
-            mma16816(d, qf[sidx][j], e4m3x2_to_f16x2(kw[j]), e4m3x2_to_f16x2(kw[j] >> 16));
-          s[gr][2 * half] = fmaf(d[0] + d[2], f, s[gr][2 * half]);
-          s[gr][2 * half + 1] = fmaf(d[1] + d[3], f, s[gr][2 * half + 1]);
+      for (int gr = 0; gr < GROUPS; ++gr) {
+        if (EDGE && 16 * gr >= nrows) {   // no such group in this tile
+          s[gr][0] = s[gr][1] = s[gr][2] = s[gr][3] = -INFINITY;
+          lv[gr] = 0.f;
+          continue;
         }
-      }
-      if (ragged) {
-        // keys 2 q4, 2 q4 + 1 of the halves are these rows of the group
-        const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
-        if (ra < skip || ra >= nrows) s[gr][0] = -INFINITY;
-        if (rb < skip || rb >= nrows) s[gr][1] = -INFINITY;
-        if (ra + 8 < skip || ra + 8 >= nrows) s[gr][2] = -INFINITY;
-        if (rb + 8 < skip || rb + 8 >= nrows) s[gr][3] = -INFINITY;
-      }
-      mt = fmaxf(mt, fmaxf(fmaxf(s[gr][0], s[gr][1]), fmaxf(s[gr][2], s[gr][3])));
-    }
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-    const bool grow = mt > m + kQ8Slack;
-    if (__any_sync(0xffffffffu, grow)) {
-      const float m_new = grow ? mt : m;
-      const float alpha = fast_exp2(m - m_new);
-      l *= alpha;
+        const int at = scale_at(gr);
+        float vs = scales[NSRC * 2 * SCW + at];
+        if constexpr (NSRC == 2) vs = fmaxf(vs, scales[(NSRC + 1) * 2 * SCW + at]);
+        lv[gr] = fast_log2(vs);
 #pragma unroll
-      for (int sidx = 0; sidx < NSRC; ++sidx)
+        for (int e = 0; e < 4; ++e) s[gr][e] = lv[gr];
 #pragma unroll
-        for (int i = 0; i < VT; ++i)
+        for (int sidx = 0; sidx < NSRC; ++sidx) {
+          const float f = scales[sidx * 2 * SCW + at] * c_row;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[sidx][i][e] *= alpha;
-      m = m_new;
-    }
-
-    // values
-    const float off = kQ8Bias - m;
+          for (int half = 0; half < 2; ++half) {
+            uint32_t kw[KW];
+            load_words<D / 4>(st + sidx * TILE + (16 * gr + 8 * half + krow) * D + q4 * (D / 4), kw);
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int gr = 0; gr < GROUPS; ++gr) {
-      if (ragged && 16 * gr >= nrows) continue;
-      const int at = scale_at(gr);
-      float pv[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(s[gr][e] + off);
-      l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), fast_exp2(-lv[gr]), l);
-#pragma unroll
-      for (int sidx = 0; sidx < NSRC; ++sidx) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = pv[e];
-        if constexpr (NSRC == 2) {
-          const float ratio = scales[(NSRC + sidx) * 2 * SCW + at] * fast_exp2(-lv[gr]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= ratio;
-        }
-        uint32_t pa[4];
-        split_f16(x[0], x[1], pa[0], pa[1]);
-        split_f16(x[2], x[3], pa[2], pa[3]);
-        uint32_t va[VW], vb[VW], vc[VW], vd[VW];   // keys 2q, 2q + 1, 2q + 8, 2q + 9
-        const uint8_t* vt = st + (NSRC + sidx) * TILE + 16 * gr * D;
-        load_value<D>(vt + vrow * D, n8, va);
-        load_value<D>(vt + vrow2 * D, n8, vb);
-        load_value<D>(vt + (vrow + 8) * D, n8, vc);
-        load_value<D>(vt + (vrow2 + 8) * D, n8, vd);
-        if (ragged) {
-          // rows that are not attended may hold anything: nothing times 0
-          const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
-#pragma unroll
-          for (int i = 0; i < VW; ++i) {
-            if (ra < skip || ra >= nrows) va[i] = 0;
-            if (rb < skip || rb >= nrows) vb[i] = 0;
-            if (ra + 8 < skip || ra + 8 >= nrows) vc[i] = 0;
-            if (rb + 8 < skip || rb + 8 >= nrows) vd[i] = 0;
+            for (int j = 0; j < KW; ++j) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16(kw[j], b0, b1);
+              mma16816(d, qf[sidx][j], b0, b1);
+            }
+            s[gr][2 * half] = fmaf(d[0] + d[2], f, s[gr][2 * half]);
+            s[gr][2 * half + 1] = fmaf(d[1] + d[3], f, s[gr][2 * half + 1]);
           }
         }
+        if constexpr (EDGE) {
+          // keys 2 q4, 2 q4 + 1 of the halves are these rows of the group
+          const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
+          if (ra < skip || ra >= nrows) s[gr][0] = -INFINITY;
+          if (rb < skip || rb >= nrows) s[gr][1] = -INFINITY;
+          if (ra + 8 < skip || ra + 8 >= nrows) s[gr][2] = -INFINITY;
+          if (rb + 8 < skip || rb + 8 >= nrows) s[gr][3] = -INFINITY;
+        }
+        mt = fmaxf(mt, fmaxf(fmaxf(s[gr][0], s[gr][1]), fmaxf(s[gr][2], s[gr][3])));
+      }
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      const bool grow = mt > m + kQ8Slack;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? mt : m;
+        const float alpha = fast_exp2(m - m_new);
+        l *= alpha;
+        m = m_new;
+        // of the heads whose O this lane holds
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * q4), a1 = __shfl_sync(0xffffffffu, alpha, 8 * q4 + 4);
 #pragma unroll
-        for (int i = 0; i < VT; i += 2) {
-          // channels i, i + 1 of both pairs of keys: bytes (a_i, b_i, a_i+1, b_i+1)
-          const uint32_t sel = i & 2 ? 0x7362u : 0x5140u;
-          const uint32_t ab = __byte_perm(va[i / 4], vb[i / 4], sel);
-          const uint32_t cd = __byte_perm(vc[i / 4], vd[i / 4], sel);
-          mma16816(o[sidx][i], pa, e4m3x2_to_f16x2(ab), e4m3x2_to_f16x2(cd));
-          mma16816(o[sidx][i + 1], pa, e4m3x2_to_f16x2(ab >> 16), e4m3x2_to_f16x2(cd >> 16));
+        for (int sidx = 0; sidx < NSRC; ++sidx)
+#pragma unroll
+          for (int i = 0; i < VT; ++i) {
+            o[sidx][i][0] *= a0;
+            o[sidx][i][1] *= a1;
+            o[sidx][i][2] *= a0;
+            o[sidx][i][3] *= a1;
+          }
+      }
+
+      // values
+      const float off = kQ8Bias - m;
+#pragma unroll
+      for (int gr = 0; gr < GROUPS; ++gr) {
+        if (EDGE && 16 * gr >= nrows) continue;
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(s[gr][e] + off);
+        const float rv = fast_exp2(-lv[gr]);
+        l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), rv, l);
+#pragma unroll
+        for (int sidx = 0; sidx < NSRC; ++sidx) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = pv[e];
+          if constexpr (NSRC == 2) {
+            const float ratio = scales[(NSRC + sidx) * 2 * SCW + scale_at(gr)] * rv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] *= ratio;
+          }
+          uint32_t ph[2];
+          [[maybe_unused]] uint32_t pl[2];
+          if constexpr (sizeof(T) == 4) {
+            split_f16(x[0], x[1], ph[0], pl[0]);
+            split_f16(x[2], x[3], ph[1], pl[1]);
+          } else {
+            ph[0] = f16x2_of(x[0], x[1]);
+            ph[1] = f16x2_of(x[2], x[3]);
+          }
+          uint32_t va[VW], vb[VW], vc[VW], vd[VW];   // keys 2q, 2q + 1, 2q + 8, 2q + 9
+          const uint8_t* vt = st + (NSRC + sidx) * TILE + 16 * gr * D;
+          load_value<D>(vt + vrow * D, n8, va);
+          load_value<D>(vt + vrow2 * D, n8, vb);
+          load_value<D>(vt + (vrow + 8) * D, n8, vc);
+          load_value<D>(vt + (vrow2 + 8) * D, n8, vd);
+          if constexpr (EDGE) {
+            // rows that are not attended may hold anything: nothing times 0
+            const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+              if (ra < skip || ra >= nrows) va[i] = 0;
+              if (rb < skip || rb >= nrows) vb[i] = 0;
+              if (ra + 8 < skip || ra + 8 >= nrows) vc[i] = 0;
+              if (rb + 8 < skip || rb + 8 >= nrows) vd[i] = 0;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < VT; ++i) {
+            // channels 2 i, 2 i + 1 of both pairs of keys: bytes (a, b, a', b')
+            const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+            uint32_t f[4];
+            e4m3x4_to_f16(__byte_perm(va[i / 2], vb[i / 2], sel), f[0], f[1]);
+            e4m3x4_to_f16(__byte_perm(vc[i / 2], vd[i / 2], sel), f[2], f[3]);
+            mma16816(o[sidx][i], f, ph[0], ph[1]);
+            if constexpr (sizeof(T) == 4) mma16816(o[sidx][i], f, pl[0], pl[1]);
+          }
         }
       }
-    }
+    };
+    if (skip != 0 || nrows != 16 * GROUPS || n1 != nrows)
+      tile(std::true_type{});
+    else
+      tile(std::false_type{});
 
     ++consumed;
     __syncwarp();
@@ -743,41 +776,38 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       // the range's part of the unit is complete: finish the unit if that is
       // all of it, else leave a partial
       const int u = b * H + h;
-      using Runs = Q8Runs<D>;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       const bool ends = t0 + n == lens[b];
-      float x[D / 4];
+      float* rec = whole ? reinterpret_cast<float*>(wring) : sh.head_rec + (size_t)warp * G * PS;
 #pragma unroll
-      for (int i = 0; i < VT; ++i)
+      for (int e = 0; e < 2; ++e) {
+        const int head = 2 * q4 + e;
+        const float inv = 1.f / __shfl_sync(0xffffffffu, l, 8 * q4 + 4 * e);
+        if (head >= G) continue;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int k = Runs::at(e, i);
-          const size_t ch = (size_t)h * D + Runs::channel(q4, k);
-          x[k] = o[0][i][e] + o[0][i][e + 2];
-          if (NSRC == 2)
-            x[k] = x[k] * p.b0[ch] + (o[NSRC - 1][i][e] + o[NSRC - 1][i][e + 2]) * p.b1[ch];
-          else if (p.b0)
-            x[k] *= p.b0[ch];
-        }
-      if (n8 < G) {
-        if (whole && ends) {
-          const float inv = 1.f / l;
-          T* row = static_cast<T*>(p.out) + ((size_t)u * G + n8) * D;
-#pragma unroll
-          for (int k = 0; k < D / 4; k += 4) {
-            const float y[4] = {x[k] * inv, x[k + 1] * inv, x[k + 2] * inv, x[k + 3] * inv};
-            store4(row + Runs::channel(q4, k), y);
+        for (int i = 0; i < VT; ++i) {
+          const int c = value_channel<D>(n8, 2 * i);
+          float x = o[0][i][e], y = o[0][i][e + 2];
+          if (NSRC == 2 || p.b0) {
+            const float2 w0 = *reinterpret_cast<const float2*>(p.b0 + (size_t)h * D + c);
+            x *= w0.x;
+            y *= w0.y;
           }
-        } else {
-          float* rec = (whole ? reinterpret_cast<float*>(wring) : sh.head_rec + (size_t)warp * G * PS) + n8 * PS;
-#pragma unroll
-          for (int k = 0; k < D / 4; k += 4) store4(rec + Runs::channel(q4, k), x + k);
-          if (q4 == 0) {
-            rec[D] = m;
-            rec[D + 1] = l;
+          if constexpr (NSRC == 2) {
+            const float2 w1 = *reinterpret_cast<const float2*>(p.b1 + (size_t)h * D + c);
+            x = fmaf(o[1][i][e], w1.x, x);
+            y = fmaf(o[1][i][e + 2], w1.y, y);
           }
+          if (whole && ends)
+            store2(static_cast<T*>(p.out) + ((size_t)u * G + head) * D + c, x * inv, y * inv);
+          else
+            store2(rec + head * PS + c, x, y);
         }
+      }
+      if (!(whole && ends) && n8 < G && q4 == 0) {
+        rec[n8 * PS + D] = m;
+        rec[n8 * PS + D + 1] = l;
       }
       if (lane == 0 && !(whole && ends)) (whole ? sh.tail : sh.head)[warp] = u;
       fresh = true;

@@ -353,14 +353,17 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
           const uint32_t w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
           const uint32_t w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t cx = e4m3x2_to_f16x2(xw[e >> 1] >> (16 * (e & 1)));
-            const uint32_t cy = e4m3x2_to_f16x2(yw[e >> 1] >> (16 * (e & 1)));
-            o[e] = hfma2u(hmul2u(cx, rr.x), w0[e], hmul2u(hmul2u(cy, rr.y), w1[e]));
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t cx[2], cy[2];
+            e4m3x4_to_f16(xw[e >> 1], cx[0], cx[1]);
+            e4m3x4_to_f16(yw[e >> 1], cy[0], cy[1]);
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              o[e + f] = hfma2u(hmul2u(cx[f], rr.x), w0[e + f], hmul2u(hmul2u(cy[f], rr.y), w1[e + f]));
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(xw[e >> 1] >> (16 * (e & 1)));
+          for (int e = 0; e < 8; e += 2) e4m3x4_to_f16(xw[e >> 1], o[e], o[e + 1]);
         }
         uint8_t* blk = dst + (size_t)(c >> 1) * BN * kSW;
         *reinterpret_cast<uint4*>(blk + swz64(row, (c & 1) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);

@@ -19,13 +19,12 @@
 
 namespace fkv {
 
-// Two e4m3 codes (the low one first) -> fp16, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r)
+// Four e4m3 codes -> two fp16 pairs (the lower codes first), exactly.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  return r;
 }
 
 // Two fp32 -> e4m3 codes (x in the low byte): nearest even, above 448 to 448,
@@ -40,7 +39,8 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float x, float y) {
 
 // Four codes in a word -> fp32, exactly.
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
-  const uint32_t h0 = e4m3x2_to_f16x2(w), h1 = e4m3x2_to_f16x2(w >> 16);
+  uint32_t h0, h1;
+  e4m3x4_to_f16(w, h0, h1);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
   f[0] = a.x;

@@ -274,6 +274,9 @@ size_t fkv_decode_workspace_bytes(const fkv_ctx* ctx);
  * [0, seq_lens[b]) (the new token already appended).  A length outside
  * [1, S_max] is clamped (0 yields a zero output) and flagged as
  * FKV_ERR_DEVICE_ARG in the device status.
+ * Rounding: fp32 throughout; over 8-bit caches queries times key weights keep
+ * 22 bits, and bf16 contexts round each probability to fp16 for its product
+ * with the values.
  * mode: for storage layers every mode is plain attention over the layer's own
  * cache; for upper layers FKV_VANILLA reads the layer's own cache (needs
  * store_upper), FKV_LITE reads K^n and V^1, FKV_FUSED reads K^1, K^n, V^1, V^n

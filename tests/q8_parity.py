@@ -61,10 +61,12 @@ def decode_bound(ref, size, pv, D, n, dtype):
     """How far fp32 arithmetic may be off: a score is a sum of 2 D products with prescaled queries
     (three roundings each) and their scales, the exponential and its base add 2^-21, a softmax
     weight is off by twice a score's error, and n weighted values are added up in fp32; then one
-    rounding of the output."""
-    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    rounding of the output.  bf16 contexts round each weight to fp16 for its product with a value
+    (the softmax's sum takes it unrounded): a factor 1 + d, |d| <= 2^-11, on each term of sum p V,
+    so at most 2^-11 sum p |V|."""
+    u, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 0.0)
     score = (2 * D + 8) * 2.0 ** -24 * size + 2.0 ** -21
-    return (2 * score + (n + 64) * 2.0 ** -24) * pv + u * ref.abs()
+    return (2 * score + w + (n + 64) * 2.0 ** -24) * pv + u * ref.abs()
 
 
 class Setup:
