@@ -9,7 +9,7 @@
 //
 // The operands are fp16, which holds every e4m3 code exactly, and the scales
 // stay outside the products.  With K_t = s_t k_t and V_t = r_t v_t (k, v the
-// tile's fp16 elements; s, r the same for 16 keys in a row of a tile),
+// tile's fp16 elements; s, r the same for a block of 32 keys),
 //     o = sum_t p_t r_t v_t / sum_t p_t,
 //     p_t r_t = 2^(c s_t (q . k_t) + log2 r_t),   c = scale * log2 e,
 // so a key scale multiplies the score and a value scale's logarithm is added
@@ -18,18 +18,19 @@
 // scales are.  The softmax's sum takes p = P' / r.  A row of Q (times its key
 // weights in the scaled mode) is brought to fp16 with a power of two that
 // places its largest element below 2^15.  Two sources are combined as
-//     w0 c0 (s0 / s) + w1 c1 (s1 / s),  s = max(s0, s1),
-// in packed fp16 arithmetic, with the head's weights brought below 1 by one
-// power of two.
+//     w0 (c0 (s0 / s)) + w1 (c1 (s1 / s)),  s = max(s0, s1),
+// in packed fp16 arithmetic (four instructions for two channels), with the
+// head's weights brought below 1 by one power of two.
 //
-// Structure (as prefill_fused_wide.cu): a CTA owns two groups of 128 query
-// rows over the same keys (two heads of a KV head, or two row tiles of one
-// head), each with a softmax warpgroup and an MMA-issuing warp that takes
-// turns with the other's; Q, S / P and O live in tensor memory.  Two warps
+// Structure (as prefill_wide.cu): a CTA owns two groups of 128 query rows over
+// the same keys (two heads of a KV head, or two row tiles of one head), each
+// with a softmax warpgroup and an MMA-issuing warp that takes turns with the
+// other's; S / P and O live in tensor memory, Q in shared memory.  Two warps
 // bring tiles of codes by cp.async.bulk (a tile's rows are contiguous, in two
 // pieces where a ring wraps, so no ring size is excluded), and a conversion
 // warpgroup writes the fp16 tiles in the swizzled layout that the MMAs read.
-// Its step k makes V_{k-1} and K_k, what MMA step k reads.
+// Its step k makes V_{k-1} and K_k, what MMA step k reads.  Tiles start at
+// multiples of 32 keys, so that a block of one scale is whole in its tile.
 //
 // Key rows that a query may not see do not reach it, whatever they hold:
 // scores are masked by position, and a value that is not a number is 0 in the
@@ -42,6 +43,7 @@
 #include <cfloat>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "fkv_kernels.h"
 #include "q8_device.cuh"
@@ -52,33 +54,36 @@ namespace q8p {
 
 constexpr int BM = 128;            // query rows per group
 constexpr int NG = 2;              // groups per CTA
-constexpr int GROUP_COLS = 256;    // TMEM columns per group: S/P, O, Q
+constexpr int GROUP_COLS = 256;    // TMEM columns per group: S/P, O
 constexpr int SMEM_LIMIT = 232448; // opt-in dynamic shared memory per CTA (227 KB)
 constexpr float kSlack = 8.f;      // log2 growth of the running max tolerated before O is rescaled
 constexpr float kBias = 7.f;       // P' <= 2^(7 + 8) < 65504, and is not flushed above 2^-31
 constexpr int NSR = 8;             // conversion-step barriers and scale records
-constexpr int NR = 2;              // slots of codes
 
-constexpr int cap4(int x) { return x > 4 ? 4 : x; }
+constexpr int cap(int x, int most) { return x > most ? most : x; }
 
 template <int D, int NSRC>
 struct Cfg {
-  static constexpr int BN = D <= 96 ? 112 : 64;        // keys per tile: S, O and Q fill 256 columns
-  static constexpr int NGRP = BN / 16;                  // key groups of one scale
+  // keys per tile; at D = 128 two sources' codes leave room for 96
+  static constexpr int BN = D == 128 && NSRC == 2 ? 96 : 128;
+  static constexpr int NGRP = BN / kQ8Block;            // blocks of a tile
   static constexpr int CB = (D + kSWE - 1) / kSWE;      // 32-element column blocks
+  static constexpr int Q_BYTES = CB * BM * kSW;         // one group's Q tile
   static constexpr int KV_BYTES = CB * BN * kSW;        // one fp16 tile
   static constexpr int RAW_BYTES = BN * D;              // one tile of codes of one source
   static constexpr int O_COL = BN;
-  static constexpr int Q_COLS = (D / 2 + 15) / 16 * 16;
-  static constexpr int Q_COL = GROUP_COLS - Q_COLS;
-  static_assert(O_COL + D <= Q_COL, "S, O and Q do not fit a group's 256 columns");
-  // fp16 weights [4][D], scale records [NSR][NGRP] float4, ratios [NSR][2][NGRP] half2, barriers and words
-  static constexpr int FIXED = 4 * D * 2 + NSR * NGRP * 16 + NSR * 2 * NGRP * 8 + 1024;
-  static constexpr int RAW = NR * 2 * NSRC * RAW_BYTES;
-  static constexpr int NS = cap4((SMEM_LIMIT - 512 - FIXED - RAW) / (2 * KV_BYTES));   // K and V slots
-  static_assert(NS >= 2, "shared memory too small for the tiles");
-  static_assert(NSR > NS + 1, "step barriers must outnumber the tile slots");
-  static constexpr size_t SMEM = 512 + (size_t)FIXED + RAW + (size_t)2 * NS * KV_BYTES;
+  static_assert(O_COL + D <= GROUP_COLS, "S and O do not fit a group's columns");
+  // fp16 weights [4][D], scale records [NSR][NGRP] float4, [NSR][2][NGRP] ratios, barriers and words
+  static constexpr int FIXED =
+      (NSRC == 2 ? 4 * D * 2 + NSR * 2 * NGRP * 8 : 0) + NSR * NGRP * 16 + 512;
+  static constexpr int ROOM = SMEM_LIMIT - 512 - FIXED - NG * Q_BYTES;
+  static constexpr int NS = 2;   // K and V slots: a K slot is freed by its only product, a step before its V's
+  static constexpr int NR = cap((ROOM - 2 * NS * KV_BYTES) / (2 * NSRC * RAW_BYTES), 2);   // slots of codes
+  static_assert(NR >= 1, "shared memory too small for the tiles");
+  static_assert(NSR > NS + 2, "step barriers must outnumber the tile slots");
+  static constexpr size_t SMEM =
+      512 + (size_t)FIXED + NG * Q_BYTES + (size_t)2 * NR * NSRC * RAW_BYTES + (size_t)2 * NS * KV_BYTES;
+  static_assert(SMEM <= SMEM_LIMIT, "shared memory above the opt-in limit");
   static constexpr int SOFTMAX_WARPS = 4 * NG;
   static constexpr int K_PRODUCER_WARP = SOFTMAX_WARPS;
   static constexpr int MMA_WARP = K_PRODUCER_WARP + 1;   // + g for group g
@@ -86,7 +91,7 @@ struct Cfg {
   static constexpr int CONV_WARP = SOFTMAX_WARPS + 4;
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 8);
   // registers: 128 per thread at launch (65536 / 512)
-  static constexpr int REGS_CONTROL = 48, REGS_CONV = 88, REGS_SOFTMAX = 184;
+  static constexpr int REGS_CONTROL = 40, REGS_CONV = NSRC == 2 ? 104 : 72, REGS_SOFTMAX = NSRC == 2 ? 184 : 200;
   static constexpr long long REGS_SPLIT =
       (long long)NG * 128 * REGS_SOFTMAX + 128LL * REGS_CONTROL + 128LL * REGS_CONV;
   static_assert(REGS_SPLIT <= (long long)THREADS * 128, "register split above the launch allocation");
@@ -139,6 +144,27 @@ __device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Packed fp32 pairs as 64-bit operands (made once where a pair is used often:
+// the compiler copies both halves for every use of a pair made in place).
+__device__ __forceinline__ unsigned long long pair_of(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ unsigned long long ffma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Whether one of four codes is not a number.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -154,23 +180,24 @@ __device__ __forceinline__ float power_of_two(int e) {   // e clamped to the nor
 template <int D, int NSRC>
 __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(const Params p) {
   using C = Cfg<D, NSRC>;
-  constexpr int BN = C::BN, NS = C::NS, NGRP = C::NGRP;
+  constexpr int BN = C::BN, NS = C::NS, NGRP = C::NGRP, NR = C::NR;
   extern __shared__ uint8_t smem_raw[];
   // 512-byte alignment: the period of the 64-byte swizzle pattern
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~uintptr_t(511));
-  uint8_t* sK = smem;                                   // fp16 tiles
+  uint8_t* sQ = smem;                                   // fp16 queries of the two groups
+  uint8_t* sK = sQ + NG * C::Q_BYTES;                   // fp16 tiles
   uint8_t* sV = sK + NS * C::KV_BYTES;
   uint8_t* sRawK = sV + NS * C::KV_BYTES;               // codes, the sources of a slot side by side
   uint8_t* sRawV = sRawK + NR * NSRC * C::RAW_BYTES;
   float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s, log2 r, 1 / r, -}
-  // (s0 / s, s1 / s) of K and V, each as two equal halves
+  // of K and V: (s0 / s, s1 / s), each as two equal halves
   uint2* sRatio = reinterpret_cast<uint2*>(sScale + NSR * NGRP);
-  uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + NSR * 2 * NGRP);            // fp16 a0, a1, b0, b1
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sW + 4 * D);
+  uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + (NSRC == 2 ? NSR * 2 * NGRP : 0));   // fp16 a0, a1, b0, b1
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sW + (NSRC == 2 ? 4 * D : 0));
   uint64_t* q_ready = bars;
-  uint64_t* k_empty = q_ready + 1;        // [4]
-  uint64_t* v_empty = k_empty + 4;        // [4]
-  uint64_t* rk_full = v_empty + 4;        // [NR]
+  uint64_t* k_empty = q_ready + 1;        // [NS]
+  uint64_t* v_empty = k_empty + NS;       // [NS]
+  uint64_t* rk_full = v_empty + NS;       // [NR]
   uint64_t* rk_empty = rk_full + NR;
   uint64_t* rv_full = rk_empty + NR;
   uint64_t* rv_empty = rv_full + NR;
@@ -201,9 +228,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   const int S_kv = p.S_kv;
   const int W = p.window;
   // key tiles of positions pos0 + j * BN: from the first group's window start
-  // (down to 16 keys, which have one scale) to each group's last position
+  // (down to the start of its block) to each group's last position
   const int pos_first = p.q_start + g_row0(0);
-  const int pos0 = W > 0 ? max(0, pos_first - W + 1) / 16 * 16 : 0;
+  const int pos0 = W > 0 ? max(0, pos_first - W + 1) / kQ8Block * kQ8Block : 0;
   auto n_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) - pos0 + BN - 1) / BN; };
   const int n_max = max(n_tiles(0), n_tiles(1));
 
@@ -213,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   if (tid == 0) {
     mbar_init(q_ready, 128 * NG);
     for (int s = 0; s < NSR; ++s) mbar_init(&step_ready[s], 128);
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < NS; ++s) {
       mbar_init(&k_empty[s], NG);    // one commit per group that reads the tile
       mbar_init(&v_empty[s], NG);
     }
@@ -272,12 +299,12 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     // ---------------- conversion warpgroup ----------------
     const int ft = tid - 32 * C::CONV_WARP;   // 0..127
     const size_t scols = (size_t)q8_scale_cols(p.rows);
-    // Scale records of tile j, one thread per group of 16 keys.
+    // Scale records of tile j, one thread per block.
     float ns[2 * NSRC];
     auto load_scales = [&](int j) {
-      const int pos = pos0 + j * BN + ft * 16;
+      const int pos = pos0 + j * BN + ft * kQ8Block;
 #pragma unroll
-      for (int i = 0; i < 2 * NSRC; ++i) ns[i] = 1.f;   // (groups behind the last key: any finite one)
+      for (int i = 0; i < 2 * NSRC; ++i) ns[i] = 1.f;   // (blocks behind the last key: any finite one)
       if (ft < NGRP && j < n_max && pos < S_kv) {
         const size_t at = (size_t)unit * scols + (p.ring > 0 ? pos % p.ring : pos) / kQ8Block;
 #pragma unroll
@@ -312,63 +339,140 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         if (W > 0 && hi <= 0 && lo >= 0 && lo < NG * BM) atomicOr(&bad[9 + (lo >> 5)], 1u << (lo & 31));
       }
     };
-    constexpr int CPR = D / 16;                      // 16-byte runs of codes per row
-    constexpr int RUNS = BN * CPR;
-    constexpr int PER = (RUNS + 127) / 128;
-    // Tile j of codes -> fp16 in the swizzled layout.
-    auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, bool value) {
-      const int n0 = pos0 + j * BN;
-      const int nv = min(BN, S_kv - n0);
-      const uint2* ratio = sRatio + (size_t)(j % NSR) * 2 * NGRP + (value ? NGRP : 0);
-      const uint16_t* w = sW + (value ? 2 * D : 0);
+    // A tile is runs of 16 codes, D / 16 a row, which become two 16-byte chunks
+    // of the swizzled tile each.  The 8 threads that a shared-memory pass
+    // serves take 4 rows times 2 runs of a 32-channel block: their chunks lie
+    // in 8 different bank groups.  Where the blocks are even in number, rows
+    // of the other row pair take the neighbouring block, so that the reads of
+    // 64- and 128-byte rows spread over the banks too (2 passes at most).
+    constexpr int CPR = D / 16, CP = CPR / 2;
+    constexpr bool TWO = CP % 2 == 0;                // threads over 32 rows and 2 blocks, or 64 rows and 1
+    constexpr int RI = TWO ? 32 : 64;                // rows of an item of 128 runs
+    constexpr int KI = BN / RI;
+    constexpr int PAIRED = (TWO ? CP / 2 : CP) * KI; // items; a D = 80 row's fifth run adds one (row = thread)
+    constexpr int ITEMS = PAIRED + CPR % 2;
+    static_assert(BN % RI == 0 && (CPR % 2 == 0 || BN == 128), "items of 128 runs");
+    const int rr = (ft >> 1) & 3;
+    const int row0 = (TWO ? ft >> 4 : ft >> 3) * 4 + rr;
+    const int blk0 = TWO ? ((ft >> 3) ^ (rr >> 1)) & 1 : 0;
+    const uint32_t raw0 = (uint32_t)(row0 * D + blk0 * 32 + (ft & 1) * 16);
+    const uint32_t place0 = (uint32_t)(blk0 * BN * kSW) + swz64(row0, (ft & 1) * 2);
+    const uint32_t place80 = (uint32_t)(CP * BN * kSW) + swz64(ft, 0);
+    // item -> row, run in the row, offsets of the codes and of the first chunk (the other: ^ 16)
+    auto item_row = [&](int it) { return it < PAIRED ? row0 + it % KI * RI : ft; };
+    auto item_run = [&](int it) {
+      return it < PAIRED ? 2 * (blk0 + it / KI * (TWO ? 2 : 1)) + (ft & 1) : CPR - 1;
+    };
+    auto item_raw = [&](int it) {
+      return it < PAIRED ? raw0 + (uint32_t)(it % KI * RI * D + it / KI * (TWO ? 64 : 32))
+                         : (uint32_t)(ft * D + (CPR - 1) * 16);
+    };
+    auto item_place = [&](int it) {
+      return it < PAIRED ? place0 + (uint32_t)(it % KI * RI * kSW + it / KI * (TWO ? 2 : 1) * BN * kSW) : place80;
+    };
+    // The head's fp16 weights of both sources for 16 channels.
+    struct Weights {
+      uint32_t w[2][8];
+    };
+    auto load_weights = [&](int it, bool value, Weights& w) {
+      if constexpr (NSRC == 2) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int run = ft + 128 * i;
-        if (run >= RUNS) break;
-        const int row = run / CPR, c = run - row * CPR;
-        uint32_t o[8];
-        uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
-        if (row < nv) {
-          x = *reinterpret_cast<const uint4*>(raw + run * 16);
-          if constexpr (NSRC == 2) y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + run * 16);
+        for (int i = 0; i < 2; ++i) {
+          const uint4* src = reinterpret_cast<const uint4*>(sW + (value ? 2 * D : 0) + i * D + item_run(it) * 16);
+          const uint4 x = src[0], y = src[1];
+          w.w[i][0] = x.x, w.w[i][1] = x.y, w.w[i][2] = x.z, w.w[i][3] = x.w;
+          w.w[i][4] = y.x, w.w[i][5] = y.y, w.w[i][6] = y.z, w.w[i][7] = y.w;
         }
-        uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-        if (value) {
-          uint32_t any = 0;
+      }
+    };
+    // 16 codes of one source or two -> 8 fp16 pairs; r: the sources' scales over the larger one
+    auto combine = [&](const uint4& x, const uint4& y, const uint2& r, const Weights& w, uint32_t* o) {
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+      if constexpr (NSRC == 2) {
+        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) any |= nan_codes(xw[e]) | (NSRC == 2 ? nan_codes(yw[e]) : 0u);
-          if (any) {
-            note_bad(n0 + row);
+        for (int e = 0; e < 4; ++e) {
+          uint32_t cx[2], cy[2];
+          e4m3x4_to_f16(xw[e], cx[0], cx[1]);
+          e4m3x4_to_f16(yw[e], cy[0], cy[1]);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            o[2 * e + f] = hfma2u(hmul2u(cx[f], r.x), w.w[0][2 * e + f], hmul2u(hmul2u(cy[f], r.y), w.w[1][2 * e + f]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xw[e], o[2 * e], o[2 * e + 1]);
+      }
+    };
+    auto load_item = [&](const uint8_t* raw, int it, int j, bool value, uint4& x, uint4& y, uint2& r) {
+      const int row = item_row(it);
+      x = *reinterpret_cast<const uint4*>(raw + item_raw(it));
+      y = x;
+      if constexpr (NSRC == 2) {
+        y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + item_raw(it));
+        r = sRatio[((j % NSR) * 2 + (value ? 1 : 0)) * NGRP + row / kQ8Block];
+      }
+      if (pos0 + j * BN + row >= S_kv) x = y = make_uint4(0, 0, 0, 0);   // behind the last key
+    };
+    auto put = [&](uint8_t* dst, int it, const uint32_t* o) {
+      *reinterpret_cast<uint4*>(dst + item_place(it)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + (item_place(it) ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    // Tile j of codes -> fp16 in the swizzled layout; then `empty` is told.
+    // Loads come a batch at a time, ahead of their use.
+    auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, auto is_value, uint64_t* empty) {
+      constexpr bool VALUE = decltype(is_value)::value;
+      constexpr int BATCH = NSRC == 1 ? 4 : 2;
+      uint32_t nan[4] = {0, 0, 0, 0};   // 0, or not a number once a value was none
+      Weights w;
+#pragma unroll
+      for (int i0 = 0; i0 < ITEMS; i0 += BATCH) {
+        uint4 x[BATCH], y[BATCH];
+        uint2 r[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          if (i0 + i < ITEMS) load_item(raw, i0 + i, j, VALUE, x[i], y[i], r[i]);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int it = i0 + i;
+          if (it >= ITEMS) continue;
+          if (it == 0 || it == PAIRED || it % KI == 0) load_weights(it, VALUE, w);
+          uint32_t o[8];
+          combine(x[i], y[i], r[i], w, o);
+          if constexpr (VALUE) {   // 0 x + nan: no code is infinite
+#pragma unroll
+            for (int e = 0; e < 8; ++e) nan[e & 3] = hfma2u(o[e], 0u, nan[e & 3]);
+          }
+          put(dst, it, o);
+        }
+      }
+      if constexpr (VALUE) {
+        if (((nan[0] | nan[1] | nan[2] | nan[3]) & 0x7fff7fffu) != 0) {
+          // values that are no numbers: noted, and zeros put in their places
+#pragma unroll 1
+          for (int it = 0; it < ITEMS; ++it) {
+            uint4 x, y;
+            uint2 r;
+            uint32_t any = 0, o[8];
+            load_item(raw, it, j, true, x, y, r);
+            uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+              any |= nan_codes(xw[e]) | nan_codes(yw[e]);
               xw[e] &= ~((nan_codes(xw[e]) >> 7) * 255u);
               yw[e] &= ~((nan_codes(yw[e]) >> 7) * 255u);
             }
+            if (!any) continue;
+            note_bad(pos0 + j * BN + item_row(it));
+            load_weights(it, true, w);
+            combine(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(yw[0], yw[1], yw[2], yw[3]), r, w, o);
+            put(dst, it, o);
           }
         }
-        if constexpr (NSRC == 2) {
-          const uint2 rr = ratio[row >> 4];
-          const uint4 wa = *reinterpret_cast<const uint4*>(w + c * 16), wb = *reinterpret_cast<const uint4*>(w + c * 16 + 8);
-          const uint4 wc = *reinterpret_cast<const uint4*>(w + D + c * 16), wd = *reinterpret_cast<const uint4*>(w + D + c * 16 + 8);
-          const uint32_t w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-          const uint32_t w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            uint32_t cx[2], cy[2];
-            e4m3x4_to_f16(xw[e >> 1], cx[0], cx[1]);
-            e4m3x4_to_f16(yw[e >> 1], cy[0], cy[1]);
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-              o[e + f] = hfma2u(hmul2u(cx[f], rr.x), w0[e + f], hmul2u(hmul2u(cy[f], rr.y), w1[e + f]));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) e4m3x4_to_f16(xw[e >> 1], o[e], o[e + 1]);
-        }
-        uint8_t* blk = dst + (size_t)(c >> 1) * BN * kSW;
-        *reinterpret_cast<uint4*>(blk + swz64(row, (c & 1) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(blk + swz64(row, (c & 1) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
+      // (only now: the arrival does not wait for loads whose values nothing has
+      // used yet, and the slot's next copy would overtake them)
+      mbar_arrive(empty);
     };
     load_scales(0);
     store_scales(0);
@@ -376,24 +480,29 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     for (int k = 0; k <= n_max; ++k) {
       const int t = k - 1;
       load_scales(k + 1);
-      bool ok = true;
-      if (k > 0) {
-        ok = wait(&rv_full[t % NR], (uint32_t)(t / NR) & 1u);
-        if (ok && t >= NS) ok = wait(&v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u);
-      }
-      if (ok && k < n_max) {
-        ok = wait(&rk_full[k % NR], (uint32_t)(k / NR) & 1u);
-        if (ok && k >= NS) ok = wait(&k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u);
-      }
+      // one thread waits (128 that spin take issue slots from the softmax);
+      // the others look once, when the phases are over
+      auto operands = [&](auto look) {
+        bool ok = true;
+        if (k > 0) {
+          ok = look(&rv_full[t % NR], (uint32_t)(t / NR) & 1u);
+          if (ok && t >= NS) ok = look(&v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u);
+        }
+        if (ok && k < n_max) {
+          ok = look(&rk_full[k % NR], (uint32_t)(k / NR) & 1u);
+          if (ok && k >= NS) ok = look(&k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u);
+        }
+        return ok;
+      };
+      const bool ok = ft != 0 || operands(wait);
       // one decision for all; and the records of this step's tiles are in place
       if (!group_and(ok)) break;
+      operands(mbar_try_wait);
       if (k > 0) {
-        convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, true);
-        mbar_arrive(&rv_empty[t % NR]);
+        convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, std::true_type{}, &rv_empty[t % NR]);
       }
       if (k < n_max) {
-        convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, false);
-        mbar_arrive(&rk_empty[k % NR]);
+        convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, std::false_type{}, &rk_empty[k % NR]);
       }
       store_scales(k + 1);
       // the tiles are read by the tensor cores (async proxy)
@@ -435,15 +544,16 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       constexpr uint32_t IDESC_QK = idesc_with_f16(idesc_bf16(BM, BN, false));
       constexpr uint32_t IDESC_PV = idesc_with_f16(idesc_bf16(BM, D, true));
       const uint32_t t_g = tmem + g * GROUP_COLS;
-      // S_g = Q_g K_j^T: A = Q_g from tensor memory (8 columns per step of 16
-      // channels), B = K_j (K-major), N = BN keys
+      const uint32_t qbase = smem_u32(sQ + g * C::Q_BYTES);
+      // S_g = Q_g K_j^T: M = 128 rows, N = BN keys, K = D in steps of 16
       auto issue_qk = [&](int j) {
         const uint32_t kbase = smem_u32(tile_k(j));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)(k & 1) * 32;
+          const uint64_t ad = sdesc(qbase + (k >> 1) * BM * kSW + off, 16, 8 * kSW);
           const uint64_t bd = sdesc(kbase + (k >> 1) * BN * kSW + off, 16, 8 * kSW);
-          mma_bf16_ts(t_g, t_g + C::Q_COL + k * 8, bd, IDESC_QK, k > 0);
+          mma_bf16(t_g, ad, bd, IDESC_QK, k > 0);
         }
       };
       // O_g += P_g V_j: A = P_g (two per column, in the first BN/2 columns of
@@ -474,6 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         tc_fence_after();
         issue_qk(0);
         mma_commit(&s_full[g]);
+        mma_commit(&k_empty[0]);
         if (g == 1) pass_turn();   // group 0's step 1 follows group 1's step 0
       }
       for (int j = 0; ok && j < ng; ++j) {
@@ -488,9 +599,8 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         pass_turn();
         if (more) issue_qk(j + 1);
         mma_commit(&s_full[g]);
-        // V_j was read by this step's PV products, K_j by the previous step's
         mma_commit(&v_empty[j % NS]);
-        mma_commit(&k_empty[j % NS]);
+        if (more) mma_commit(&k_empty[(j + 1) % NS]);
       }
       // pass group 1's extra turns once the phase before has completed (an
       // early arrival would count towards that phase)
@@ -516,41 +626,41 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     float c_row;   // what a raw score times its key scale is multiplied by
     {
       // this thread's Q row (times its key weights where one source has some)
-      // into tensor memory as D/2 packed fp16 pairs, its largest element in
-      // [2^14, 2^15); rows beyond the chunk, and the columns past D/2, are zero
+      // into shared memory as fp16, its largest element in [2^14, 2^15); rows
+      // beyond the chunk are zero
       const uint4* qrow = reinterpret_cast<const uint4*>(
           static_cast<const __nv_bfloat16*>(p.q) + (((size_t)b * H_q + g_head(g)) * p.S + m_row) * D);
       const float* wa = NSRC == 1 && p.a[0] ? p.a[0] + (size_t)kh * D : nullptr;
+      auto chunk = [&](int i, float* f) {
+        unpack16<__nv_bfloat16>(row_valid ? qrow[i] : make_uint4(0, 0, 0, 0), f);
+        if (wa) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= wa[i * 8 + e];
+        }
+      };
       float top = 0.f;
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         float f[8];
-        unpack16<__nv_bfloat16>(row_valid ? qrow[i] : make_uint4(0, 0, 0, 0), f);
+        chunk(i, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(wa ? f[e] * wa[i * 8 + e] : f[e]));
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
       }
       const int eq = top > 0.f && top < INFINITY ? 14 - exponent_of(top) : 0;
       // two factors, since 2^eq alone may lie outside the normal range
       const float f0 = power_of_two(eq / 2), f1 = power_of_two(eq - eq / 2);
       c_row = p.scale_log2 / f0 / f1;
-      for (int c = 0; c < C::Q_COLS; c += 8) {
-        float qw[8];
+      uint8_t* qg = sQ + g * C::Q_BYTES;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ch = c / 4 + i;      // 16-byte chunk of Q
-          float f[8];
-          unpack16<__nv_bfloat16>(row_valid && ch < D / 8 ? qrow[ch] : make_uint4(0, 0, 0, 0), f);
+      for (int i = 0; i < D / 8; ++i) {
+        float f[8];
+        chunk(i, f);
+        uint32_t o[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (wa && ch < D / 8) f[e] *= wa[ch * 8 + e];
-            f[e] = f[e] * f0 * f1;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qw[4 * i + e] = __uint_as_float(f16x2_of(f[2 * e], f[2 * e + 1]));
-        }
-        tmem_st8(t_s + C::Q_COL + c, qw);
+        for (int e = 0; e < 4; ++e) o[e] = f16x2_of(f[2 * e] * f0 * f1, f[2 * e + 1] * f0 * f1);
+        *reinterpret_cast<uint4*>(qg + (i >> 2) * BM * kSW + swz64(row, i & 3)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      tmem_wait_st();
-      tc_fence_before();
+      fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
     if constexpr (NSRC == 2)   // the head's power of two of the key weights
@@ -567,60 +677,82 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         break;
       }
       tc_fence_after();
-      float sv[BN];
-#pragma unroll
-      for (int c = 0; c + 32 <= BN; c += 32) tmem_ld32(t_s + c, sv + c);
-      if constexpr (BN % 32 != 0) tmem_ld16(t_s + BN / 32 * 32, sv + BN / 32 * 32);
-      tmem_wait_ld();
       // masking needed: the causal diagonal, the key extent, or (window) the
-      // lowest row-window start of the tile (warp-uniform)
-      const bool diag = n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W);
-      if (diag) {
+      // lowest row-window start of the tile (warp-uniform).  It is done where
+      // the scores lie, so that the usual tile's registers are not merged with
+      // a masked tile's (128 moves a thread).
+      if (n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W)) {
         // visible keys of this row, as tile columns: lo <= c < hi
         const int hi = min(qpos + 1, S_kv) - n0;
         const int lo = W > 0 ? qpos - W + 1 - n0 : INT_MIN;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          float x[32];
+          tmem_ld32(t_s + c, x);
+          tmem_wait_ld();
+          uint32_t y[32];
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (c >= hi || c < lo) sv[c] = -INFINITY;
+          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(c + e >= hi || c + e < lo ? -INFINITY : x[e]);
+          tmem_st32(t_s + c, y);
+        }
+        tmem_wait_st();
       }
+      float sv[BN];
+#pragma unroll
+      for (int c = 0; c + 32 <= BN; c += 32) tmem_ld32(t_s + c, sv + c);
+      // the blocks' factors, all before the scores arrive: a load between two
+      // blocks' stores of P would stop the pipeline of their exponentials
       const float4* rec = sScale + (j % NSR) * NGRP;
-      // row max of score + log2 value scale: per group of 16 keys the raw
-      // scores' (the factors are positive, so it commutes)
+      float f[NGRP], lv[NGRP], rv[NGRP];
+#pragma unroll
+      for (int gr = 0; gr < NGRP; ++gr) {
+        const float4 sc = rec[gr];
+        f[gr] = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
+        lv[gr] = sc.y;
+        rv[gr] = sc.z;
+      }
+      tmem_wait_ld();
+      // row max of score + log2 value scale: per block the raw scores' (the
+      // factors are positive, so it commutes)
       float mt_row = -INFINITY;
 #pragma unroll
       for (int gr = 0; gr < NGRP; ++gr) {
-        const float* x = sv + gr * 16;
-        const float m0 = fmax3f(fmaxf(x[0], x[1]), x[2], x[3]), m1 = fmax3f(fmaxf(x[4], x[5]), x[6], x[7]);
-        const float m2 = fmax3f(fmaxf(x[8], x[9]), x[10], x[11]), m3 = fmax3f(fmaxf(x[12], x[13]), x[14], x[15]);
-        const float4 sc = rec[gr];
-        const float f = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
-        mt_row = fmaxf(mt_row, fmaf(fmax3f(fmaxf(m0, m1), m2, m3), f, sc.y));
+        const float* x = sv + gr * 32;
+        float mx[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx[r] = fmaxf(x[2 * r], x[2 * r + 1]);
+#pragma unroll
+        for (int c = 8; c < 32; c += 8)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) mx[r] = fmax3f(mx[r], x[c + 2 * r], x[c + 2 * r + 1]);
+        mt_row = fmaxf(mt_row, fmaf(fmaxf(fmax3f(mx[0], mx[1], mx[2]), mx[3]), f[gr], lv[gr]));
       }
       // Keep a stale max until it is exceeded by more than 2^8: P' stays below
       // 2^15 and O needs no rescaling.
       const float m_new = mt_row > m_run + kSlack ? mt_row : m_run;
       const float alpha = fast_exp2(m_run - m_new);
       const float neg_m = kBias - m_new;
-      float psum = 0.f;
-      // P' over the S tile just read: BN / 2 packed columns, 8 a group
+      unsigned long long lsum = 0ull;   // (0, 0)
+      // P' over the S tile just read: BN / 2 packed columns, 16 a block
 #pragma unroll
       for (int gr = 0; gr < NGRP; ++gr) {
-        const float4 sc = rec[gr];
-        const float f = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
-        const float add = sc.y + neg_m;
-        float pk[8], ps[4] = {0.f, 0.f, 0.f, 0.f};
+        const float add = lv[gr] + neg_m;
+        const unsigned long long f2 = pair_of(f[gr], f[gr]), add2 = pair_of(add, add);
+        float pk[16];
+        unsigned long long ps[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int cc = gr * 16 + 2 * c;
-          // x = s * f + log2 r - m for two scores with one packed FMA; exp2(-inf) = 0
-          float x0 = add, x1 = add;
-          fma2(x0, x1, sv[cc], sv[cc + 1], f, f);
+        for (int c = 0; c < 16; ++c) {
+          const int cc = gr * 32 + 2 * c;
+          // s * f + log2 r - m for two scores with one packed FMA; exp2(-inf) = 0
+          float x0, x1;
+          unpair(ffma2(pair_of(sv[cc], sv[cc + 1]), f2, add2), x0, x1);
           const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-          add2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], e0, e1);
+          const unsigned long long e2 = pair_of(e0, e1);
+          ps[c & 3] = c < 4 ? e2 : fadd2(ps[c & 3], e2);
           pk[c] = __uint_as_float(f16x2_of(e0, e1));
         }
-        psum = fmaf((ps[0] + ps[1]) + (ps[2] + ps[3]), sc.z, psum);
-        tmem_st8(t_s + gr * 8, pk);
+        tmem_st16(t_s + gr * 16, pk);
+        lsum = ffma2(fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3])), pair_of(rv[gr], rv[gr]), lsum);
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha < 1.f)) {
         // O_g holds every PV product up to tile j-1 (s_full of tile j); the
@@ -635,7 +767,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
           tmem_st16(t_o + c, ov);
         }
       }
-      l_run = l_run * alpha + psum;
+      float l0, l1;
+      unpair(lsum, l0, l1);
+      l_run = l_run * alpha + (l0 + l1);
       m_run = m_new;
       tmem_wait_st();
       tc_fence_before();
