@@ -480,28 +480,26 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     for (int k = 0; k <= n_max; ++k) {
       const int t = k - 1;
       load_scales(k + 1);
-      // one thread waits (128 that spin take issue slots from the softmax);
-      // the others look once, when the phases are over
-      auto operands = [&](auto look) {
+      // One thread waits (128 that spin take issue slots from the softmax); the
+      // others look once, when the phases are over.  K's operands are awaited
+      // after V is made, so that with one slot of codes K's copy has had the
+      // time of V's conversion, and the next V's that of K's.
+      auto ready = [&](uint64_t* full, uint32_t full_parity, uint64_t* empty, uint32_t empty_parity, bool reused) {
         bool ok = true;
-        if (k > 0) {
-          ok = look(&rv_full[t % NR], (uint32_t)(t / NR) & 1u);
-          if (ok && t >= NS) ok = look(&v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u);
-        }
-        if (ok && k < n_max) {
-          ok = look(&rk_full[k % NR], (uint32_t)(k / NR) & 1u);
-          if (ok && k >= NS) ok = look(&k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u);
-        }
-        return ok;
+        if (ft == 0) ok = wait(full, full_parity) && (!reused || wait(empty, empty_parity));
+        if (!group_and(ok)) return false;   // one decision for all; and the scale records are in place
+        (void)mbar_try_wait(full, full_parity);
+        if (reused) (void)mbar_try_wait(empty, empty_parity);
+        return true;
       };
-      const bool ok = ft != 0 || operands(wait);
-      // one decision for all; and the records of this step's tiles are in place
-      if (!group_and(ok)) break;
-      operands(mbar_try_wait);
       if (k > 0) {
+        if (!ready(&rv_full[t % NR], (uint32_t)(t / NR) & 1u, &v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u, t >= NS))
+          break;
         convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, std::true_type{}, &rv_empty[t % NR]);
       }
       if (k < n_max) {
+        if (!ready(&rk_full[k % NR], (uint32_t)(k / NR) & 1u, &k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u, k >= NS))
+          break;
         convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, std::false_type{}, &rk_empty[k % NR]);
       }
       store_scales(k + 1);
@@ -670,9 +668,22 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     for (int j = 0; ok && j < ng; ++j) {
       const int n0 = pos0 + j * BN;
       // waits are made warp-uniform: tcgen05.ld/st below are warp-collective
-      // (the step's barrier, long since passed, orders the scale records)
-      if (!__all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)j & 1u) &&
-                                       wait(&step_ready[j % NSR], (uint32_t)(j / NSR) & 1u))) {
+      if (!__all_sync(0xffffffffu, wait(&step_ready[j % NSR], (uint32_t)(j / NSR) & 1u))) {
+        ok = false;
+        break;
+      }
+      // the blocks' factors, before the scores are there: a load between two
+      // blocks' stores of P would stop the pipeline of their exponentials
+      const float4* rec = sScale + (j % NSR) * NGRP;
+      float f[NGRP], lv[NGRP], rv[NGRP];
+#pragma unroll
+      for (int gr = 0; gr < NGRP; ++gr) {
+        const float4 sc = rec[gr];
+        f[gr] = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
+        lv[gr] = sc.y;
+        rv[gr] = sc.z;
+      }
+      if (!__all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)j & 1u))) {
         ok = false;
         break;
       }
@@ -700,17 +711,6 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       float sv[BN];
 #pragma unroll
       for (int c = 0; c + 32 <= BN; c += 32) tmem_ld32(t_s + c, sv + c);
-      // the blocks' factors, all before the scores arrive: a load between two
-      // blocks' stores of P would stop the pipeline of their exponentials
-      const float4* rec = sScale + (j % NSR) * NGRP;
-      float f[NGRP], lv[NGRP], rv[NGRP];
-#pragma unroll
-      for (int gr = 0; gr < NGRP; ++gr) {
-        const float4 sc = rec[gr];
-        f[gr] = fminf(fmaxf(c_row * sc.x, FLT_MIN), FLT_MAX);
-        lv[gr] = sc.y;
-        rv[gr] = sc.z;
-      }
       tmem_wait_ld();
       // row max of score + log2 value scale: per block the raw scores' (the
       // factors are positive, so it commutes)
