@@ -271,6 +271,9 @@ bool any_q8(const fkv_ctx* c) {
   return false;
 }
 
+// Whether a grid can have a column for K and for V of every (sequence, KV head).
+bool planes_fit_grid(const fkv_ctx* c) { return 2LL * c->cfg.batch * c->cfg.num_kv_heads < (1LL << 31); }
+
 // Whether the context's device is the calling thread's current one.
 bool on_device(const fkv_ctx* c) {
   int dev = -1;
@@ -471,6 +474,7 @@ fkv_status fkv_append_kv(fkv_ctx* c, int layer, const void* k_new, const void* v
   if (c->ring[layer] > 0 && T > c->ring[layer]) return FKV_ERR_INVALID_ARG;
   if (!c->k[layer] || !c->v[layer]) return FKV_ERR_INVALID_ARG;
   const int format = c->format[layer];
+  if (format == fkv::kCacheQ8 && !planes_fit_grid(c)) return FKV_ERR_UNSUPPORTED;
   if (format == fkv::kCacheQ8 && c->ring[layer] > 0) {
     if (c->ring[layer] % fkv::kQ8Block != 0) return FKV_ERR_UNSUPPORTED;
     // the rows may not come round to the block that they start in
@@ -512,6 +516,7 @@ fkv_status fkv_read_kv(fkv_ctx* c, int layer, int mode, const int32_t* pos, int 
       resolve_sources(c, layer, mode, r.k, r.v, r.a, r.b, &r.nsrc, &r.format, &r.ring, src);
   if (s != FKV_OK) return s;
   if (T < 0 || T > (r.ring > 0 ? r.ring : c->cfg.max_seq)) return FKV_ERR_INVALID_ARG;
+  if (!planes_fit_grid(c)) return FKV_ERR_UNSUPPORTED;
   if (T == 0) return FKV_OK;
   if (!pos || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) ||
       (reinterpret_cast<uintptr_t>(pos) & 3u))

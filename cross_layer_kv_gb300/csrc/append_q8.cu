@@ -9,28 +9,35 @@
 // rows before the new ones store e4m3(code * s_old / s).  Rows of the block
 // behind the new ones are free.
 //
-// One warp per block; a lane holds up to D/16 runs of 16 channels in
-// registers between the maximum and the codes, so the new rows are read once,
-// in 32 (bf16) or 64 (fp32) contiguous bytes a lane, and the codes are written
-// 16 bytes a lane.  A block belongs to one warp (the host refuses calls whose
-// rows would come round to their first block of a ring), so nothing is atomic.
+// One warp per block; a lane holds up to D/8 runs of 8 channels in registers
+// between the maximum and the codes, so the new rows are read once; a load of
+// the warp is 512 contiguous bytes (bf16) and a store of codes 256.  A block
+// belongs to one warp (the host refuses calls whose rows would come round to
+// their first block of a ring), so nothing is atomic.  Bound: HBM, 3 bytes an
+// element (bf16) for prompts, latency for single tokens.
+#include <type_traits>
+
 #include "fkv_kernels.h"
 #include "q8_device.cuh"
 
 namespace fkv {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;   // of a CTA, at most
 
-// 16 elements of the context's type -> fp32.
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, float* f) {
-  unpack16<__nv_bfloat16>(reinterpret_cast<const uint4*>(src)[0], f);
-  unpack16<__nv_bfloat16>(reinterpret_cast<const uint4*>(src)[1], f + 8);
-}
-__device__ __forceinline__ void load16(const float* src, float* f) {
+// 8 elements of the context's type, as they are, and their bits as fp32.
+template <typename T>
+struct Run8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack16<float>(reinterpret_cast<const uint4*>(src)[i], f + 4 * i);
-}
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+  }
+  __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) unpack16<T>(v[i], f + i * (16 / (int)sizeof(T)));
+  }
+};
 
 // The smallest power of two whose 448-fold (1.75 * 2^8) reaches amax.
 __device__ __forceinline__ float scale_for(float amax) {
@@ -42,24 +49,21 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, int blocks) {
-  constexpr int PER = D / 16;   // runs of 16 channels per row, and per lane and block
+  constexpr int PER = D / 8;   // runs of 8 channels per row, and per lane and block
   static_assert(kQ8Block == 32, "a lane's runs of a block are one row's");
   grid_dep_trigger();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const long long units = (long long)a.batch * a.kv_heads;
-  const long long total = 2 * units * blocks;
-  for (long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); w < total;
-       w += (long long)gridDim.x * kWarps) {
-    const int i = (int)(w % blocks);           // block of the call
-    const long long u2 = w / blocks;
-    const bool value = u2 >= units;
-    const long long u = value ? u2 - units : u2;
-    const int b = (int)(u / a.kv_heads);
+  const int units = a.batch * a.kv_heads;
+  const int warps = (int)blockDim.x >> 5;
+  for (int i = (int)blockIdx.y * warps + (threadIdx.x >> 5); i < blocks; i += (int)gridDim.y * warps) {   // block of the call
+    const bool value = (int)blockIdx.x >= units;
+    const int u = (int)blockIdx.x - (value ? units : 0);
+    const int b = u / a.kv_heads;
     const int p = a.pos[b];
     if (p < 0 || (long long)p + a.T > a.max_seq) {
       if (lane == 0 && i == 0 && !value && u % a.kv_heads == 0) flag_status(a.status, kDevBadArg);
-      continue;
+      return;
     }
     // rows [r0, r1) of block g are new; the first of them is row t0 of the call
     const int g = p / kQ8Block + i;
@@ -77,16 +81,19 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, in
     const int runs = (r1 - r0) * PER;
 
     const float s_old = r0 > 0 ? *sp : 0.f;
-    float x[PER][16];
+    Run8<T> x[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (lane + 32 * k < runs) x[k].load(src + (size_t)(lane + 32 * k) * 8);
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int c = lane + 32 * k;
-      if (c < runs) {
-        load16(src + (size_t)c * 16, x[k]);
+      if (lane + 32 * k < runs) {
+        float f[8];
+        x[k].values(f);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t m = __float_as_uint(x[k][e]) & 0x7fffffffu;
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t m = __float_as_uint(f[e]) & 0x7fffffffu;
           if (m < 0x7f800000u) top = m > top ? m : top;
         }
       }
@@ -97,29 +104,36 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, in
     const float s = had && s_old > need ? s_old : need;
     // dividing by a power of two is multiplying by its reciprocal
     const bool power = (__float_as_uint(s) & 0x7fffffu) == 0 && s > 0x1p-120f && s < 0x1p+120f;
-    const float inv = power ? 1.f / s : 0.f;
+    auto encode = [&](auto divide) {
+      const float inv = 1.f / s;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int c = lane + 32 * k;
-      if (c < runs) {
-        uint32_t o[4];
+      for (int k = 0; k < PER; ++k) {
+        const int c = lane + 32 * k;
+        if (c < runs) {
+          float f[8];
+          x[k].values(f);
+          uint32_t o[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const float v = x[k][4 * e + f];
-            y[f] = power ? v * inv : __fdiv_rn(v, s);
-            if ((__float_as_uint(v) & 0x7fffffffu) >= 0x7f800000u) y[f] = __uint_as_float(0x7fffffffu);
+          for (int e = 0; e < 8; ++e) {
+            const bool finite = (__float_as_uint(f[e]) & 0x7fffffffu) < 0x7f800000u;
+            if constexpr (decltype(divide)::value) f[e] = __fdiv_rn(f[e], s);
+            else f[e] *= inv;
+            if (!finite) f[e] = __uint_as_float(0x7fffffffu);
           }
-          o[e] = e4m3x2_of(y[0], y[1]) | (e4m3x2_of(y[2], y[3]) << 16);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            o[e] = e4m3x2_of(f[4 * e], f[4 * e + 1]) | (e4m3x2_of(f[4 * e + 2], f[4 * e + 3]) << 16);
+          *reinterpret_cast<uint2*>(codes + (size_t)r0 * D + c * 8) = make_uint2(o[0], o[1]);
         }
-        *reinterpret_cast<uint4*>(codes + (size_t)r0 * D + c * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-    }
+    };
+    if (power)
+      encode(std::false_type{});
+    else
+      encode(std::true_type{});
     if (had && s != s_old) {
       const float ratio = __fdiv_rn(s_old, s);
-      for (int c = lane; c < r0 * PER; c += 32) {
+      for (int c = lane; c < r0 * (D / 16); c += 32) {
         uint4* pc = reinterpret_cast<uint4*>(codes + c * 16);
         const uint4 q = *pc;
         const uint32_t in[4] = {q.x, q.y, q.z, q.w};
@@ -141,10 +155,9 @@ template <typename T>
 cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
   // blocks that T rows can touch, wherever they start
   const int blocks = (a.T + kQ8Block - 2) / kQ8Block + 1;
-  const long long total = 2LL * a.batch * a.kv_heads * blocks;
-  long long ctas = (total + kWarps - 1) / kWarps;
-  if (ctas > 65535LL * 8) ctas = 65535LL * 8;
-  const dim3 grid((unsigned)ctas), block(kWarps * 32);
+  const int warps = blocks < kWarps ? blocks : kWarps;
+  const int rows = (blocks + warps - 1) / warps;   // of the grid: a unit's K or V is a column
+  const dim3 grid((unsigned)(2LL * a.batch * a.kv_heads), (unsigned)(rows < 65535 ? rows : 65535)), block(warps * 32);
   switch (a.head_dim) {
     case 64: return launch_pdl(append_q8_kernel<T, 64>, grid, block, 0, stream, a, blocks);
     case 80: return launch_pdl(append_q8_kernel<T, 80>, grid, block, 0, stream, a, blocks);

@@ -476,36 +476,42 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     };
     load_scales(0);
     store_scales(0);
+    (void)group_and(true);
     // step 0 makes K_0; step k > 0 makes V_{k-1}, then K_k (k < n_max)
     for (int k = 0; k <= n_max; ++k) {
       const int t = k - 1;
       load_scales(k + 1);
-      // One thread waits (128 that spin take issue slots from the softmax); the
-      // others look once, when the phases are over.  K's operands are awaited
-      // after V is made, so that with one slot of codes K's copy has had the
-      // time of V's conversion, and the next V's that of K's.
+      // Each warp waits for itself: one look where the phases are over, else
+      // one lane waits (32 that spin take issue slots from the softmax).  K's
+      // operands are awaited after V is made, so that with one slot of codes
+      // K's copy has had the time of V's conversion, and the next V's that of
+      // K's.
       auto ready = [&](uint64_t* full, uint32_t full_parity, uint64_t* empty, uint32_t empty_parity, bool reused) {
+        auto look = [&]() { return mbar_try_wait(full, full_parity) && (!reused || mbar_try_wait(empty, empty_parity)); };
+        if (__all_sync(0xffffffffu, look())) return true;
         bool ok = true;
-        if (ft == 0) ok = wait(full, full_parity) && (!reused || wait(empty, empty_parity));
-        if (!group_and(ok)) return false;   // one decision for all; and the scale records are in place
-        (void)mbar_try_wait(full, full_parity);
-        if (reused) (void)mbar_try_wait(empty, empty_parity);
-        return true;
+        if (lane == 0) ok = wait(full, full_parity) && (!reused || wait(empty, empty_parity));
+        return __all_sync(0xffffffffu, ok) && __all_sync(0xffffffffu, look());
       };
+      bool ok = true;
       if (k > 0) {
-        if (!ready(&rv_full[t % NR], (uint32_t)(t / NR) & 1u, &v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u, t >= NS))
-          break;
-        convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, std::true_type{}, &rv_empty[t % NR]);
+        ok = ready(&rv_full[t % NR], (uint32_t)(t / NR) & 1u, &v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u, t >= NS);
+        if (ok)
+          convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, std::true_type{}, &rv_empty[t % NR]);
       }
-      if (k < n_max) {
-        if (!ready(&rk_full[k % NR], (uint32_t)(k / NR) & 1u, &k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u, k >= NS))
-          break;
-        convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, std::false_type{}, &rk_empty[k % NR]);
+      if (ok && k < n_max) {
+        ok = ready(&rk_full[k % NR], (uint32_t)(k / NR) & 1u, &k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u, k >= NS);
+        if (ok)
+          convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, std::false_type{}, &rk_empty[k % NR]);
       }
-      store_scales(k + 1);
-      // the tiles are read by the tensor cores (async proxy)
-      fence_proxy_async_smem();
-      mbar_arrive(&step_ready[k % NSR]);
+      if (ok) {
+        store_scales(k + 1);
+        // the tiles are read by the tensor cores (async proxy)
+        fence_proxy_async_smem();
+        mbar_arrive(&step_ready[k % NSR]);
+      }
+      // one decision for all; and the next step's scale records are in place
+      if (!group_and(ok)) break;
     }
   } else if (warp >= C::SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
