@@ -547,7 +547,7 @@ size_t fkv_decode_workspace_bytes(const fkv_ctx* c) {
       best = p.workspace_bytes;
     if (fkv::decode_q4_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
       best = p.workspace_bytes;
-    if (fkv::decode_q8_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
+    if (any_q8(c) && fkv::decode_q8_plan(d, c->num_sms, &p) == cudaSuccess && p.workspace_bytes > best)
       best = p.workspace_bytes;
   }
   return best;

@@ -39,7 +39,7 @@ cudaError_t decode_q8_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan) {
   const size_t units = (size_t)a.batch * a.kv_heads;
   const size_t slots = (size_t)ctas + units;   // a CTA's partial of unit u: slot CTA + u
   plan->partial_bytes = (slots * a.group * partial_stride(a.head_dim) * sizeof(float) + 15) / 16 * 16;
-  plan->workspace_bytes = plan->partial_bytes + units * sizeof(unsigned long long);
+  plan->workspace_bytes = plan->partial_bytes + units * a.group * sizeof(unsigned long long);
   return cudaSuccess;
 }
 

@@ -5,7 +5,8 @@
 // its own (cp.async.bulk, one mbarrier a stage), as in decode_split_kernel.
 // Ranges are cut at groups of 16 rows, counted from rows that are multiples of
 // 16, so that a group has one key scale and one value scale; they come with
-// the codes, in 16-byte pieces.
+// the codes, a lane holding one of the next tile's, since small bulk copies cost
+// the copy engine as much as large ones.
 //
 // A (sequence, KV head) unit that lies in one warp's range is finished by that
 // warp.  Of the others a warp holds at most two, at its range's ends; these
@@ -75,12 +76,20 @@ struct Q8Cfg {
   using S = Q8Shape<D, NSRC>;
   static constexpr int TR = 16 * S::GROUPS;            // rows per tile
   static constexpr int TILE_BYTES = TR * D;            // codes of one plane's tile
-  // scales of one plane's tile in whole 16-byte pieces (4 blocks each); a tile
-  // that wraps in a ring has two such runs
-  static constexpr int SCW = ((TR - 1) / (4 * kQ8Block) + 2) * 4;
   static constexpr int CODE_BYTES = 2 * NSRC * TILE_BYTES;
-  static constexpr int STAGE_BYTES = CODE_BYTES + 2 * NSRC * 2 * SCW * 4;
-  static_assert(TILE_BYTES % 16 == 0 && STAGE_BYTES % 16 == 0, "stages are read in 16-byte pieces");
+  static constexpr int STAGE_BYTES = CODE_BYTES + 128;   // and a scale for every plane and group
+  static_assert(TILE_BYTES % 16 == 0, "stages are read in 16-byte pieces");
+  static_assert(2 * NSRC * S::GROUPS <= 32, "a lane copies one of a tile's scales");
+};
+
+// Division by a number known at launch: floor(x / d) of 32-bit x.
+struct Q8Div {
+  unsigned long long m;   // ceil(2^64 / d); 0: d = 1
+  unsigned d;
+  static Q8Div of(unsigned d) { return {d > 1 ? ~0ull / d + 1 : 0, d}; }
+  __device__ __forceinline__ unsigned operator()(unsigned x) const {
+    return m ? (unsigned)__umul64hi(m, x) : x;
+  }
 };
 
 struct Q8Params {
@@ -89,7 +98,17 @@ struct Q8Params {
   const float* vs[2];
   int G;
   int aux_bytes;
+  Q8Div by_ctas, by_heads;
 };
+
+// Copy 4 bytes to shared memory without waiting; and arrive on a barrier once
+// this lane's copies so far have landed.
+__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // d += a b: m16n8k16, fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -136,6 +155,30 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t* w) {
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(src)[i];
+  }
+}
+
+// N elements of global memory, aligned to the largest power of two that
+// divides their bytes (16 at most), -> fp32.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* src, float* f) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) unpack16<float>(reinterpret_cast<const uint4*>(src)[i], f + 4 * i);
+}
+template <int N>
+__device__ __forceinline__ void load_floats(const __nv_bfloat16* src, float* f) {
+  if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) unpack16<__nv_bfloat16>(reinterpret_cast<const uint4*>(src)[i], f + 8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint2 w = reinterpret_cast<const uint2*>(src)[i];
+      f[4 * i] = bf16lo(w.x);
+      f[4 * i + 1] = bf16hi(w.x);
+      f[4 * i + 2] = bf16lo(w.y);
+      f[4 * i + 3] = bf16hi(w.y);
+    }
   }
 }
 
@@ -198,179 +241,231 @@ __device__ __forceinline__ unsigned q8_arrive(unsigned long long* word, unsigned
   return 0;
 }
 
-// A warp's running combination of partials of G heads, lane = channel.
-template <int D, int G>
+// Equal shares: part c of n has [start(c), start(c + 1)), start(c) = floor(c
+// total / n), in 32-bit arithmetic (total < 2^32, n < 2^16).
+struct Q8Split {
+  Q8Div by;
+  unsigned each, rest;
+  __device__ __forceinline__ Q8Split(unsigned total, const Q8Div& parts) : by(parts) {
+    each = by(total);
+    rest = total - each * by.d;
+  }
+  __device__ __forceinline__ unsigned start(unsigned c) const { return c * each + by(c * rest); }
+  // the part that holds group g
+  __device__ __forceinline__ unsigned part(unsigned g, unsigned total) const {
+    unsigned c = min((unsigned)__fdividef((float)g * (float)by.d, (float)total), by.d - 1);
+    while (c > 0 && start(c) > g) --c;
+    while (c + 1 < by.d && start(c + 1) <= g) ++c;
+    return c;
+  }
+};
+
+// A warp's combination of partials of one head (records o[D], m, l), lane =
+// channel of o.
+template <int D>
 struct Q8Acc {
   static constexpr int DPL = (D + 31) / 32;
-  float M[G], L[G], o[G][DPL];
+  float M, L, o[DPL];
   __device__ __forceinline__ void clear() {
+    M = -FLT_MAX;
+    L = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      M[g] = -FLT_MAX;
-      L[g] = 0.f;
+    for (int k = 0; k < DPL; ++k) o[k] = 0.f;
+  }
+  // Add up to 32 records, rec(j) for the bits j of `members`: lane j takes
+  // record j's m and l, so that the weights come in one step.  GLOBAL: read
+  // through L2, where other SMs put them, several rows at a time.
+  template <bool GLOBAL, typename Rec>
+  __device__ __forceinline__ void add(unsigned members, Rec rec, int lane) {
+    auto get = [](const float* p) { return GLOBAL ? __ldcg(p) : *p; };
+    float m = -FLT_MAX, l = 0.f;
+    if ((members >> lane) & 1u) {
+      const float* r = rec(lane);
+      m = get(r + D);
+      l = get(r + D + 1);
+    }
+    const float top = fmaxf(M, warp_max(m)), old = fast_exp2(M - top);
+    const float w = (members >> lane) & 1u ? fast_exp2(m - top) : 0.f;
+    L = L * old + warp_sum(w * l);
+    M = top;
 #pragma unroll
-      for (int k = 0; k < DPL; ++k) o[g][k] = 0.f;
+    for (int k = 0; k < DPL; ++k) o[k] *= old;
+    constexpr int AT = GLOBAL ? 4 : 2;
+    while (members) {
+      float wj[AT], x[AT][DPL];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const int j = members ? __ffs((int)members) - 1 : 0;
+        wj[i] = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) x[i][k] = 0.f;
+        if (members) {
+          const float* r = rec(j);
+#pragma unroll
+          for (int k = 0; k < DPL; ++k)
+            if (lane + 32 * k < D) x[i][k] = get(r + lane + 32 * k);
+        }
+        members &= members - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) o[k] = fmaf(wj[i], x[i][k], o[k]);
     }
   }
-  // add a record (o[D], m, l per head); GLOBAL: read through L2, where other
-  // SMs put it
-  template <bool GLOBAL>
-  __device__ __forceinline__ void add(const float* rec, int lane) {
+  __device__ __forceinline__ void store(float* r, int lane) const {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float* r = rec + g * partial_stride(D);
-      const float m = GLOBAL ? __ldcg(r + D) : r[D], l = GLOBAL ? __ldcg(r + D + 1) : r[D + 1];
-      const float top = fmaxf(M[g], m);
-      const float a = exp2f(M[g] - top), b = exp2f(m - top);
-      L[g] = L[g] * a + l * b;
-#pragma unroll
-      for (int k = 0; k < DPL; ++k) {
-        const int d = lane + 32 * k;
-        const float x = d < D ? (GLOBAL ? __ldcg(r + d) : r[d]) : 0.f;
-        o[g][k] = o[g][k] * a + x * b;
-      }
-      M[g] = top;
-    }
-  }
-  __device__ __forceinline__ void store(float* rec, int lane) const {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float* r = rec + g * partial_stride(D);
-#pragma unroll
-      for (int k = 0; k < DPL; ++k)
-        if (lane + 32 * k < D) r[lane + 32 * k] = o[g][k];
-      if (lane == 0) {
-        r[D] = M[g];
-        r[D + 1] = L[g];
-      }
+    for (int k = 0; k < DPL; ++k)
+      if (lane + 32 * k < D) r[lane + 32 * k] = o[k];
+    if (lane == 0) {
+      r[D] = M;
+      r[D + 1] = L;
     }
   }
   template <typename T>
-  __device__ __forceinline__ void finish(T* out, int lane) const {   // out: the unit's G rows
+  __device__ __forceinline__ void finish(T* out, int lane) const {
+    const float inv = 1.f / L;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float inv = 1.f / L[g];
-#pragma unroll
-      for (int k = 0; k < DPL; ++k)
-        if (lane + 32 * k < D) out[g * D + lane + 32 * k] = T(o[g][k] * inv);
-    }
+    for (int k = 0; k < DPL; ++k)
+      if (lane + 32 * k < D) out[lane + 32 * k] = T(o[k] * inv);
   }
 };
 
-constexpr int kQ8FewPartials = 6;   // merged by one warp
+constexpr int kQ8FewPartials = 8;   // merged by one warp
+constexpr int kQ8Stopped = -2;      // Q8Shared::head of a warp that gave up
 
 // What the warps of a CTA left: partials of units that cross warps (`head`:
 // record of the unit that a warp's range starts inside, `tail`: of the one
-// that it ends inside; unit numbers, -1: none), and the units that this CTA
-// is the last to reach, for all its warps to merge.
+// that it ends inside; unit numbers, -1: none), and the heads (unit * G + head)
+// that this CTA is the last to reach, for all its warps to merge.
 struct Q8Shared {
   int* head;
   int* tail;
-  int* merge;          // [2] units
+  int* merge;          // [2][4], -1: none
   float* head_rec;     // [W][G] records
   uint8_t* ring;       // tails: at the start of each warp's ring
-  size_t ring_bytes;   // of a warp
+  unsigned ring_bytes; // of a warp
 };
 
-template <typename T, int D, int G>
-__device__ __noinline__ void q8_tail(const SplitParams& p, const Q8Shared sh, int W, long long total,
-                                     const int* lens, const int* pre) {
+// [c0, c1): the CTA's groups; `split`: all CTAs' (not looked at where no unit
+// crosses CTAs).  A warp takes a chain of partials and a head at a time.
+template <typename T, int D, int W>
+__device__ __forceinline__ void q8_tail(const SplitParams& p, const Q8Shared& sh, int G, unsigned total,
+                                        const Q8Split& split, unsigned c0, unsigned c1, const int* lens,
+                                        const int* pre) {
   constexpr int PS = partial_stride(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H = p.H_kv;
-  const long long grid = gridDim.x;
-  const long long c0 = blockIdx.x * total / grid, c1 = (blockIdx.x + 1) * total / grid;   // the CTA's groups
-  auto head_rec = [&](int w) { return sh.head_rec + (size_t)w * G * PS; };
-  auto tail_rec = [&](int w) { return reinterpret_cast<const float*>(sh.ring + (size_t)w * sh.ring_bytes); };
-
-  // a unit's groups [su, eu)
-  auto unit_range = [&](int u, long long& su, long long& eu) {
+  T* out = static_cast<T*>(p.out);
+  const int my_head = lane < W ? sh.head[lane] : -1, my_tail = lane < W ? sh.tail[lane] : -1;
+  // Chains: a tail with the heads that go on with its unit; and, of the unit
+  // that the CTA starts inside, the first head and the others of it.
+  const unsigned tails = __ballot_sync(0xffffffffu, my_tail >= 0);
+  const unsigned heads = __ballot_sync(0xffffffffu, my_head >= 0);
+  const int k0 = heads ? __ffs((int)heads) - 1 : 0;
+  const int u0 = __shfl_sync(0xffffffffu, my_head, k0);
+  const bool starts_inside = heads && !__any_sync(0xffffffffu, my_tail == u0);
+  const int chains = __popc(tails) + (starts_inside ? 1 : 0);
+  auto unit_range = [&](int u, unsigned& su, unsigned& eu) {   // its groups
     const int b = u / H, h = u - b * H;
-    su = (long long)H * pre[b] + (long long)h * lens[b];
+    su = (unsigned)H * pre[b] + (unsigned)h * lens[b];
     eu = su + lens[b];
   };
-  // chain of unit u from warp `w` on (from its tail, or its head)
-  auto chain = [&](int u, int w, bool from_tail) {
-    Q8Acc<D, G> acc;
+  for (int task = warp; task < chains * G; task += W) {
+    const int c = task / G, g = task - c * G;
+    unsigned left = tails;
+    for (int i = starts_inside ? 1 : 0; i < c; ++i) left &= left - 1;
+    const bool from_tail = !starts_inside || c > 0;
+    const int leader = from_tail ? __ffs((int)left) - 1 : -1;
+    const int u = from_tail ? __shfl_sync(0xffffffffu, my_tail, leader) : u0;
+    // (a warp that a unit goes through has no tail of it: a record a warp)
+    const unsigned members = __ballot_sync(0xffffffffu, my_head == u) | (from_tail ? 1u << leader : 0u);
+    Q8Acc<D> acc;
     acc.clear();
-    if (from_tail) acc.template add<false>(tail_rec(w), lane);
-    for (int k = from_tail ? w + 1 : w; k < W; ++k)
-      if (sh.head[k] == u) acc.template add<false>(head_rec(k), lane);
-    long long su, eu;
+    acc.template add<false>(
+        members,
+        [&](int j) {
+          const float* r = j == leader ? reinterpret_cast<const float*>(sh.ring + j * sh.ring_bytes)
+                                       : sh.head_rec + j * G * PS;
+          return r + g * PS;
+        },
+        lane);
+    unsigned su, eu;
     unit_range(u, su, eu);
-    T* out = static_cast<T*>(p.out) + (size_t)u * G * D;
     if (su >= c0 && eu <= c1) {
-      acc.finish(out, lane);
-      return;
+      acc.finish(out + ((size_t)u * G + g) * D, lane);
+      continue;
     }
-    acc.store(p.ws + ((size_t)blockIdx.x + u) * G * PS, lane);
-    const long long cf = ((su + 1) * grid - 1) / total, cl = (eu * grid - 1) / total;
+    acc.store(p.ws + (((size_t)blockIdx.x + u) * G + g) * PS, lane);
+    const unsigned cf = split.part(su, total), cl = split.part(eu - 1, total);
     int need = (int)(cl - cf + 1);
-    if (total < grid) {   // some CTAs have no groups
+    if (total < split.by.d) {   // some CTAs have no groups
       need = 0;
-      for (long long k = cf; k <= cl; k += 32) {
-        const long long c = k + lane;
-        need += __popc(__ballot_sync(0xffffffffu, c <= cl && c * total / grid < (c + 1) * total / grid));
+      for (unsigned k = cf; k <= cl; k += 32) {
+        const unsigned i = k + lane;
+        need += __popc(__ballot_sync(0xffffffffu, i <= cl && split.start(i) < split.start(i + 1)));
       }
     }
     __threadfence();
     __syncwarp();
     unsigned arrived = 0;
-    if (lane == 0) arrived = q8_arrive(p.counters + u, p.epoch);
+    if (lane == 0) arrived = q8_arrive(p.counters + (size_t)u * G + g, p.epoch);
     arrived = __shfl_sync(0xffffffffu, arrived, 0);
     if (arrived == 0) flag_status(p.status, lane == 0 ? kDevTimeout : 0);
-    if (arrived != (unsigned)need) return;
+    if (arrived != (unsigned)need) continue;
     // No arrival of this call can follow: clear the word, so that a call with
     // the same epoch (a CUDA graph replaying this launch) starts at 1.
-    if (lane == 0) p.counters[u] = 0ull;
+    if (lane == 0) p.counters[(size_t)u * G + g] = 0ull;
     __threadfence();
     if (cl - cf + 1 <= kQ8FewPartials) {
-      const int b = u / H;
-      merge_unit<T, D, G, kQ8FewPartials>(p.ws, static_cast<T*>(p.out), u, cf, cl, grid, total, b,
-                                          u - b * H, H, lane);
+      const bool has = cf + lane <= cl && split.start(cf + lane) < split.start(cf + lane + 1);
+      acc.clear();
+      acc.template add<true>(
+          __ballot_sync(0xffffffffu, has),
+          [&](int j) { return p.ws + (((size_t)cf + j + u) * G + g) * PS; }, lane);
+      acc.finish(out + ((size_t)u * G + g) * D, lane);
     } else if (lane == 0) {
-      sh.merge[from_tail ? 1 : 0] = u;
+      sh.merge[(from_tail ? 4 : 0) + g] = u;
     }
-  };
-  // the unit that the CTA starts inside belongs to its first warp with rows,
-  // and the others to the warps that end inside them
-  if (sh.head[warp] >= 0) {
-    bool leads = true;
-    for (int k = 0; k < warp; ++k)
-      if (sh.head[k] == sh.head[warp] || sh.tail[k] == sh.head[warp]) leads = false;
-    if (leads) chain(sh.head[warp], warp, false);
   }
-  if (sh.tail[warp] >= 0) chain(sh.tail[warp], warp, true);
   __syncthreads();
-  for (int i = 0; i < 2; ++i) {
-    const int u = sh.merge[i];
+  for (int i = 0; i < 8; ++i) {
+    const int u = sh.merge[i], g = i & 3;
     if (u < 0) continue;
-    // all warps: each some of the unit's partials, then the first one theirs
-    long long su, eu;
+    // all warps: each some of the head's partials, then the first one theirs
+    unsigned su, eu;
     unit_range(u, su, eu);
-    const long long cf = ((su + 1) * grid - 1) / total, cl = (eu * grid - 1) / total;
-    Q8Acc<D, G> acc;
+    const unsigned cf = split.part(su, total), cl = split.part(eu - 1, total);
+    Q8Acc<D> acc;
     acc.clear();
-    for (long long c = cf + warp; c <= cl; c += W)
-      if (c * total / grid < (c + 1) * total / grid)
-        acc.template add<true>(p.ws + ((size_t)c + u) * G * PS, lane);
-    acc.store(head_rec(warp), lane);
+    for (unsigned base = cf; base <= cl; base += 32 * W) {
+      const unsigned k = base + lane * W + warp;   // lane j's partial
+      acc.template add<true>(
+          __ballot_sync(0xffffffffu, k <= cl && split.start(k) < split.start(k + 1)),
+          [&](int j) { return p.ws + (((size_t)base + j * W + warp + u) * G + g) * PS; }, lane);
+    }
+    acc.store(sh.head_rec + warp * PS, lane);
     __syncthreads();
     if (warp == 0) {
       acc.clear();
-      for (int k = 0; k < W; ++k) acc.template add<false>(head_rec(k), lane);
-      acc.finish(static_cast<T*>(p.out) + (size_t)u * G * D, lane);
+      acc.template add<false>((1u << W) - 1u, [&](int j) { return sh.head_rec + j * PS; }, lane);
+      acc.finish(out + ((size_t)u * G + g) * D, lane);
     }
     __syncthreads();
   }
 }
+
+// Sequences of up to this many groups of 16 rows are short: a CTA takes whole
+// units then, since a merge through global memory (3 us) costs more than an
+// uneven split.
+constexpr int kQ8ShortGroups = 48;
 
 template <typename T, int D, int NSRC>
 __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(const Q8Params prm) {
   const SplitParams& p = prm.p;
   using Cfg = Q8Cfg<D, NSRC>;
   using S = typename Cfg::S;
-  constexpr int GROUPS = S::GROUPS, SCW = Cfg::SCW;
+  constexpr int GROUPS = S::GROUPS;
   constexpr int TILE = Cfg::TILE_BYTES, STAGE = Cfg::STAGE_BYTES;
   constexpr int NS = S::NS, W = S::W;
   constexpr int PS = partial_stride(D);
@@ -389,53 +484,56 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   sh.head = count + p.B;
   sh.tail = sh.head + W;
   sh.merge = sh.tail + W;
-  int* abort_flag = sh.merge + 2;
   sh.head_rec = reinterpret_cast<float*>(smem + (size_t)W * NS * STAGE + prm.aux_bytes);
   sh.ring = smem;
-  sh.ring_bytes = (size_t)NS * STAGE;
+  sh.ring_bytes = NS * STAGE;
 
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) mbar_init(&bars[warp * NS + s], 1);
+    for (int s = 0; s < NS; ++s) mbar_init(&bars[warp * NS + s], 33);   // a copy's bytes, and the lanes
     fence_mbar_init();
     sh.head[warp] = sh.tail[warp] = -1;
   }
-  if (threadIdx.x == 0) sh.merge[0] = sh.merge[1] = -1, *abort_flag = 0;
+  if (threadIdx.x < 8) sh.merge[threadIdx.x] = -1;
   grid_dep_trigger();
   grid_dep_wait();
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
 
-  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-    int L = p.seq_lens[i];
-    if (L < 1 || L > p.S_max) {
-      if (blockIdx.x == 0) flag_status(p.status, kDevBadArg);
-      L = L < 0 ? 0 : (L > p.S_max ? p.S_max : L);
-    }
-    const int Le = p.window > 0 && L > p.window ? p.window : L;
-    const int f = p.ring > 0 ? (L - Le) % p.ring : L - Le;   // (in a ring: its row)
-    first[i] = f;
-    count[i] = Le;
-    lens[i] = Le > 0 ? (f % 16 + Le + 15) / 16 : 0;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int run = 0;
-    for (int base = 0; base < p.B; base += 32) {
-      const int x = base + lane < p.B ? lens[base + lane] : 0;
-      int incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+  // Lengths and their sums, by every warp for itself (all write the same
+  // values): no warp waits for another.
+  int run = 0, longest = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int i = base + lane;
+    int f = 0, Le = 0, x = 0;
+    if (i < p.B) {
+      int L = p.seq_lens[i];
+      if (L < 1 || L > p.S_max) {
+        if (blockIdx.x == 0 && warp == 0) flag_status(p.status, kDevBadArg);
+        L = L < 0 ? 0 : (L > p.S_max ? p.S_max : L);
       }
-      if (base + lane < p.B) pre[base + lane] = run + incl - x;
-      run += __shfl_sync(0xffffffffu, incl, 31);
+      Le = p.window > 0 && L > p.window ? p.window : L;
+      f = p.ring > 0 ? (L - Le) % p.ring : L - Le;   // (in a ring: its row)
+      x = Le > 0 ? (f % 16 + Le + 15) / 16 : 0;
     }
-    if (lane == 0) pre[p.B] = run;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (i < p.B) {
+      first[i] = f;
+      count[i] = Le;
+      lens[i] = x;
+      pre[i] = run + incl - x;
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+    longest = max(longest, __reduce_max_sync(0xffffffffu, x));
   }
-  __syncthreads();
+  if (lane == 0) pre[p.B] = run;
+  __syncwarp();
 
   const int H = p.H_kv;
   if (blockIdx.x == 0) {
@@ -447,24 +545,38 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
         static_cast<T*>(p.out)[(size_t)bb * row_elems + i] = T(0.f);
     }
   }
-  // ranges of groups
-  const long long total = (long long)H * pre[p.B];
-  const long long N = (long long)gridDim.x * W;
-  const long long w = (long long)blockIdx.x * W + warp;
-  const long long r0 = w * total / N, r1 = (w + 1) * total / N;
+  // The CTA's groups [c0, c1): an equal share of all, or whole units where
+  // these are short; and the warp's share of them.
+  const unsigned total = (unsigned)H * run;
+  const Q8Split split(total, prm.by_ctas);
+  auto unit_start = [&](unsigned u) {
+    const unsigned b = prm.by_heads(u);
+    return b < (unsigned)p.B ? (unsigned)H * pre[b] + (u - b * H) * lens[b] : total;
+  };
+  unsigned c0, c1;
+  if (longest <= kQ8ShortGroups) {
+    const Q8Split units((unsigned)p.B * H, prm.by_ctas);
+    c0 = unit_start(units.start(blockIdx.x));
+    c1 = unit_start(units.start(blockIdx.x + 1));
+  } else {
+    c0 = split.start(blockIdx.x);
+    c1 = split.start(blockIdx.x + 1);
+  }
+  const unsigned share = (c1 - c0) / W, odd = (c1 - c0) % W;   // the first `odd` warps take one more
+  const unsigned r0 = c0 + warp * share + min((unsigned)warp, odd), r1 = r0 + share + ((unsigned)warp < odd ? 1 : 0);
   if (r0 < r1) {
   RowWalker walk;
   {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)H * pre[mid + 1] > r0) hi = mid; else lo = mid + 1;
+      if ((unsigned)H * pre[mid + 1] > r0) hi = mid; else lo = mid + 1;
     }
-    const long long off = r0 - (long long)H * pre[lo];
-    const int L = lens[lo];
+    const unsigned off = r0 - (unsigned)H * pre[lo];
+    const unsigned L = lens[lo];
     walk.b = lo;
     walk.h = (int)(off / L);
-    walk.t = (int)(off - (long long)walk.h * L);
+    walk.t = (int)(off - walk.h * L);
     walk.r = r0;
     walk.r1 = r1;
   }
@@ -489,38 +601,40 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     n1 = p.ring > 0 && row0 + nrows > p.ring ? p.ring - row0 : nrows;
   };
 
+  // This lane's scale of a tile: of plane lane / GROUPS (key sources, then
+  // value sources) and group lane % GROUPS.
+  const float* my_scales = nullptr;
+#pragma unroll
+  for (int i = 0; i < 2 * NSRC; ++i)
+    if (lane / GROUPS == i) my_scales = i >= NSRC ? prm.vs[i % NSRC] : prm.ks[i % NSRC];
+
   auto issue = [&](int stage, int b, int h, int t, int n) {
+    uint8_t* dst = wring + (size_t)stage * STAGE;
+    uint64_t* bar = &wbars[stage];
+    const size_t u = (size_t)b * H + h;
+    int row0, nrows, n1;
+    tile_rows(b, t, n, row0, nrows, n1);
     if (lane == 0) {
-      uint8_t* dst = wring + (size_t)stage * STAGE;
-      float* dsc = reinterpret_cast<float*>(dst + Cfg::CODE_BYTES);
-      uint64_t* bar = &wbars[stage];
-      const size_t u = (size_t)b * H + h;
-      int row0, nrows, n1;
-      tile_rows(b, t, n, row0, nrows, n1);
-      const int n2 = nrows - n1;
-      const int g0 = row0 / (4 * kQ8Block);                       // first 16-byte piece of scales
-      const uint32_t sb1 = (uint32_t)((row0 + n1 - 1) / (4 * kQ8Block) - g0 + 1) * 16;
-      const uint32_t sb2 = n2 > 0 ? (uint32_t)((n2 - 1) / (4 * kQ8Block) + 1) * 16 : 0;
-      const uint32_t b1 = (uint32_t)n1 * D, b2 = (uint32_t)n2 * D;
+      const uint32_t b1 = (uint32_t)n1 * D, b2 = (uint32_t)(nrows - n1) * D;
       const size_t base = u * plane_codes, off = base + (size_t)row0 * D;
-      const size_t sbase = u * plane_scales;
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(bar, (b1 + b2 + sb1 + sb2) * 2 * NSRC);
+      mbar_arrive_expect_tx(bar, (b1 + b2) * 2 * NSRC);
 #pragma unroll
       for (int i = 0; i < 2 * NSRC; ++i) {
-        const bool value = i >= NSRC;
-        const int sidx = value ? i - NSRC : i;
+        const int sidx = i % NSRC;
         const uint8_t* src =
-            static_cast<const uint8_t*>(value ? (sidx ? p.v1 : p.v0) : (sidx ? p.k1 : p.k0));
-        const float* sc = value ? prm.vs[sidx] : prm.ks[sidx];
+            static_cast<const uint8_t*>(i >= NSRC ? (sidx ? p.v1 : p.v0) : (sidx ? p.k1 : p.k0));
         bulk_g2s(dst + i * TILE, src + off, b1, bar, policy);
-        bulk_g2s(dsc + i * 2 * SCW, sc + sbase + (size_t)g0 * 4, sb1, bar, policy);
-        if (n2 > 0) {
-          bulk_g2s(dst + i * TILE + b1, src + base, b2, bar, policy);
-          bulk_g2s(dsc + (i * 2 + 1) * SCW, sc + sbase, sb2, bar, policy);
-        }
+        if (b2) bulk_g2s(dst + i * TILE + b1, src + base, b2, bar, policy);
       }
     }
+    const int gr = lane % GROUPS;
+    if (my_scales && gr < n) {
+      int row = row0 + 16 * gr;
+      if (p.ring > 0 && row >= p.ring) row -= p.ring;
+      copy4_async(dst + Cfg::CODE_BYTES + lane * 4, my_scales + u * plane_scales + row / kQ8Block);
+    }
+    arrive_after_copies(bar);
   };
 
   int issued = 0;
@@ -562,16 +676,25 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     if (fresh) {
       whole = t0 == 0;
       // head n8's query, channels [q4 D/4, + D/4), brought to [2^14, 2^15)
-      const T* qp = static_cast<const T*>(p.q) + (((size_t)b * H + h) * G + n8) * D + q4 * (D / 4);
-      float top = 0.f, x[D / 4];
+      float top = 0.f, x[D / 4], wk[NSRC][D / 4];
 #pragma unroll
-      for (int e = 0; e < D / 4; ++e) {
-        x[e] = n8 < G ? (float)qp[e] * p.qscale : 0.f;
-        const float wmax = NSRC == 2 ? fmaxf(fabsf(p.a0[(size_t)h * D + q4 * (D / 4) + e]),
-                                             fabsf(p.a1[(size_t)h * D + q4 * (D / 4) + e]))
-                           : p.a0    ? fabsf(p.a0[(size_t)h * D + q4 * (D / 4) + e])
-                                     : 1.f;
-        top = fmaxf(top, fabsf(x[e]) * wmax);
+      for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
+      if (n8 < G)
+        load_floats<D / 4>(static_cast<const T*>(p.q) + (((size_t)b * H + h) * G + n8) * D + q4 * (D / 4), x);
+#pragma unroll
+      for (int sidx = 0; sidx < NSRC; ++sidx) {
+        const float* ap = sidx == 0 ? p.a0 : p.a1;
+        if (NSRC == 2 || ap) {
+          load_floats<D / 4>(ap + (size_t)h * D + q4 * (D / 4), wk[sidx]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) wk[sidx][e] = 1.f;
+        }
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) {
+          wk[sidx][e] *= x[e] * p.qscale;
+          top = fmaxf(top, fabsf(wk[sidx][e]));
+        }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -581,18 +704,11 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       c_row = __uint_as_float((uint32_t)(127 - eq) << 23);
 #pragma unroll
       for (int sidx = 0; sidx < NSRC; ++sidx) {
-        const float* ap = sidx == 0 ? p.a0 : p.a1;
 #pragma unroll
         for (int j = 0; j < KW; ++j) {
-          float y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[e] = x[4 * j + e];
-            if (NSRC == 2 || ap) y[e] *= ap[(size_t)h * D + q4 * (D / 4) + 4 * j + e];
-            y[e] *= f;
-          }
-          split_f16(y[0], y[1], qf[sidx][j][0], qf[sidx][j][1]);
-          split_f16(y[2], y[3], qf[sidx][j][2], qf[sidx][j][3]);
+          const float* y = wk[sidx] + 4 * j;
+          split_f16(y[0] * f, y[1] * f, qf[sidx][j][0], qf[sidx][j][1]);
+          split_f16(y[2] * f, y[3] * f, qf[sidx][j][2], qf[sidx][j][3]);
         }
 #pragma unroll
         for (int i = 0; i < VT; ++i)
@@ -610,7 +726,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       // let every stage issued and not yet consumed land, this one included
       for (int k = consumed; k < issued; ++k)
         (void)mbar_wait_bounded(&wbars[k % NS], (uint32_t)(k / NS) & 1u, kDrainLimitNs);
-      if (lane == 0) *abort_flag = 1;
+      if (lane == 0) sh.head[warp] = kQ8Stopped;
       break;
     }
 
@@ -624,12 +740,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     // the tile wraps in a ring.
     auto tile = [&](auto edge) {
       constexpr bool EDGE = decltype(edge)::value;
-      // where the scale of the tile's group gr lies in a plane's run of scales
-      const int sc0 = row0 & (4 * kQ8Block - 1);
-      auto scale_at = [&](int gr) {
-        if (EDGE && 16 * gr >= n1) return SCW + (16 * gr - n1) / kQ8Block;
-        return (sc0 + 16 * gr) / kQ8Block;
-      };
+      // scale of plane i (key sources, then value sources), group gr
+      auto scale = [&](int i, int gr) { return scales[i * GROUPS + gr]; };
       // scores in base 2 plus the group's value exponent: s[gr][2 half + e] is
       // key 2 q4 + e of the half
       float s[GROUPS][4], lv[GROUPS];
@@ -641,15 +753,14 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
           lv[gr] = 0.f;
           continue;
         }
-        const int at = scale_at(gr);
-        float vs = scales[NSRC * 2 * SCW + at];
-        if constexpr (NSRC == 2) vs = fmaxf(vs, scales[(NSRC + 1) * 2 * SCW + at]);
+        float vs = scale(NSRC, gr);
+        if constexpr (NSRC == 2) vs = fmaxf(vs, scale(NSRC + 1, gr));
         lv[gr] = fast_log2(vs);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[gr][e] = lv[gr];
 #pragma unroll
         for (int sidx = 0; sidx < NSRC; ++sidx) {
-          const float f = scales[sidx * 2 * SCW + at] * c_row;
+          const float f = scale(sidx, gr) * c_row;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t kw[KW];
@@ -712,7 +823,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = pv[e];
           if constexpr (NSRC == 2) {
-            const float ratio = scales[(NSRC + sidx) * 2 * SCW + scale_at(gr)] * rv;
+            const float ratio = scale(NSRC + sidx, gr) * rv;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] *= ratio;
           }
@@ -816,16 +927,14 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   }
 
   __syncthreads();
-  if (*abort_flag) return;
-  if (G == 1) q8_tail<T, D, 1>(p, sh, W, total, lens, pre);
-  if (G == 2) q8_tail<T, D, 2>(p, sh, W, total, lens, pre);
-  if (G == 4) q8_tail<T, D, 4>(p, sh, W, total, lens, pre);
+  if (__any_sync(0xffffffffu, lane < W && sh.head[lane] == kQ8Stopped)) return;   // a wait ran out
+  q8_tail<T, D, W>(p, sh, G, total, split, c0, c1, lens, pre);
 }
 
 // Shared memory behind the rings: barriers, lengths and the words of Q8Shared;
 // then the records.
 __host__ __device__ constexpr size_t q8_aux_bytes(int warps, int stages, int B) {
-  return ((size_t)warps * stages * 8 + (size_t)(4 * B + 1 + 2 * warps + 3) * 4 + 15) / 16 * 16;
+  return ((size_t)warps * stages * 8 + (size_t)(4 * B + 1 + 2 * warps + 8) * 4 + 15) / 16 * 16;
 }
 
 template <int D, int NSRC>
@@ -867,6 +976,8 @@ cudaError_t launch_q8(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t 
     prm.vs[i] = a.v_scale[i];
   }
   prm.G = a.group;
+  prm.by_ctas = Q8Div::of((unsigned)plan.ctas);
+  prm.by_heads = Q8Div::of((unsigned)a.kv_heads);
   prm.aux_bytes = (int)q8_aux_bytes(Q8Shape<D, NSRC>::W, Q8Shape<D, NSRC>::NS, a.batch);
   auto kern = decode_q8_kernel<T, D, NSRC>;
   cudaError_t e =
