@@ -497,6 +497,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     sh.head[warp] = sh.tail[warp] = -1;
   }
   if (threadIdx.x < 8) sh.merge[threadIdx.x] = -1;
+  // the parameters' cache lines, while the kernel ahead still runs
+  asm volatile("" ::"r"(prm.by_heads.d), "r"(prm.G), "l"(prm.vs[0]), "r"(p.H_kv), "l"(p.out), "l"(p.ws));
   grid_dep_trigger();
   grid_dep_wait();
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
@@ -732,27 +734,23 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
     int row0, nrows, n1;
     tile_rows(b, t0, n, row0, nrows, n1);
-    const int skip = t0 == 0 ? first[b] % 16 : 0;   // rows of the first group before the first attended
     const uint8_t* st = wring + (size_t)stage * STAGE;
     const float* scales = reinterpret_cast<const float*>(st + Cfg::CODE_BYTES);
 
-    // One tile.  EDGE: rows before `skip` or from nrows on are not attended, or
-    // the tile wraps in a ring.
-    auto tile = [&](auto edge) {
+    // A whole tile (EDGE false), or its group g0, of whose rows those before
+    // `skip` and from `nrows` on are not attended.
+    auto tile = [&](auto edge, int g0, int skip, int nrows) {
       constexpr bool EDGE = decltype(edge)::value;
-      // scale of plane i (key sources, then value sources), group gr
-      auto scale = [&](int i, int gr) { return scales[i * GROUPS + gr]; };
+      constexpr int NG = EDGE ? 1 : GROUPS;
+      const uint8_t* codes = st + 16 * g0 * D;
+      // scale of plane i (key sources, then value sources), group g0 + gr
+      auto scale = [&](int i, int gr) { return scales[i * GROUPS + g0 + gr]; };
       // scores in base 2 plus the group's value exponent: s[gr][2 half + e] is
       // key 2 q4 + e of the half
-      float s[GROUPS][4], lv[GROUPS];
+      float s[NG][4], lv[NG];
       float mt = -INFINITY;
 #pragma unroll
-      for (int gr = 0; gr < GROUPS; ++gr) {
-        if (EDGE && 16 * gr >= nrows) {   // no such group in this tile
-          s[gr][0] = s[gr][1] = s[gr][2] = s[gr][3] = -INFINITY;
-          lv[gr] = 0.f;
-          continue;
-        }
+      for (int gr = 0; gr < NG; ++gr) {
         float vs = scale(NSRC, gr);
         if constexpr (NSRC == 2) vs = fmaxf(vs, scale(NSRC + 1, gr));
         lv[gr] = fast_log2(vs);
@@ -764,7 +762,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t kw[KW];
-            load_words<D / 4>(st + sidx * TILE + (16 * gr + 8 * half + krow) * D + q4 * (D / 4), kw);
+            load_words<D / 4>(codes + sidx * TILE + (16 * gr + 8 * half + krow) * D + q4 * (D / 4), kw);
             float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
@@ -778,7 +776,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
         }
         if constexpr (EDGE) {
           // keys 2 q4, 2 q4 + 1 of the halves are these rows of the group
-          const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
+          const int ra = vrow, rb = vrow2;
           if (ra < skip || ra >= nrows) s[gr][0] = -INFINITY;
           if (rb < skip || rb >= nrows) s[gr][1] = -INFINITY;
           if (ra + 8 < skip || ra + 8 >= nrows) s[gr][2] = -INFINITY;
@@ -810,8 +808,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       // values
       const float off = kQ8Bias - m;
 #pragma unroll
-      for (int gr = 0; gr < GROUPS; ++gr) {
-        if (EDGE && 16 * gr >= nrows) continue;
+      for (int gr = 0; gr < NG; ++gr) {
         float pv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(s[gr][e] + off);
@@ -837,14 +834,14 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
             ph[1] = f16x2_of(x[2], x[3]);
           }
           uint32_t va[VW], vb[VW], vc[VW], vd[VW];   // keys 2q, 2q + 1, 2q + 8, 2q + 9
-          const uint8_t* vt = st + (NSRC + sidx) * TILE + 16 * gr * D;
+          const uint8_t* vt = codes + (NSRC + sidx) * TILE + 16 * gr * D;
           load_value<D>(vt + vrow * D, n8, va);
           load_value<D>(vt + vrow2 * D, n8, vb);
           load_value<D>(vt + (vrow + 8) * D, n8, vc);
           load_value<D>(vt + (vrow2 + 8) * D, n8, vd);
           if constexpr (EDGE) {
             // rows that are not attended may hold anything: nothing times 0
-            const int ra = 16 * gr + vrow, rb = 16 * gr + vrow2;
+            const int ra = vrow, rb = vrow2;
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
               if (ra < skip || ra >= nrows) va[i] = 0;
@@ -866,10 +863,13 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
         }
       }
     };
-    if (skip != 0 || nrows != 16 * GROUPS || n1 != nrows)
-      tile(std::true_type{});
-    else
-      tile(std::false_type{});
+    const int skip = t0 == 0 ? first[b] % 16 : 0;   // rows of the first group before the first attended
+    if (skip == 0 && nrows == 16 * GROUPS) {
+      tile(std::false_type{}, 0, 0, 16 * GROUPS);
+    } else {
+#pragma unroll 1
+      for (int g0 = 0; g0 < n; ++g0) tile(std::true_type{}, g0, skip - 16 * g0, nrows - 16 * g0);
+    }
 
     ++consumed;
     __syncwarp();
