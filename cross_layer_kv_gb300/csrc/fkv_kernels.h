@@ -157,6 +157,7 @@ struct PrefillArgs {
   float softmax_scale;
   const float* k_scale[2];   // scales of 8-bit sources
   const float* v_scale[2];
+  int num_sms;               // (8-bit caches: how far a short chunk's keys are split)
 };
 
 // Returns cudaErrorNotSupported for shapes the tensor-core kernels do not

@@ -36,6 +36,11 @@
 // scores are masked by position, and a value that is not a number is 0 in the
 // tile and makes NaN of the rows that see it at the end.
 //
+// Where a call has few query tiles over many keys (a short chunk behind a long
+// prefix), the key tiles of a CTA's rows are split over a cluster of 2, 4 or 8
+// CTAs, which join their O, maxima and sums through distributed shared memory,
+// each for its share of the rows.
+//
 // Every wait is bounded; a wait that runs out sets an abort flag that each
 // role checks, flags the device status, and the CTA frees its tensor memory.
 #pragma once
@@ -116,6 +121,7 @@ struct Params {
   int rows;            // rows of a (sequence, KV head) in the caches
   int ring;            // > 0: position t at row t % ring
   float scale_log2;
+  int splits;          // CTAs of a cluster, which share the key tiles
 };
 
 // All of the warpgroup's 128 threads arrive; true where all were ok.
@@ -128,6 +134,34 @@ __device__ __forceinline__ bool group_and(bool ok) {
       : "r"(ok ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+
+// The same for the 256 softmax threads.
+__device__ __forceinline__ bool softmax_and(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// All threads of the cluster's CTAs meet (every one of them gets here, since
+// every wait before is bounded).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of another CTA's shared memory, at this CTA's address `addr`.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
@@ -177,7 +211,8 @@ __device__ __forceinline__ float power_of_two(int e) {   // e clamped to the nor
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <int D, int NSRC>
+// SPLIT: a cluster of p.splits CTAs shares the key tiles.
+template <int D, int NSRC, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(const Params p) {
   using C = Cfg<D, NSRC>;
   constexpr int BN = C::BN, NS = C::NS, NGRP = C::NGRP, NR = C::NR;
@@ -216,7 +251,14 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   int ux, mt;
-  prefill_cta_tile(ux, mt);   // longest query tiles first
+  const int splits = SPLIT ? p.splits : 1;
+  const int rank = SPLIT ? (int)blockIdx.x % splits : 0;   // in the cluster
+  if constexpr (SPLIT) {
+    ux = (int)blockIdx.x / splits;
+    mt = (int)(gridDim.y - 1 - blockIdx.y);
+  } else {
+    prefill_cta_tile(ux, mt);   // longest query tiles first
+  }
   const bool two_heads = p.G % 2 == 0;
   const int pairs = two_heads ? p.G / 2 : p.G;   // CTAs of a unit's heads
   const int unit = ux / pairs, pair = ux % pairs;
@@ -227,12 +269,21 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   auto g_row0 = [&](int g) { return two_heads ? mt * BM : mt * (NG * BM) + g * BM; };
   const int S_kv = p.S_kv;
   const int W = p.window;
-  // key tiles of positions pos0 + j * BN: from the first group's window start
+  // key tiles of positions start + j * BN: from the first group's window start
   // (down to the start of its block) to each group's last position
   const int pos_first = p.q_start + g_row0(0);
-  const int pos0 = W > 0 ? max(0, pos_first - W + 1) / kQ8Block * kQ8Block : 0;
-  auto n_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) - pos0 + BN - 1) / BN; };
-  const int n_max = max(n_tiles(0), n_tiles(1));
+  const int start = W > 0 ? max(0, pos_first - W + 1) / kQ8Block * kQ8Block : 0;
+  auto all_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) - start + BN - 1) / BN; };
+  // of which the CTA takes [jb, je) (all of them but in a cluster), group 1 all
+  // and group 0 those up to its own last position, one at least (a tile that is
+  // masked for all its rows, if need be); a CTA with none (idle: the first query
+  // rows have few keys) takes its neighbour's, masked
+  const int n_all = all_tiles(1);
+  const int jb = rank * n_all / splits, je = max((rank + 1) * n_all / splits, jb + 1);
+  const bool idle = SPLIT && (rank + 1) * n_all / splits == jb;
+  const int pos0 = start + jb * BN;
+  auto n_tiles = [&](int g) { return max(1, min(all_tiles(g), je) - jb); };
+  const int n_max = je - jb;
 
   auto tile_k = [&](int j) { return sK + (size_t)(j % NS) * C::KV_BYTES; };
   auto tile_v = [&](int j) { return sV + (size_t)(j % NS) * C::KV_BYTES; };
@@ -513,6 +564,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       // one decision for all; and the next step's scale records are in place
       if (!group_and(ok)) break;
     }
+    if constexpr (SPLIT) {   // the partials are there; the partials are read
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp >= C::SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
     if ((warp == C::K_PRODUCER_WARP || warp == C::V_PRODUCER_WARP) && lane == 0) {
@@ -614,6 +669,11 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
           if (ok) pass_turn();
         }
     }
+    __syncwarp();
+    if constexpr (SPLIT) {
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ---------------- softmax warpgroup of group g ----------------
@@ -698,9 +758,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       // lowest row-window start of the tile (warp-uniform).  It is done where
       // the scores lie, so that the usual tile's registers are not merged with
       // a masked tile's (128 moves a thread).
-      if (n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W)) {
+      if (n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W) || idle) {
         // visible keys of this row, as tile columns: lo <= c < hi
-        const int hi = min(qpos + 1, S_kv) - n0;
+        const int hi = idle ? 0 : min(qpos + 1, S_kv) - n0;
         const int lo = W > 0 ? qpos - W + 1 - n0 : INT_MIN;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
@@ -782,32 +842,33 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       mbar_arrive(&p_full[g]);
     }
     // the commit after the last PV product is phase ng of s_full[g]
-    if (ok && __all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)ng & 1u) &&
-                                          wait(&step_ready[ng % NSR], (uint32_t)(ng / NSR) & 1u))) {
+    ok = ok && __all_sync(0xffffffffu, wait(&s_full[g], (uint32_t)ng & 1u) &&
+                                           wait(&step_ready[ng % NSR], (uint32_t)(ng / NSR) & 1u));
+    if (ok) {
       tc_fence_after();
       // values that are not numbers among the keys that this row sees
       bool nan = bad[0] != 0;
-      {
-        const int q0 = pos_first;
-        const int lo0 = q0 - W + 1;
-        for (int i = 0; i < 8; ++i) {
-          uint32_t x = *const_cast<volatile uint32_t*>(&bad[1 + i]);
-          while (x) {
-            const int pos = q0 + i * 32 + __ffs((int)x) - 1;
-            x &= x - 1;
-            nan = nan || (pos <= qpos && (W == 0 || pos > qpos - W));
-          }
-          x = *const_cast<volatile uint32_t*>(&bad[9 + i]);
-          while (x) {
-            const int pos = lo0 + i * 32 + __ffs((int)x) - 1;
-            x &= x - 1;
-            nan = nan || (pos <= qpos && pos > qpos - W);
-          }
+      const int q0 = pos_first, lo0 = q0 - W + 1;
+      for (int i = 0; i < 8; ++i) {
+        uint32_t x = *const_cast<volatile uint32_t*>(&bad[1 + i]);
+        while (x) {
+          const int pos = q0 + i * 32 + __ffs((int)x) - 1;
+          x &= x - 1;
+          nan = nan || (pos <= qpos && (W == 0 || pos > qpos - W));
+        }
+        x = *const_cast<volatile uint32_t*>(&bad[9 + i]);
+        while (x) {
+          const int pos = lo0 + i * 32 + __ffs((int)x) - 1;
+          x &= x - 1;
+          nan = nan || (pos <= qpos && pos > qpos - W);
         }
       }
-      float inv = nan ? __uint_as_float(0x7fffffffu) : 1.f / l_run;
-      if constexpr (NSRC == 2) inv *= power_of_two(exponent_of(__uint_as_float(w_top[1])) + 1);
-      const float* wb = NSRC == 1 && p.b[0] && p.a[0] ? p.b[0] + (size_t)kh * D : nullptr;
+      if (nan) l_run = __uint_as_float(0x7fffffffu);
+    }
+    const float out_scale = NSRC == 2 ? power_of_two(exponent_of(__uint_as_float(w_top[1])) + 1) : 1.f;
+    const float* wb = NSRC == 1 && p.b[0] && p.a[0] ? p.b[0] + (size_t)kh * D : nullptr;
+    if (!SPLIT && ok) {
+      const float inv = out_scale / l_run;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                             (((size_t)b * H_q + g_head(g)) * p.S + m_row) * D;
 #pragma unroll
@@ -831,6 +892,64 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
           dst[1] = make_uint4(o8[4], o8[5], o8[6], o8[7]);
         }
       }
+    }
+    if constexpr (SPLIT) {
+      // The partials go where Q and the tiles were: O [D][256 rows], the
+      // maxima, the sums.  (Both groups' products are done once all are here.)
+      constexpr int ROWS = NG * BM;
+      static_assert((size_t)(D + 2) * ROWS * 4 <= (size_t)NG * C::Q_BYTES + 2 * NS * C::KV_BYTES, "partials fit");
+      float* part = reinterpret_cast<float*>(sQ);
+      const int r = g * BM + row;
+      if (softmax_and(ok)) {
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float ov[16];
+          tmem_ld16(t_o + c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[(c + e) * ROWS + r] = ov[e];
+        }
+        part[D * ROWS + r] = m_run;
+        part[(D + 1) * ROWS + r] = l_run;
+      }
+      cluster_sync();
+      bool stop = false;   // a CTA of the cluster gave up
+      for (int k = 0; k < splits; ++k)
+        stop = stop || ld_cluster(smem_u32(const_cast<int*>(abort_flag)), k) != 0.f;
+      if (!stop) {
+        // this CTA's share of the rows, `splits` threads a row
+        const int share = ROWS / splits, mine = rank * share + r % share, piece = r / share;
+        const int og = mine / BM, orow = g_row0(og) + mine % BM, width = D / splits;
+        const uint32_t at = smem_u32(part) + mine * 4;
+        float top = -FLT_MAX, sum = 0.f, w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          w[k] = k < splits ? ld_cluster(at + D * ROWS * 4, k) : -FLT_MAX;
+          top = fmaxf(top, w[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          w[k] = k < splits ? fast_exp2(w[k] - top) : 0.f;
+          if (k < splits) sum = fmaf(w[k], ld_cluster(at + (D + 1) * ROWS * 4, k), sum);
+        }
+        const float inv = out_scale / sum;
+        if (orow < p.S) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                               (((size_t)b * H_q + g_head(og)) * p.S + orow) * D;
+          for (int d = piece * width; d < (piece + 1) * width; d += 2) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < splits) {
+                x = fmaf(w[k], ld_cluster(at + d * ROWS * 4, k), x);
+                y = fmaf(w[k], ld_cluster(at + (d + 1) * ROWS * 4, k), y);
+              }
+            if (wb) x *= wb[d], y *= wb[d + 1];
+            *reinterpret_cast<__nv_bfloat162*>(dst + d) = __floats2bfloat162_rn(x * inv, y * inv);
+          }
+        }
+      }
+      cluster_sync();
     }
   }
 
@@ -888,7 +1007,22 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   p.rows = a.plane_rows;
   p.ring = a.ring;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-  auto kern = prefill_q8_kernel<D, NSRC>;
+  // one CTA per (unit, 128 query rows of two heads, or 256 of one)
+  const bool two_heads = a.group % 2 == 0;
+  const int rows_per_cta = two_heads ? BM : NG * BM;
+  const long long units = (long long)a.batch * a.kv_heads * (two_heads ? a.group / 2 : a.group);
+  const long long tiles = (a.S + rows_per_cta - 1) / rows_per_cta;
+  if (tiles > 65535 || units * tiles > INT_MAX / 8) return cudaErrorNotSupported;
+  // Few CTAs with many key tiles each: clusters that share them, of as many
+  // CTAs as still find an SM each, with two tiles a CTA at least (a join costs
+  // about a tile).  8 units of 16 rows behind 16368 keys (D = 96): 232 us with
+  // one CTA a unit, 45 with 8.
+  long long keys = p.S_kv;
+  if (a.window > 0 && a.window + rows_per_cta < keys) keys = a.window + rows_per_cta;
+  const long long key_tiles = (keys + C::BN - 1) / C::BN;
+  p.splits = 1;
+  while (p.splits < 8 && units * tiles * p.splits * 2 <= a.num_sms && key_tiles >= 4 * p.splits) p.splits *= 2;
+  auto kern = p.splits > 1 ? prefill_q8_kernel<D, NSRC, true> : prefill_q8_kernel<D, NSRC, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   // The register split inside the kernel must fit the launch allocation, or
@@ -897,14 +1031,18 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if ((long long)fa.numRegs * C::THREADS < C::REGS_SPLIT) return cudaErrorNotSupported;
-  // one CTA per (unit, 128 query rows of two heads, or 256 of one)
-  const bool two_heads = a.group % 2 == 0;
-  const int rows_per_cta = two_heads ? BM : NG * BM;
-  const long long units = (long long)a.batch * a.kv_heads * (two_heads ? a.group / 2 : a.group);
-  const long long tiles = (a.S + rows_per_cta - 1) / rows_per_cta;
-  if (tiles > 65535 || units * tiles > INT_MAX) return cudaErrorNotSupported;
-  kern<<<dim3((unsigned)units, (unsigned)tiles), C::THREADS, C::SMEM, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * p.splits), (unsigned)tiles);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace q8p
