@@ -205,6 +205,7 @@ fkv::DecodeArgs decode_args(const fkv_ctx* c) {
   d.status = c->status;
   d.wait_limit = c->wait_limit;
   d.num_ctas = c->cfg.decode_ctas;
+  d.device = c->device;
   return d;
 }
 
@@ -604,6 +605,7 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   p.softmax_scale = c->scale;
   source_scales(c, src, p.k_scale, p.v_scale);
   p.num_sms = c->num_sms;
+  p.device = c->device;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = q8 ? fkv::prefill_q8_launch(p, st) : fkv::prefill_launch(p, st);
   if (e == cudaErrorNotSupported) return FKV_ERR_UNSUPPORTED;

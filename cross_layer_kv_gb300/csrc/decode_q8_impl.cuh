@@ -77,7 +77,7 @@ struct Q8Cfg {
   static constexpr int TR = 16 * S::GROUPS;            // rows per tile
   static constexpr int TILE_BYTES = TR * D;            // codes of one plane's tile
   static constexpr int CODE_BYTES = 2 * NSRC * TILE_BYTES;
-  static constexpr int STAGE_BYTES = CODE_BYTES + 128;   // and a scale for every plane and group
+  static constexpr int STAGE_BYTES = CODE_BYTES + (2 * NSRC * S::GROUPS * 4 + 15) / 16 * 16;   // and a scale for every plane and group
   static_assert(TILE_BYTES % 16 == 0, "stages are read in 16-byte pieces");
   static_assert(2 * NSRC * S::GROUPS <= 32, "a lane copies one of a tile's scales");
 };
@@ -98,7 +98,7 @@ struct Q8Params {
   const float* vs[2];
   int G;
   int aux_bytes;
-  Q8Div by_ctas, by_heads;
+  Q8Div by_ctas, by_heads, by_ring;
 };
 
 // Copy 4 bytes to shared memory without waiting; and arrive on a barrier once
@@ -351,7 +351,7 @@ struct Q8Shared {
 // crosses CTAs).  A warp takes a chain of partials and a head at a time.
 template <typename T, int D, int W>
 __device__ __forceinline__ void q8_tail(const SplitParams& p, const Q8Shared& sh, int G, unsigned total,
-                                        const Q8Split& split, unsigned c0, unsigned c1, const int* lens,
+                                        const Q8Split& split, unsigned c0, unsigned c1,
                                         const int* pre) {
   constexpr int PS = partial_stride(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -368,8 +368,9 @@ __device__ __forceinline__ void q8_tail(const SplitParams& p, const Q8Shared& sh
   const int chains = __popc(tails) + (starts_inside ? 1 : 0);
   auto unit_range = [&](int u, unsigned& su, unsigned& eu) {   // its groups
     const int b = u / H, h = u - b * H;
-    su = (unsigned)H * pre[b] + (unsigned)h * lens[b];
-    eu = su + lens[b];
+    const int L = pre[b + 1] - pre[b];
+    su = (unsigned)H * pre[b] + (unsigned)h * L;
+    eu = su + L;
   };
   for (int task = warp; task < chains * G; task += W) {
     const int c = task / G, g = task - c * G;
@@ -455,6 +456,35 @@ __device__ __forceinline__ void q8_tail(const SplitParams& p, const Q8Shared& sh
   }
 }
 
+// Walk of a warp's range of groups, one tile at a time, crossing units.  pre:
+// sums of the sequences' groups.
+struct Q8Walker {
+  unsigned r, r1;
+  int b, h, t;
+  __device__ __forceinline__ bool next(const int* pre, int H, int B, int most, int& tb, int& th, int& tt, int& tn,
+                                       bool& last) {
+    if (r >= r1) return false;
+    const int L = pre[b + 1] - pre[b];
+    const int seg = (int)min((unsigned)(L - t), r1 - r), n = min(most, seg);
+    tb = b;
+    th = h;
+    tt = t;
+    tn = n;
+    last = n == seg;
+    t += n;
+    r += n;
+    if (t == L) {
+      t = 0;
+      if (++h == H) {
+        h = 0;
+        ++b;
+        while (r < r1 && b < B && pre[b + 1] == pre[b]) ++b;
+      }
+    }
+    return true;
+  }
+};
+
 // Sequences of up to this many groups of 16 rows are short: a CTA takes whole
 // units then, since a merge through global memory (3 us) costs more than an
 // uneven split.
@@ -476,12 +506,10 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)W * NS * STAGE);
-  int* lens = reinterpret_cast<int*>(bars + W * NS);   // groups of 16 rows per sequence
-  int* pre = lens + p.B;                               // their sums before a sequence
-  int* first = pre + p.B + 1;                          // first attended row
-  int* count = first + p.B;                            // attended rows
+  int* len = reinterpret_cast<int*>(bars + W * NS);   // the sequences' lengths, clamped
+  int* pre = len + p.B;                               // sums of their groups of 16 rows
   Q8Shared sh;
-  sh.head = count + p.B;
+  sh.head = pre + p.B + 1;
   sh.tail = sh.head + W;
   sh.merge = sh.tail + W;
   sh.head_rec = reinterpret_cast<float*>(smem + (size_t)W * NS * STAGE + prm.aux_bytes);
@@ -505,19 +533,24 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
   // Lengths and their sums, by every warp for itself (all write the same
   // values): no warp waits for another.
+  auto attended = [&](int L, int& f, int& rows) {   // first attended row (in a ring: its row), and how many
+    rows = p.window > 0 && L > p.window ? p.window : L;
+    f = L - rows;
+    if (p.ring > 0) f -= (int)prm.by_ring(f) * p.ring;
+  };
   int run = 0, longest = 0;
   for (int base = 0; base < p.B; base += 32) {
     const int i = base + lane;
-    int f = 0, Le = 0, x = 0;
+    int L = 0, x = 0;
     if (i < p.B) {
-      int L = p.seq_lens[i];
+      L = p.seq_lens[i];
       if (L < 1 || L > p.S_max) {
         if (blockIdx.x == 0 && warp == 0) flag_status(p.status, kDevBadArg);
         L = L < 0 ? 0 : (L > p.S_max ? p.S_max : L);
       }
-      Le = p.window > 0 && L > p.window ? p.window : L;
-      f = p.ring > 0 ? (L - Le) % p.ring : L - Le;   // (in a ring: its row)
-      x = Le > 0 ? (f % 16 + Le + 15) / 16 : 0;
+      int f, rows;
+      attended(L, f, rows);
+      x = rows > 0 ? (f % 16 + rows + 15) / 16 : 0;
     }
     int incl = x;
 #pragma unroll
@@ -526,9 +559,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       if (lane >= o) incl += y;
     }
     if (i < p.B) {
-      first[i] = f;
-      count[i] = Le;
-      lens[i] = x;
+      len[i] = L;
       pre[i] = run + incl - x;
     }
     run += __shfl_sync(0xffffffffu, incl, 31);
@@ -542,7 +573,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     // sequences of length 0 have no rows and so no merging warp: zero output
     const int row_elems = H * G * D;
     for (int bb = 0; bb < p.B; ++bb) {
-      if (lens[bb] != 0) continue;
+      if (pre[bb + 1] != pre[bb]) continue;
       for (int i = threadIdx.x; i < row_elems; i += blockDim.x)
         static_cast<T*>(p.out)[(size_t)bb * row_elems + i] = T(0.f);
     }
@@ -553,7 +584,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   const Q8Split split(total, prm.by_ctas);
   auto unit_start = [&](unsigned u) {
     const unsigned b = prm.by_heads(u);
-    return b < (unsigned)p.B ? (unsigned)H * pre[b] + (u - b * H) * lens[b] : total;
+    return b < (unsigned)p.B ? (unsigned)H * pre[b] + (u - b * H) * (pre[b + 1] - pre[b]) : total;
   };
   unsigned c0, c1;
   if (longest <= kQ8ShortGroups) {
@@ -567,7 +598,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   const unsigned share = (c1 - c0) / W, odd = (c1 - c0) % W;   // the first `odd` warps take one more
   const unsigned r0 = c0 + warp * share + min((unsigned)warp, odd), r1 = r0 + share + ((unsigned)warp < odd ? 1 : 0);
   if (r0 < r1) {
-  RowWalker walk;
+  Q8Walker walk;
   {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
@@ -575,14 +606,14 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       if ((unsigned)H * pre[mid + 1] > r0) hi = mid; else lo = mid + 1;
     }
     const unsigned off = r0 - (unsigned)H * pre[lo];
-    const unsigned L = lens[lo];
+    const unsigned L = pre[lo + 1] - pre[lo];
     walk.b = lo;
     walk.h = (int)(off / L);
     walk.t = (int)(off - walk.h * L);
     walk.r = r0;
     walk.r1 = r1;
   }
-  RowWalker prod = walk;
+  Q8Walker prod = walk;
 
   uint8_t* wring = smem + (size_t)warp * NS * STAGE;   // this warp's stages
   uint64_t* wbars = bars + warp * NS;
@@ -593,13 +624,17 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
   // A tile of n groups from group t of sequence b: the row of its first one,
   // how many of its rows are read (the sequence's last rows may end inside a
-  // group), and how many of those come before a ring's end (a whole number of
-  // groups; the others follow from the ring's start).
-  auto tile_rows = [&](int b, int t, int n, int& row0, int& nrows, int& n1) {
-    const int lead = first[b] % 16;
-    row0 = first[b] - lead + 16 * t;
+  // group), how many of those come before a ring's end (a whole number of
+  // groups; the others follow from the ring's start), and how many come before
+  // the first attended one.
+  auto tile_rows = [&](int b, int t, int n, int& row0, int& nrows, int& n1, int& skip) {
+    int f, rows;
+    attended(len[b], f, rows);
+    const int lead = f % 16;
+    row0 = f - lead + 16 * t;
     if (p.ring > 0 && row0 >= p.ring) row0 -= p.ring;
-    nrows = min(16 * n, lead + count[b] - 16 * t);
+    nrows = min(16 * n, lead + rows - 16 * t);
+    skip = t == 0 ? lead : 0;
     n1 = p.ring > 0 && row0 + nrows > p.ring ? p.ring - row0 : nrows;
   };
 
@@ -614,8 +649,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     uint8_t* dst = wring + (size_t)stage * STAGE;
     uint64_t* bar = &wbars[stage];
     const size_t u = (size_t)b * H + h;
-    int row0, nrows, n1;
-    tile_rows(b, t, n, row0, nrows, n1);
+    int row0, nrows, n1, before;
+    tile_rows(b, t, n, row0, nrows, n1, before);
     if (lane == 0) {
       const uint32_t b1 = (uint32_t)n1 * D, b2 = (uint32_t)(nrows - n1) * D;
       const size_t base = u * plane_codes, off = base + (size_t)row0 * D;
@@ -644,7 +679,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   for (int s = 0; s < NS; ++s) {
     int tb, th, tt, tn;
     bool tl;
-    if (!prod.next(lens, H, p.B, GROUPS, tb, th, tt, tn, tl)) break;
+    if (!prod.next(pre, H, p.B, GROUPS, tb, th, tt, tn, tl)) break;
     issue(s, tb, th, tt, tn);
     ++issued;
   }
@@ -671,7 +706,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   for (;;) {
     int b, h, t0, n;
     bool last;
-    if (!walk.next(lens, H, p.B, GROUPS, b, h, t0, n, last)) break;
+    if (!walk.next(pre, H, p.B, GROUPS, b, h, t0, n, last)) break;
     const int stage = consumed % NS;
     const uint32_t parity = (uint32_t)(consumed / NS) & 1u;
 
@@ -732,8 +767,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       break;
     }
 
-    int row0, nrows, n1;
-    tile_rows(b, t0, n, row0, nrows, n1);
+    int row0, nrows, n1, skip;   // skip: rows of the first group before the first attended
+    tile_rows(b, t0, n, row0, nrows, n1, skip);
     const uint8_t* st = wring + (size_t)stage * STAGE;
     const float* scales = reinterpret_cast<const float*>(st + Cfg::CODE_BYTES);
 
@@ -863,7 +898,6 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
         }
       }
     };
-    const int skip = t0 == 0 ? first[b] % 16 : 0;   // rows of the first group before the first attended
     if (skip == 0 && nrows == 16 * GROUPS) {
       tile(std::false_type{}, 0, 0, 16 * GROUPS);
     } else {
@@ -877,7 +911,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     {
       int tb, th, tt, tn;
       bool tl;
-      if (prod.next(lens, H, p.B, GROUPS, tb, th, tt, tn, tl)) {
+      if (prod.next(pre, H, p.B, GROUPS, tb, th, tt, tn, tl)) {
         issue(stage, tb, th, tt, tn);
         ++issued;
       }
@@ -889,7 +923,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       const int u = b * H + h;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const bool ends = t0 + n == lens[b];
+      const bool ends = t0 + n == pre[b + 1] - pre[b];
       float* rec = whole ? reinterpret_cast<float*>(wring) : sh.head_rec + (size_t)warp * G * PS;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -928,13 +962,13 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
   __syncthreads();
   if (__any_sync(0xffffffffu, lane < W && sh.head[lane] == kQ8Stopped)) return;   // a wait ran out
-  q8_tail<T, D, W>(p, sh, G, total, split, c0, c1, lens, pre);
+  q8_tail<T, D, W>(p, sh, G, total, split, c0, c1, pre);
 }
 
 // Shared memory behind the rings: barriers, lengths and the words of Q8Shared;
 // then the records.
 __host__ __device__ constexpr size_t q8_aux_bytes(int warps, int stages, int B) {
-  return ((size_t)warps * stages * 8 + (size_t)(4 * B + 1 + 2 * warps + 8) * 4 + 15) / 16 * 16;
+  return ((size_t)warps * stages * 8 + (size_t)(2 * B + 1 + 2 * warps + 8) * 4 + 15) / 16 * 16;
 }
 
 template <int D, int NSRC>
@@ -978,10 +1012,15 @@ cudaError_t launch_q8(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t 
   prm.G = a.group;
   prm.by_ctas = Q8Div::of((unsigned)plan.ctas);
   prm.by_heads = Q8Div::of((unsigned)a.kv_heads);
+  prm.by_ring = Q8Div::of((unsigned)(a.ring > 0 ? a.ring : 1));
   prm.aux_bytes = (int)q8_aux_bytes(Q8Shape<D, NSRC>::W, Q8Shape<D, NSRC>::NS, a.batch);
   auto kern = decode_q8_kernel<T, D, NSRC>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_bytes);
+  static KernelReady ready;   // (for the largest batch and group)
+  static_assert(Q8Cfg<D, NSRC>::STAGE_BYTES * Q8Shape<D, NSRC>::W * Q8Shape<D, NSRC>::NS +
+                        (int)q8_aux_bytes(Q8Shape<D, NSRC>::W, Q8Shape<D, NSRC>::NS, 1024) +
+                        Q8Shape<D, NSRC>::W * 4 * partial_stride(D) * 4 <= 232448,
+                "shared memory of the largest batch and group");
+  const cudaError_t e = ready.check(kern, a.device, (int)q8_smem_bytes<D, NSRC>(1024, 4), 0, 0);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(plan.ctas), dim3(plan.warps_per_cta * 32), plan.smem_bytes, stream, prm);
 }

@@ -40,6 +40,7 @@ struct DecodeArgs {
   unsigned epoch;            // distinct per call (tags the unit arrival counts)
   const float* k_scale[2];   // scales of 8-bit sources
   const float* v_scale[2];
+  int device;
 };
 
 // Launch configuration the library picks for a decode call shape.
@@ -157,7 +158,7 @@ struct PrefillArgs {
   float softmax_scale;
   const float* k_scale[2];   // scales of 8-bit sources
   const float* v_scale[2];
-  int num_sms;               // (8-bit caches: how far a short chunk's keys are split)
+  int device, num_sms;       // (8-bit caches: num_sms, how far a short chunk's keys are split)
 };
 
 // Returns cudaErrorNotSupported for shapes the tensor-core kernels do not

@@ -1023,14 +1023,11 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   p.splits = 1;
   while (p.splits < 8 && units * tiles * p.splits * 2 <= a.num_sms && key_tiles >= 4 * p.splits) p.splits *= 2;
   auto kern = p.splits > 1 ? prefill_q8_kernel<D, NSRC, true> : prefill_q8_kernel<D, NSRC, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-  if (e != cudaSuccess) return e;
   // The register split inside the kernel must fit the launch allocation, or
-  // the softmax warpgroups' increase would never be granted: refuse instead.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
+  // the softmax warpgroups' increase would never be granted: refused then.
+  static KernelReady ready[2];
+  const cudaError_t e = ready[p.splits > 1].check(kern, a.device, (int)C::SMEM, C::THREADS, (int)C::REGS_SPLIT);
   if (e != cudaSuccess) return e;
-  if ((long long)fa.numRegs * C::THREADS < C::REGS_SPLIT) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * p.splits), (unsigned)tiles);
   cfg.blockDim = dim3(C::THREADS);
