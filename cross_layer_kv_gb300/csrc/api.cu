@@ -300,6 +300,7 @@ fkv_status decode_attn_impl(fkv_ctx* c, const void* q, int layer, int mode,
   // ring caches hold the last `ring` positions: the layer must attend within them
   if (ring > 0 && (c->window[layer] < 1 || c->window[layer] > ring)) return FKV_ERR_INVALID_ARG;
   if (ring > 0 && format == fkv::kCacheQ8 && c->window[layer] > ring - kQ8Lost) return FKV_ERR_UNSUPPORTED;
+  if (format == fkv::kCacheQ8 && !on_device(c)) return FKV_ERR_INVALID_ARG;
   if (!q || !out || !seq_lens || !aligned16(q) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
     return FKV_ERR_INVALID_ARG;
@@ -475,6 +476,7 @@ fkv_status fkv_append_kv(fkv_ctx* c, int layer, const void* k_new, const void* v
   if (c->ring[layer] > 0 && T > c->ring[layer]) return FKV_ERR_INVALID_ARG;
   if (!c->k[layer] || !c->v[layer]) return FKV_ERR_INVALID_ARG;
   const int format = c->format[layer];
+  if (format == fkv::kCacheQ8 && !on_device(c)) return FKV_ERR_INVALID_ARG;
   if (format == fkv::kCacheQ8 && !planes_fit_grid(c)) return FKV_ERR_UNSUPPORTED;
   if (format == fkv::kCacheQ8 && c->ring[layer] > 0) {
     if (c->ring[layer] % fkv::kQ8Block != 0) return FKV_ERR_UNSUPPORTED;
@@ -576,6 +578,7 @@ fkv_status fkv_prefill_attn_chunk(fkv_ctx* c, const void* q, int layer, int mode
   if (s != FKV_OK) return s;
   if (format == fkv::kCacheQ4) return FKV_ERR_UNSUPPORTED;   // prefill reads bf16 and 8-bit caches
   const bool q8 = format == fkv::kCacheQ8;
+  if (q8 && !on_device(c)) return FKV_ERR_INVALID_ARG;
   if (c->cfg.dtype != FKV_BF16) return FKV_ERR_UNSUPPORTED;
   if (S < 1 || q_start < 0 || (long long)q_start + S > c->cfg.max_seq) return FKV_ERR_INVALID_ARG;
   // Over ring caches whose positions have wrapped, every key a query of the

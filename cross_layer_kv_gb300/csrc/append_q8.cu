@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, in
     }
     // rows [r0, r1) of block g are new; the first of them is row t0 of the call
     const int g = p / kQ8Block + i;
+    if (g > (p + a.T - 1) / kQ8Block) continue;
     const int base = g * kQ8Block;
-    if (base >= p + a.T) continue;
     const int r0 = p > base ? p - base : 0;
     const int r1 = p + a.T - base < kQ8Block ? p + a.T - base : kQ8Block;
     const int t0 = base + r0 - p;
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, in
         *pc = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    __syncwarp();   // all lanes have read the scale
     if (lane == 0) *sp = s;
   }
 }

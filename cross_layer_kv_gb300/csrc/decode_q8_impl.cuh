@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       for (int gr = 0; gr < NG; ++gr) {
         float vs = scale(NSRC, gr);
         if constexpr (NSRC == 2) vs = fmaxf(vs, scale(NSRC + 1, gr));
-        lv[gr] = fast_log2(vs);
+        lv[gr] = fast_log2(fmaxf(vs, kQ8MinValue));
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[gr][e] = lv[gr];
 #pragma unroll
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = pv[e];
-          if constexpr (NSRC == 2) {
+          if (NSRC == 2 || scale(NSRC, gr) < kQ8MinValue) {
             const float ratio = scale(NSRC + sidx, gr) * rv;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] *= ratio;

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   uint8_t* sV = sK + NS * C::KV_BYTES;
   uint8_t* sRawK = sV + NS * C::KV_BYTES;               // codes, the sources of a slot side by side
   uint8_t* sRawV = sRawK + NR * NSRC * C::RAW_BYTES;
-  float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s, log2 r, 1 / r, -}
+  float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s, log2 r, 1 / r, rest of r}
   // of K and V: (s0 / s, s1 / s), each as two equal halves
   uint2* sRatio = reinterpret_cast<uint2*>(sScale + NSR * NGRP);
   uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + (NSRC == 2 ? NSR * 2 * NGRP : 0));   // fp16 a0, a1, b0, b1
@@ -367,16 +367,16 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     };
     auto store_scales = [&](int j) {
       if (ft >= NGRP) return;
-      float s = ns[0], r = ns[NSRC];
+      float s = ns[0], r = fmaxf(ns[NSRC], kQ8MinValue);
       if constexpr (NSRC == 2) {
-        s = fmaxf(ns[0], ns[1]);
-        r = fmaxf(ns[2], ns[3]);
+        s = fmaxf(fmaxf(ns[0], ns[1]), FLT_MIN);
+        r = fmaxf(fmaxf(ns[2], ns[3]), kQ8MinValue);
         const float is = 1.f / s, ir = 1.f / r;
         uint2* rec = sRatio + (size_t)(j % NSR) * 2 * NGRP;
         rec[ft] = make_uint2(f16x2_of(ns[0] * is, ns[0] * is), f16x2_of(ns[1] * is, ns[1] * is));
         rec[NGRP + ft] = make_uint2(f16x2_of(ns[2] * ir, ns[2] * ir), f16x2_of(ns[3] * ir, ns[3] * ir));
       }
-      sScale[(j % NSR) * NGRP + ft] = make_float4(s, log2f(r), 1.f / r, 0.f);
+      sScale[(j % NSR) * NGRP + ft] = make_float4(s, log2f(r), 1.f / r, ns[NSRC] / r);
     };
     // A value that is not a number: noted for the rows that see it, 0 in the tile.
     auto note_bad = [&](int pos) {
@@ -498,7 +498,14 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         }
       }
       if constexpr (VALUE) {
-        if (((nan[0] | nan[1] | nan[2] | nan[3]) & 0x7fff7fffu) != 0) {
+        // the rest of one source's scale, where the exponents do not take it whole
+        [[maybe_unused]] const float4* rec = sScale + (j % NSR) * NGRP;
+        bool whole = true;
+        if constexpr (NSRC == 1) {
+#pragma unroll
+          for (int gr = 0; gr < NGRP; ++gr) whole = whole && rec[gr].w == 1.f;
+        }
+        if (((nan[0] | nan[1] | nan[2] | nan[3]) & 0x7fff7fffu) != 0 || !whole) {
           // values that are no numbers: noted, and zeros put in their places
 #pragma unroll 1
           for (int it = 0; it < ITEMS; ++it) {
@@ -513,10 +520,15 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
               xw[e] &= ~((nan_codes(xw[e]) >> 7) * 255u);
               yw[e] &= ~((nan_codes(yw[e]) >> 7) * 255u);
             }
-            if (!any) continue;
-            note_bad(pos0 + j * BN + item_row(it));
+            if (any) note_bad(pos0 + j * BN + item_row(it));
+            if (!any && whole) continue;
             load_weights(it, true, w);
             combine(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(yw[0], yw[1], yw[2], yw[3]), r, w, o);
+            if constexpr (NSRC == 1) {
+              const float rest = rec[item_row(it) / kQ8Block].w;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = hmul2u(o[e], f16x2_of(rest, rest));
+            }
             put(dst, it, o);
           }
         }
@@ -915,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       cluster_sync();
       bool stop = false;   // a CTA of the cluster gave up
       for (int k = 0; k < splits; ++k)
-        stop = stop || ld_cluster(smem_u32(const_cast<int*>(abort_flag)), k) != 0.f;
+        stop = stop || __float_as_int(ld_cluster(smem_u32(const_cast<int*>(abort_flag)), k)) != 0;
       if (!stop) {
         // this CTA's share of the rows, `splits` threads a row
         const int share = ROWS / splits, mine = rank * share + r % share, piece = r / share;
@@ -1011,14 +1023,14 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   const bool two_heads = a.group % 2 == 0;
   const int rows_per_cta = two_heads ? BM : NG * BM;
   const long long units = (long long)a.batch * a.kv_heads * (two_heads ? a.group / 2 : a.group);
-  const long long tiles = (a.S + rows_per_cta - 1) / rows_per_cta;
+  const long long tiles = ((long long)a.S + rows_per_cta - 1) / rows_per_cta;
   if (tiles > 65535 || units * tiles > INT_MAX / 8) return cudaErrorNotSupported;
   // Few CTAs with many key tiles each: clusters that share them, of as many
   // CTAs as still find an SM each, with two tiles a CTA at least (a join costs
   // about a tile).  8 units of 16 rows behind 16368 keys (D = 96): 232 us with
-  // one CTA a unit, 45 with 8.
+  // one CTA a unit, 43 with 8.
   long long keys = p.S_kv;
-  if (a.window > 0 && a.window + rows_per_cta < keys) keys = a.window + rows_per_cta;
+  if (a.window > 0 && (long long)a.window + rows_per_cta < keys) keys = (long long)a.window + rows_per_cta;
   const long long key_tiles = (keys + C::BN - 1) / C::BN;
   p.splits = 1;
   while (p.splits < 8 && units * tiles * p.splits * 2 <= a.num_sms && key_tiles >= 4 * p.splits) p.splits *= 2;

@@ -19,6 +19,12 @@
 
 namespace fkv {
 
+// Attention keeps a block's value scale in the exponents of its softmax
+// weights, down to this one.  Below it (a block of zeros has 2^-100, one never
+// written 0) the rest of the scale goes into the product, so that such a block
+// still takes its part of the softmax's sum beside blocks of far larger scales.
+constexpr float kQ8MinValue = 0x1p-64f;
+
 // Four e4m3 codes -> two fp16 pairs (the lower codes first), exactly.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"

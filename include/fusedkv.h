@@ -137,9 +137,13 @@ int fkv_q8_scale_cols(int rows);
  * exponent bits, 3 fraction bits, 0x7F and 0xFF not a number); k_scales,
  * v_scales: device fp32 [B, H_kv, fkv_q8_scale_cols(R)]; R = S_max, or the
  * layer's ring rows.  All 16-byte aligned.  Row r's values are its codes times
- * scale r / 32 of its (sequence, KV head), in K and V apart.  Scales are
- * positive and finite; fkv_append_kv makes them powers of two, and scales that
- * a caller fills in may be others.
+ * scale r / 32 of its (sequence, KV head), in K and V apart.  Scales are finite
+ * and not negative (0: the block's values are zeros); fkv_append_kv makes them
+ * powers of two, and scales that a caller fills in may be others.  Attention is
+ * as precise as stated there for value scales from 2^-64 to 2^39 (blocks whose
+ * largest value lies between 10^-16 and 10^14) and blocks of zeros; smaller
+ * values lose bits and may count as 0, and beside larger ones a softmax weight
+ * may.
  * fkv_append_kv quantises new rows as they are written: with amax the largest
  * finite magnitude of the rows that a call writes into a block of 32, and need
  * = 2^e the smallest power of two with amax <= 448 * 2^e (e clamped to [-100,
@@ -159,7 +163,8 @@ int fkv_q8_scale_cols(int rows);
  * (_noalloc) and, in bf16 contexts, fkv_prefill_attn (_chunk), where every
  * source of the call is 8-bit (a mix of formats is FKV_ERR_UNSUPPORTED).
  * fkv_tree_attn over them, and fkv_compact_rows and fkv_reorder_seqs while a
- * layer holds them, are FKV_ERR_UNSUPPORTED.
+ * layer holds them, are FKV_ERR_UNSUPPORTED.  The calls are made with the
+ * context's device current (FKV_ERR_INVALID_ARG otherwise).
  * Rings: R a multiple of 32 (FKV_ERR_UNSUPPORTED otherwise, from the calls);
  * an append that comes round to a block loses the up to 31 older rows behind
  * the new ones in it, so fkv_append_kv needs T + 31 <= R (FKV_ERR_INVALID_ARG),

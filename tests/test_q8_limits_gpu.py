@@ -177,3 +177,77 @@ def test_planes_that_start_inside_an_allocation():
     for _, raw in whole + [(am, ra), (bm, rb)] + back:
         assert bool((raw[:16] == 0x55).all()) and bool((raw[-32:] == 0x55).all())
     s.close()
+
+
+def _far_apart(s):
+    """Values of about 2^30, beside a block of zeros with the scale that appended zeros have, one
+    with codes but no scale (never written), and keys without a scale."""
+    for l, ((kc, ks), (vc, vs)) in s.planes.items():
+        vs *= 2.0 ** 30
+        vc.view(torch.uint8)[:, :, 64:96] = 0
+        vs[:, :, 2] = 2.0 ** -100
+        vs[:, :, 4] = ks[:, :, 4] = ks[:, :, 1] = 0
+
+
+@pytest.mark.parametrize("mode,dtype", [("vanilla", "bf16"), ("lite", "f32"), ("scaled", "bf16"), ("fused", "bf16"),
+                                        ("fused", "f32")])
+def test_decode_blocks_of_zeros_beside_large_values(mode, dtype):
+    s = Setup(mode, 2, 300, 2, 2, 96, dtype=dtype, seed=14)
+    _far_apart(s)
+    check_decode(s, [300, 100])
+    s.close()
+
+
+@pytest.mark.parametrize("mode", ["vanilla", "scaled", "fused"])
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_prefill_blocks_of_zeros_beside_large_values(mode, D):
+    s = Setup(mode, 1, 300, 2, 2, D, seed=14)
+    _far_apart(s)
+    check_prefill(s, 20, 280)
+    s.close()
+
+
+@pytest.mark.parametrize("mode", ["vanilla", "fused"])
+def test_caches_that_were_never_written_read_as_zeros(mode):
+    s = Setup(mode, 2, 300, 2, 2, 64, seed=15)
+    for planes in s.planes.values():
+        for codes, scales in planes:
+            codes.view(torch.uint8).zero_()
+            scales.zero_()
+    q, qp = s.query(2, 4, 64), s.query(2, 4, 300, 64)
+    out, outp = torch.full_like(q, float("nan")), torch.full_like(qp, float("nan"))
+    s.ctx.fkv_decode_attn(q, s.layer, mode, i32([300, 33]), out, s.ctx.workspace())
+    s.ctx.fkv_prefill_attn(qp, s.layer, mode, 300, outp)
+    assert bool((out == 0).all()) and bool((outp == 0).all())
+    # and one written block counts beside them
+    new, pos = s.query(2, 2, 1, 64), i32([200, 32])
+    for l in s.planes:
+        s.ctx.fkv_append_kv(l, new, new, pos)
+    check_decode(s, [300, 33], q)
+    check_prefill(s, 0, 300, qp)
+    s.close()
+
+
+@pytest.mark.parametrize("mode", ["vanilla", "fused"])
+def test_values_of_tiny_scales(mode):
+    """Smaller than attention keeps: no more than the values themselves, and numbers."""
+    s = Setup(mode, 1, 300, 2, 2, 64, seed=16)
+    for _, (vc, vs) in s.planes.values():
+        vs *= 2.0 ** -80
+    top = float(s.rows()[1].abs().max()) * 1.01
+    q, qp = s.query(1, 4, 64), s.query(1, 4, 300, 64)
+    out, outp = torch.full_like(q, float("nan")), torch.full_like(qp, float("nan"))
+    s.ctx.fkv_decode_attn(q, s.layer, mode, i32([300]), out, s.ctx.workspace())
+    s.ctx.fkv_prefill_attn(qp, s.layer, mode, 300, outp)
+    assert bool((out.abs() <= top).all()) and bool((outp.abs() <= top).all())
+    s.close()
+
+
+def test_decode_of_no_rows_at_all():
+    s = Setup("lite", 3, 300, 2, 2, 64, seed=17)
+    q = s.query(3, 4, 64)
+    out = torch.full_like(q, float("nan"))
+    s.ctx.fkv_decode_attn(q, s.layer, "lite", i32([0, 0, 0]), out, s.ctx.workspace())
+    assert s.ctx.fkv_get_device_status() == B.FKV_ERR_DEVICE_ARG
+    assert bool((out == 0).all())
+    s.close()
