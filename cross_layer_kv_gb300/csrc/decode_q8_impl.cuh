@@ -25,8 +25,8 @@
 // three to five.  Nothing goes back to shared memory, which is why these are
 // not tcgen05 products: their operands would have to be written there as fp16,
 // twice the bytes that arrive.  332M Lite call (0.27 GB, 40 us at the measured
-// copy rate): 78 us with scalar arithmetic, 50 with these; 4B fused call of
-// full length (2.69 GB, 402 us): 549 us with 16 rows of values' products, 442
+// copy rate): 78 us with scalar arithmetic, 49 with these; 4B fused call of
+// full length (2.69 GB, 402 us): 549 us with 16 rows of values' products, 418
 // with the transposed ones below, which take half the registers and products.
 //
 // Scores: S [16 x 8 keys] = Q [16 x 16 channels] . K^T.  Row g < G of Q is
@@ -37,7 +37,8 @@
 // head g (a score's place in the first product is its weight's place in the
 // second).  With the value scale r in the exponent, P' = p r = 2^(s + log2 r
 // - M), no scale can take P' out of fp16's range (M is the running maximum of
-// that sum, with a slack of 2^8 before O is rescaled); the softmax's sum takes
+// that sum, with a slack of 2^8 before O is rescaled; r below kQ8MinValue takes the
+// rest with P'); the softmax's sum takes
 // P' / r.  P' is rounded to fp16, 2^-12, for bf16 outputs; fp32 contexts add a
 // second product with what the rounding left.  Two value sources have one
 // exponent, of the larger scale, and two P with the factors r_i / r.

@@ -13,7 +13,8 @@
 //     o = sum_t p_t r_t v_t / sum_t p_t,
 //     p_t r_t = 2^(c s_t (q . k_t) + log2 r_t),   c = scale * log2 e,
 // so a key scale multiplies the score and a value scale's logarithm is added
-// to it: the running maximum is that of the sum, and P' = p r, at most
+// to it (down to kQ8MinValue; the rest of a smaller one goes into the tile):
+// the running maximum is that of the sum, and P' = p r, at most
 // 2^(kBias + kSlack) in its frame, is rounded to fp16 (2^-12) whatever the
 // scales are.  The softmax's sum takes p = P' / r.  A row of Q (times its key
 // weights in the scaled mode) is brought to fp16 with a power of two that
@@ -27,8 +28,10 @@
 // with a softmax warpgroup and an MMA-issuing warp that takes turns with the
 // other's; S / P and O live in tensor memory, Q in shared memory.  Two warps
 // bring tiles of codes by cp.async.bulk (a tile's rows are contiguous, in two
-// pieces where a ring wraps, so no ring size is excluded), and a conversion
-// warpgroup writes the fp16 tiles in the swizzled layout that the MMAs read.
+// pieces where a ring wraps, so no ring size is excluded), the issuers bring
+// their group's query rows the same way (read row by row by their threads,
+// they took 10,000 to 20,000 cycles a CTA), and a conversion warpgroup writes
+// the fp16 tiles in the swizzled layout that the MMAs read.
 // Its step k makes V_{k-1} and K_k, what MMA step k reads.  Tiles start at
 // multiples of 32 keys, so that a block of one scale is whole in its tile.
 //
@@ -40,6 +43,13 @@
 // prefix), the key tiles of a CTA's rows are split over a cluster of 2, 4 or 8
 // CTAs, which join their O, maxima and sums through distributed shared memory,
 // each for its share of the rows.
+//
+// What bounds it: each group's chain of softmax (about 1550 cycles for 128 keys
+// of 96 channels), hand-offs (400) and products (1450, in turns with the other
+// group's), at 39% of the tensor pipe's cycles, half of the issue slots and 44%
+// of shared memory's; and about 8 us a CTA before its first scores and after
+// its last products.  650M calls of 8192 rows, 824.7 GFLOP: Lite 891 us (926
+// TFLOP/s), fused 1182 (698); 1.5B: Lite 989 (1112), fused 1562 (704).
 //
 // Every wait is bounded; a wait that runs out sets an abort flag that each
 // role checks, flags the device status, and the CTA frees its tensor memory.
@@ -95,11 +105,15 @@ struct Cfg {
   static constexpr int V_PRODUCER_WARP = MMA_WARP + NG;
   static constexpr int CONV_WARP = SOFTMAX_WARPS + 4;
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 8);
-  // registers: 128 per thread at launch (65536 / 512)
-  static constexpr int REGS_CONTROL = 40, REGS_CONV = NSRC == 2 ? 104 : 72, REGS_SOFTMAX = NSRC == 2 ? 184 : 200;
+  // registers: 128 per thread at launch (65536 / 512); a warpgroup may only give
+  // some up (conversion, control) or take some (softmax).  Two sources: 650M
+  // fused 1190 us with 104 and 184, 1182 with 120 and 176 (88, 192: 1226); one
+  // source: 650M Lite 902 with 72 and 200, 891 with 104 and 184.
+  static constexpr int REGS_CONTROL = 40, REGS_CONV = NSRC == 2 ? 120 : 104, REGS_SOFTMAX = NSRC == 2 ? 176 : 184;
   static constexpr long long REGS_SPLIT =
       (long long)NG * 128 * REGS_SOFTMAX + 128LL * REGS_CONTROL + 128LL * REGS_CONV;
   static_assert(REGS_SPLIT <= (long long)THREADS * 128, "register split above the launch allocation");
+  static_assert(REGS_CONTROL <= 128 && REGS_CONV <= 128 && REGS_SOFTMAX >= 128, "each moves its own way");
 };
 
 struct Params {
@@ -146,6 +160,14 @@ __device__ __forceinline__ bool softmax_and(bool ok) {
       : "r"(ok ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+
+// The 128 threads of softmax warpgroup g meet.
+__device__ __forceinline__ void group_sync(int g) {
+  if (g == 0)
+    asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+  else
+    asm volatile("barrier.cta.sync 4, 128;" ::: "memory");
 }
 
 // All threads of the cluster's CTAs meet (every one of them gets here, since
@@ -224,13 +246,14 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   uint8_t* sV = sK + NS * C::KV_BYTES;
   uint8_t* sRawK = sV + NS * C::KV_BYTES;               // codes, the sources of a slot side by side
   uint8_t* sRawV = sRawK + NR * NSRC * C::RAW_BYTES;
-  float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s, log2 r, 1 / r, rest of r}
+  float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s (times what the weights were divided by), log2 r, 1 / r, rest of r}
   // of K and V: (s0 / s, s1 / s), each as two equal halves
   uint2* sRatio = reinterpret_cast<uint2*>(sScale + NSR * NGRP);
   uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + (NSRC == 2 ? NSR * 2 * NGRP : 0));   // fp16 a0, a1, b0, b1
   uint64_t* bars = reinterpret_cast<uint64_t*>(sW + (NSRC == 2 ? 4 * D : 0));
   uint64_t* q_ready = bars;
-  uint64_t* k_empty = q_ready + 1;        // [NS]
+  uint64_t* q_raw = q_ready + 1;          // [NG]
+  uint64_t* k_empty = q_raw + NG;         // [NS]
   uint64_t* v_empty = k_empty + NS;       // [NS]
   uint64_t* rk_full = v_empty + NS;       // [NR]
   uint64_t* rk_empty = rk_full + NR;
@@ -244,9 +267,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   uint32_t* tmem_slot = words;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 1);
   int* sm_issued = reinterpret_cast<int*>(words + 2);   // [2] tiles each producer issued
-  uint32_t* w_top = words + 4;                          // [2] largest key / value weight (bits)
-  uint32_t* bad = words + 6;       // [1 + 8 + 8] values that are not numbers: seen by all; near the
-                                   // diagonal; near the window's start (bits of positions)
+  uint32_t* w_top = words + 4;     // [4] largest weight of a0, a1, b0, b1 (bits)
+  uint32_t* bad = words + 8;       // [1 + 8 + 8] values that are not numbers: 1: seen by all, 2: some near
+                                   // the diagonal or the window's start; which (bits of positions)
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -290,6 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
 
   if (tid == 0) {
     mbar_init(q_ready, 128 * NG);
+    for (int g = 0; g < NG; ++g) mbar_init(&q_raw[g], 1);
     for (int s = 0; s < NSR; ++s) mbar_init(&step_ready[s], 128);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&k_empty[s], NG);    // one commit per group that reads the tile
@@ -310,7 +334,6 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     }
     *abort_flag = 0;
     sm_issued[0] = sm_issued[1] = 0;
-    w_top[0] = w_top[1] = 0;
     for (int i = 0; i < 17; ++i) bad[i] = 0;
     fence_mbar_init();
   }
@@ -320,23 +343,6 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
-  if constexpr (NSRC == 2) {
-    // the head's weights below 1: one power of two for keys, one for values
-    for (int i = tid; i < 4 * D; i += C::THREADS) {
-      const int v = i / D;
-      const float w = fabsf((v < 2 ? p.a[v] : p.b[v - 2])[kh * D + i % D]);
-      if (w < INFINITY) atomicMax(&w_top[v >> 1], __float_as_uint(w));
-    }
-    __syncthreads();
-    for (int i = tid; i < 4 * D; i += C::THREADS) {
-      const int v = i / D;
-      const float top = __uint_as_float(w_top[v >> 1]);
-      const float w = (v < 2 ? p.a[v] : p.b[v - 2])[kh * D + i % D];
-      const __half h = __float2half_rn(w * power_of_two(-exponent_of(top) - 1));
-      sW[i] = *reinterpret_cast<const uint16_t*>(&h);
-    }
-    __syncthreads();
-  }
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (*abort_flag) return false;
     if (mbar_wait_bounded(bar, parity, wlim)) return true;
@@ -352,6 +358,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     const size_t scols = (size_t)q8_scale_cols(p.rows);
     // Scale records of tile j, one thread per block.
     float ns[2 * NSRC];
+    float k_power = 1.f;   // what the key weights were divided by
     auto load_scales = [&](int j) {
       const int pos = pos0 + j * BN + ft * kQ8Block;
 #pragma unroll
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         rec[ft] = make_uint2(f16x2_of(ns[0] * is, ns[0] * is), f16x2_of(ns[1] * is, ns[1] * is));
         rec[NGRP + ft] = make_uint2(f16x2_of(ns[2] * ir, ns[2] * ir), f16x2_of(ns[3] * ir, ns[3] * ir));
       }
-      sScale[(j % NSR) * NGRP + ft] = make_float4(s, log2f(r), 1.f / r, ns[NSRC] / r);
+      sScale[(j % NSR) * NGRP + ft] = make_float4(s * k_power, log2f(r), 1.f / r, ns[NSRC] / r);
     };
     // A value that is not a number: noted for the rows that see it, 0 in the tile.
     auto note_bad = [&](int pos) {
@@ -384,8 +391,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       if (pos >= S_kv) return;
       const int hi = pos - q0, lo = pos - (q0 - W + 1);
       if (hi <= 0 && (W == 0 || pos > q1 - W))
-        bad[0] = 1;
+        atomicOr(&bad[0], 1u);
       else {
+        atomicOr(&bad[0], 2u);
         if (hi > 0 && hi < NG * BM) atomicOr(&bad[1 + (hi >> 5)], 1u << (hi & 31));
         if (W > 0 && hi <= 0 && lo >= 0 && lo < NG * BM) atomicOr(&bad[9 + (lo >> 5)], 1u << (lo & 31));
       }
@@ -409,17 +417,18 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     const uint32_t raw0 = (uint32_t)(row0 * D + blk0 * 32 + (ft & 1) * 16);
     const uint32_t place0 = (uint32_t)(blk0 * BN * kSW) + swz64(row0, (ft & 1) * 2);
     const uint32_t place80 = (uint32_t)(CP * BN * kSW) + swz64(ft, 0);
-    // item -> row, run in the row, offsets of the codes and of the first chunk (the other: ^ 16)
-    auto item_row = [&](int it) { return it < PAIRED ? row0 + it % KI * RI : ft; };
+    // item it + i, of the same channels as item `it` -> row, run in the row,
+    // offsets of the codes and of the first chunk (the other: ^ 16)
+    auto item_row = [&](int it, int i) { return it < PAIRED ? row0 + (it % KI + i) * RI : ft; };
     auto item_run = [&](int it) {
       return it < PAIRED ? 2 * (blk0 + it / KI * (TWO ? 2 : 1)) + (ft & 1) : CPR - 1;
     };
-    auto item_raw = [&](int it) {
-      return it < PAIRED ? raw0 + (uint32_t)(it % KI * RI * D + it / KI * (TWO ? 64 : 32))
+    auto item_raw = [&](int it, int i) {
+      return it < PAIRED ? raw0 + (uint32_t)((it % KI + i) * RI * D + it / KI * (TWO ? 64 : 32))
                          : (uint32_t)(ft * D + (CPR - 1) * 16);
     };
-    auto item_place = [&](int it) {
-      return it < PAIRED ? place0 + (uint32_t)(it % KI * RI * kSW + it / KI * (TWO ? 2 : 1) * BN * kSW) : place80;
+    auto item_place = [&](int it, int i) {
+      return it < PAIRED ? place0 + (uint32_t)((it % KI + i) * RI * kSW + it / KI * (TWO ? 2 : 1) * BN * kSW) : place80;
     };
     // The head's fp16 weights of both sources for 16 channels.
     struct Weights {
@@ -455,49 +464,50 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xw[e], o[2 * e], o[2 * e + 1]);
       }
     };
-    auto load_item = [&](const uint8_t* raw, int it, int j, bool value, uint4& x, uint4& y, uint2& r) {
-      const int row = item_row(it);
-      x = *reinterpret_cast<const uint4*>(raw + item_raw(it));
+    auto load_item = [&](const uint8_t* raw, int it, int i, int j, bool value, uint4& x, uint4& y, uint2& r) {
+      const int row = item_row(it, i);
+      x = *reinterpret_cast<const uint4*>(raw + item_raw(it, i));
       y = x;
       if constexpr (NSRC == 2) {
-        y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + item_raw(it));
+        y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + item_raw(it, i));
         r = sRatio[((j % NSR) * 2 + (value ? 1 : 0)) * NGRP + row / kQ8Block];
       }
       if (pos0 + j * BN + row >= S_kv) x = y = make_uint4(0, 0, 0, 0);   // behind the last key
     };
-    auto put = [&](uint8_t* dst, int it, const uint32_t* o) {
-      *reinterpret_cast<uint4*>(dst + item_place(it)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + (item_place(it) ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+    auto put = [&](uint8_t* dst, int it, int i, const uint32_t* o) {
+      *reinterpret_cast<uint4*>(dst + item_place(it, i)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + (item_place(it, i) ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
     };
     // Tile j of codes -> fp16 in the swizzled layout; then `empty` is told.
-    // Loads come a batch at a time, ahead of their use.
-    auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, auto is_value, uint64_t* empty) {
-      constexpr bool VALUE = decltype(is_value)::value;
-      constexpr int BATCH = NSRC == 1 ? 4 : 2;
+    // One copy of a short loop for K and V: the softmax warps' code, unrolled
+    // over a tile, and this one share the instruction caches (650M fused: 1310 us
+    // with the tile's items unrolled for K and for V, 1190 so).
+    auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, bool value, uint64_t* empty) {
       uint32_t nan[4] = {0, 0, 0, 0};   // 0, or not a number once a value was none
       Weights w;
+      // N items from `it` on, of the same channels
+      auto items = [&](int it, auto count) {
+        constexpr int N = decltype(count)::value;
+        uint4 x[N], y[N];
+        uint2 r[N];
+        load_weights(it, value, w);
 #pragma unroll
-      for (int i0 = 0; i0 < ITEMS; i0 += BATCH) {
-        uint4 x[BATCH], y[BATCH];
-        uint2 r[BATCH];
+        for (int i = 0; i < N; ++i) load_item(raw, it, i, j, value, x[i], y[i], r[i]);
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-          if (i0 + i < ITEMS) load_item(raw, i0 + i, j, VALUE, x[i], y[i], r[i]);
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int it = i0 + i;
-          if (it >= ITEMS) continue;
-          if (it == 0 || it == PAIRED || it % KI == 0) load_weights(it, VALUE, w);
+        for (int i = 0; i < N; ++i) {
           uint32_t o[8];
           combine(x[i], y[i], r[i], w, o);
-          if constexpr (VALUE) {   // 0 x + nan: no code is infinite
+          if (value) {   // 0 x + nan: no code is infinite
 #pragma unroll
             for (int e = 0; e < 8; ++e) nan[e & 3] = hfma2u(o[e], 0u, nan[e & 3]);
           }
-          put(dst, it, o);
+          put(dst, it, i, o);
         }
-      }
-      if constexpr (VALUE) {
+      };
+#pragma unroll 1
+      for (int it = 0; it < PAIRED; it += KI) items(it, std::integral_constant<int, KI>{});
+      if constexpr (ITEMS > PAIRED) items(PAIRED, std::integral_constant<int, 1>{});
+      if (value) {
         // the rest of one source's scale, where the exponents do not take it whole
         [[maybe_unused]] const float4* rec = sScale + (j % NSR) * NGRP;
         bool whole = true;
@@ -512,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
             uint4 x, y;
             uint2 r;
             uint32_t any = 0, o[8];
-            load_item(raw, it, j, true, x, y, r);
+            load_item(raw, it, 0, j, true, x, y, r);
             uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -520,16 +530,16 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
               xw[e] &= ~((nan_codes(xw[e]) >> 7) * 255u);
               yw[e] &= ~((nan_codes(yw[e]) >> 7) * 255u);
             }
-            if (any) note_bad(pos0 + j * BN + item_row(it));
+            if (any) note_bad(pos0 + j * BN + item_row(it, 0));
             if (!any && whole) continue;
             load_weights(it, true, w);
             combine(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(yw[0], yw[1], yw[2], yw[3]), r, w, o);
             if constexpr (NSRC == 1) {
-              const float rest = rec[item_row(it) / kQ8Block].w;
+              const float rest = rec[item_row(it, 0) / kQ8Block].w;
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] = hmul2u(o[e], f16x2_of(rest, rest));
             }
-            put(dst, it, o);
+            put(dst, it, 0, o);
           }
         }
       }
@@ -537,6 +547,30 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       // used yet, and the slot's next copy would overtake them)
       mbar_arrive(empty);
     };
+    if constexpr (NSRC == 2) {
+      // the head's weights below 1: one power of two for keys, one for values
+      const int v = ft / 32;   // a warp's vector
+      const float* src = (v == 0 ? p.a[0] : v == 1 ? p.a[1] : v == 2 ? p.b[0] : p.b[1]) + kh * D;
+      float x[(D + 31) / 32];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < (D + 31) / 32; ++i) {
+        x[i] = lane + 32 * i < D ? src[lane + 32 * i] : 0.f;
+        const uint32_t u = __float_as_uint(fabsf(x[i]));
+        if (u < 0x7f800000u) top = max(top, u);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) w_top[v] = top;
+      (void)group_and(true);
+      const float f = power_of_two(-exponent_of(__uint_as_float(max(w_top[v & 2], w_top[v | 1]))) - 1);
+      k_power = power_of_two(exponent_of(__uint_as_float(max(w_top[0], w_top[1]))) + 1);
+#pragma unroll
+      for (int i = 0; i < (D + 31) / 32; ++i)
+        if (lane + 32 * i < D) {
+          const __half h = __float2half_rn(x[i] * f);
+          sW[v * D + lane + 32 * i] = *reinterpret_cast<const uint16_t*>(&h);
+        }
+    }
     load_scales(0);
     store_scales(0);
     (void)group_and(true);
@@ -557,15 +591,16 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         return __all_sync(0xffffffffu, ok) && __all_sync(0xffffffffu, look());
       };
       bool ok = true;
-      if (k > 0) {
-        ok = ready(&rv_full[t % NR], (uint32_t)(t / NR) & 1u, &v_empty[t % NS], (uint32_t)(t / NS - 1) & 1u, t >= NS);
+#pragma unroll 1
+      for (int which = k > 0 ? 0 : 1; ok && which < (k < n_max ? 2 : 1); ++which) {
+        const bool value = which == 0;
+        const int c = value ? t : k;   // the tile
+        uint64_t *full = value ? rv_full : rk_full, *empty = value ? rv_empty : rk_empty;
+        ok = ready(&full[c % NR], (uint32_t)(c / NR) & 1u, &(value ? v_empty : k_empty)[c % NS],
+                   (uint32_t)(c / NS - 1) & 1u, c >= NS);
         if (ok)
-          convert(tile_v(t), sRawV + (size_t)(t % NR) * NSRC * C::RAW_BYTES, t, std::true_type{}, &rv_empty[t % NR]);
-      }
-      if (ok && k < n_max) {
-        ok = ready(&rk_full[k % NR], (uint32_t)(k / NR) & 1u, &k_empty[k % NS], (uint32_t)(k / NS - 1) & 1u, k >= NS);
-        if (ok)
-          convert(tile_k(k), sRawK + (size_t)(k % NR) * NSRC * C::RAW_BYTES, k, std::false_type{}, &rk_empty[k % NR]);
+          convert(value ? tile_v(c) : tile_k(c), (value ? sRawV : sRawK) + (size_t)(c % NR) * NSRC * C::RAW_BYTES, c, value,
+                  &empty[c % NR]);
       }
       if (ok) {
         store_scales(k + 1);
@@ -585,8 +620,8 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     if ((warp == C::K_PRODUCER_WARP || warp == C::V_PRODUCER_WARP) && lane == 0) {
       // ---------------- producers: K codes, V codes ----------------
       const bool is_k = warp == C::K_PRODUCER_WARP;
-      uint64_t* full = is_k ? rk_full : rv_full;
       uint64_t* empty = is_k ? rk_empty : rv_empty;
+      uint64_t* full = is_k ? rk_full : rv_full;
       uint8_t* ring = is_k ? sRawK : sRawV;
       uint64_t policy;   // the CTAs of a unit read the same tiles
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
@@ -616,6 +651,15 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       constexpr uint32_t IDESC_PV = idesc_with_f16(idesc_bf16(BM, D, true));
       const uint32_t t_g = tmem + g * GROUP_COLS;
       const uint32_t qbase = smem_u32(sQ + g * C::Q_BYTES);
+      {
+        // the group's query rows, as they are, where they will be as fp16
+        const int rows = max(0, min(BM, p.S - g_row0(g)));
+        mbar_arrive_expect_tx(&q_raw[g], (uint32_t)rows * D * 2);
+        if (rows > 0)
+          bulk_g2s(sQ + g * C::Q_BYTES,
+                   static_cast<const __nv_bfloat16*>(p.q) + (((size_t)b * H_q + g_head(g)) * p.S + g_row0(g)) * D,
+                   (uint32_t)rows * D * 2, &q_raw[g], l2_policy_evict_first());
+      }
       // S_g = Q_g K_j^T: M = 128 rows, N = BN keys, K = D in steps of 16
       auto issue_qk = [&](int j) {
         const uint32_t kbase = smem_u32(tile_k(j));
@@ -699,50 +743,64 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     const bool row_valid = m_row < p.S;
     const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + g * GROUP_COLS;
     const uint32_t t_o = t_s + C::O_COL;
-    float c_row;   // what a raw score times its key scale is multiplied by
+    float c_row = 0.f;   // what a raw score times its key scale is multiplied by
+    bool ok = __all_sync(0xffffffffu, wait(&q_raw[g], 0));
     {
       // this thread's Q row (times its key weights where one source has some)
-      // into shared memory as fp16, its largest element in [2^14, 2^15); rows
-      // beyond the chunk are zero
-      const uint4* qrow = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(p.q) + (((size_t)b * H_q + g_head(g)) * p.S + m_row) * D);
-      const float* wa = NSRC == 1 && p.a[0] ? p.a[0] + (size_t)kh * D : nullptr;
-      auto chunk = [&](int i, float* f) {
-        unpack16<__nv_bfloat16>(row_valid ? qrow[i] : make_uint4(0, 0, 0, 0), f);
-        if (wa) {
+      // to fp16, its largest element in [2^14, 2^15), in the place of the
+      // group's rows as they came; rows beyond the chunk are zero.  Neighbours
+      // read from chunks of 8 channels next to each other, whatever a row's
+      // length, so that they meet in few banks.
+      constexpr int N = D / 8;
+      uint8_t* qg = sQ + g * C::Q_BYTES;
+      auto place = [&](int i) {   // the i-th chunk that this thread takes
+        const int c = row % N + i;
+        return c < N ? c : c - N;
+      };
+      uint4 raw[N];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= wa[i * 8 + e];
+      for (int i = 0; i < N; ++i)
+        raw[i] = ok && row_valid ? *reinterpret_cast<const uint4*>(qg + row * D * 2 + place(i) * 16) : make_uint4(0, 0, 0, 0);
+      auto fill = [&](auto weighted) {
+        auto chunk = [&](int i, float* f) {
+          unpack16<__nv_bfloat16>(raw[i], f);
+          if constexpr (decltype(weighted)::value) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= p.a[0][(size_t)kh * D + place(i) * 8 + e];
+          }
+        };
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float f[8];
+          chunk(i, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+        }
+        const int eq = top > 0.f && top < INFINITY ? 14 - exponent_of(top) : 0;
+        // two factors, since 2^eq alone may lie outside the normal range
+        const float f0 = power_of_two(eq / 2), f1 = power_of_two(eq - eq / 2);
+        c_row = p.scale_log2 / f0 / f1;
+        group_sync(g);   // all rows are read
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float f[8];
+          chunk(i, f);
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = f16x2_of(f[2 * e] * f0 * f1, f[2 * e + 1] * f0 * f1);
+          const int c = place(i);
+          *reinterpret_cast<uint4*>(qg + (c >> 2) * BM * kSW + swz64(row, c & 3)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       };
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        float f[8];
-        chunk(i, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-      }
-      const int eq = top > 0.f && top < INFINITY ? 14 - exponent_of(top) : 0;
-      // two factors, since 2^eq alone may lie outside the normal range
-      const float f0 = power_of_two(eq / 2), f1 = power_of_two(eq - eq / 2);
-      c_row = p.scale_log2 / f0 / f1;
-      uint8_t* qg = sQ + g * C::Q_BYTES;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        float f[8];
-        chunk(i, f);
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = f16x2_of(f[2 * e] * f0 * f1, f[2 * e + 1] * f0 * f1);
-        *reinterpret_cast<uint4*>(qg + (i >> 2) * BM * kSW + swz64(row, i & 3)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+      if (NSRC == 1 && p.a[0])
+        fill(std::true_type{});
+      else
+        fill(std::false_type{});
       fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
-    if constexpr (NSRC == 2)   // the head's power of two of the key weights
-      c_row *= power_of_two(exponent_of(__uint_as_float(w_top[0])) + 1);
     float m_run = -FLT_MAX, l_run = 0.f;
-    bool ok = true;
     for (int j = 0; ok && j < ng; ++j) {
       const int n0 = pos0 + j * BN;
       // waits are made warp-uniform: tcgen05.ld/st below are warp-collective
@@ -859,9 +917,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     if (ok) {
       tc_fence_after();
       // values that are not numbers among the keys that this row sees
-      bool nan = bad[0] != 0;
+      const uint32_t noted = *const_cast<volatile uint32_t*>(&bad[0]);
+      bool nan = (noted & 1u) != 0;
       const int q0 = pos_first, lo0 = q0 - W + 1;
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8 && (noted & 2u); ++i) {
         uint32_t x = *const_cast<volatile uint32_t*>(&bad[1 + i]);
         while (x) {
           const int pos = q0 + i * 32 + __ffs((int)x) - 1;
@@ -877,7 +936,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       }
       if (nan) l_run = __uint_as_float(0x7fffffffu);
     }
-    const float out_scale = NSRC == 2 ? power_of_two(exponent_of(__uint_as_float(w_top[1])) + 1) : 1.f;
+    const float out_scale = NSRC == 2 ? power_of_two(exponent_of(__uint_as_float(max(w_top[2], w_top[3]))) + 1) : 1.f;
     const float* wb = NSRC == 1 && p.b[0] && p.a[0] ? p.b[0] + (size_t)kh * D : nullptr;
     if (!SPLIT && ok) {
       const float inv = out_scale / l_run;
@@ -928,38 +987,66 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       bool stop = false;   // a CTA of the cluster gave up
       for (int k = 0; k < splits; ++k)
         stop = stop || __float_as_int(ld_cluster(smem_u32(const_cast<int*>(abort_flag)), k)) != 0;
-      if (!stop) {
-        // this CTA's share of the rows, `splits` threads a row
-        const int share = ROWS / splits, mine = rank * share + r % share, piece = r / share;
-        const int og = mine / BM, orow = g_row0(og) + mine % BM, width = D / splits;
+      // this CTA's share of the rows, SP threads a row: the channels of several
+      // loads at once, since each is a trip to another SM
+      auto join = [&](auto parts) {
+        constexpr int SP = decltype(parts)::value, WIDTH = D / SP;
+        constexpr int CH = WIDTH % 16 == 0 && SP == 2 ? 16 : WIDTH % 8 == 0 && SP <= 4 ? 8 : WIDTH % 4 == 0 ? 4 : 2;
+        static_assert(WIDTH % CH == 0, "whole batches of channels");
+        constexpr int SHARE = ROWS / SP;
+        const int mine = rank * SHARE + r % SHARE, piece = r / SHARE;
+        const int og = mine / BM, orow = g_row0(og) + mine % BM;
+        if (orow >= p.S) return;
         const uint32_t at = smem_u32(part) + mine * 4;
-        float top = -FLT_MAX, sum = 0.f, w[8];
+        float top = -FLT_MAX, sum = 0.f, w[SP], l[SP];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          w[k] = k < splits ? ld_cluster(at + D * ROWS * 4, k) : -FLT_MAX;
-          top = fmaxf(top, w[k]);
+        for (int k = 0; k < SP; ++k) {
+          w[k] = ld_cluster(at + D * ROWS * 4, k);
+          l[k] = ld_cluster(at + (D + 1) * ROWS * 4, k);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          w[k] = k < splits ? fast_exp2(w[k] - top) : 0.f;
-          if (k < splits) sum = fmaf(w[k], ld_cluster(at + (D + 1) * ROWS * 4, k), sum);
+        for (int k = 0; k < SP; ++k) top = fmaxf(top, w[k]);
+#pragma unroll
+        for (int k = 0; k < SP; ++k) {
+          w[k] = fast_exp2(w[k] - top);
+          sum = fmaf(w[k], l[k], sum);
         }
         const float inv = out_scale / sum;
-        if (orow < p.S) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                               (((size_t)b * H_q + g_head(og)) * p.S + orow) * D;
-          for (int d = piece * width; d < (piece + 1) * width; d += 2) {
-            float x = 0.f, y = 0.f;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (((size_t)b * H_q + g_head(og)) * p.S + orow) * D;
+#pragma unroll 1
+        for (int d = piece * WIDTH; d < (piece + 1) * WIDTH; d += CH) {
+          float x[CH][SP];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < splits) {
-                x = fmaf(w[k], ld_cluster(at + d * ROWS * 4, k), x);
-                y = fmaf(w[k], ld_cluster(at + (d + 1) * ROWS * 4, k), y);
-              }
-            if (wb) x *= wb[d], y *= wb[d + 1];
-            *reinterpret_cast<__nv_bfloat162*>(dst + d) = __floats2bfloat162_rn(x * inv, y * inv);
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int k = 0; k < SP; ++k) x[c][k] = ld_cluster(at + (d + c) * ROWS * 4, k);
+          uint32_t o[CH / 2];
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            float y[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < SP; ++k) {
+              y[0] = fmaf(w[k], x[c][k], y[0]);
+              y[1] = fmaf(w[k], x[c + 1][k], y[1]);
+            }
+            if (wb) y[0] *= wb[d + c], y[1] *= wb[d + c + 1];
+            const __nv_bfloat162 v2 = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
+            o[c / 2] = *reinterpret_cast<const uint32_t*>(&v2);
+          }
+          if constexpr (CH >= 8) {
+#pragma unroll
+            for (int c = 0; c < CH / 8; ++c)
+              reinterpret_cast<uint4*>(dst + d)[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < CH / 2; ++c) reinterpret_cast<uint32_t*>(dst + d)[c] = o[c];
           }
         }
+      };
+      if (!stop) {
+        if (splits == 2) join(std::integral_constant<int, 2>{});
+        else if (splits == 4) join(std::integral_constant<int, 4>{});
+        else join(std::integral_constant<int, 8>{});
       }
       cluster_sync();
     }
@@ -981,6 +1068,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         (void)mbar_wait_bounded(&(is_k ? rk_full : rv_full)[j % NR], (uint32_t)(j / NR) & 1u, kDrainLimitNs);
     }
     if (warp >= C::MMA_WARP && warp < C::MMA_WARP + NG && lane == 0) {
+      (void)mbar_wait_bounded(&q_raw[warp - C::MMA_WARP], 0, kDrainLimitNs);
       mma_commit(&mma_drain[warp - C::MMA_WARP]);
       (void)mbar_wait_bounded(&mma_drain[warp - C::MMA_WARP], 0, kDrainLimitNs);
     }
