@@ -486,10 +486,13 @@ struct Q8Walker {
   }
 };
 
-// Sequences of up to this many groups of 16 rows are short: a CTA takes whole
-// units then, since a merge through global memory (3 us) costs more than an
-// uneven split.
-constexpr int kQ8ShortGroups = 48;
+// A CTA takes whole units where the busiest one then has at most these codes
+// (bytes) more than an equal share: a merge through global memory costs 4 us,
+// about what they take.  At 96 channels, one source, 75 groups of 16 rows, in
+// us whole and split: 128 units of 1000 rows 10.4 and 15.9, of 4000 24.2 and
+// 27.2, of 8000 (75 groups more) 40.7 and 40.9; 32 of 1500 11.9 and 13.3, of
+// 2000 (99 more) 14.6 and 14.2; 160 of 2000 (118 more) 24.4 and 22.1.
+constexpr int kQ8Uneven = 230400;
 
 template <typename T, int D, int NSRC>
 __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(const Q8Params prm) {
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     }
   }
   // The CTA's groups [c0, c1): an equal share of all, or whole units where
-  // these are short; and the warp's share of them.
+  // these come to little more; and the warp's share of them.
   const unsigned total = (unsigned)H * run;
   const Q8Split split(total, prm.by_ctas);
   auto unit_start = [&](unsigned u) {
@@ -588,8 +591,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     return b < (unsigned)p.B ? (unsigned)H * pre[b] + (u - b * H) * (pre[b + 1] - pre[b]) : total;
   };
   unsigned c0, c1;
-  if (longest <= kQ8ShortGroups) {
-    const Q8Split units((unsigned)p.B * H, prm.by_ctas);
+  const Q8Split units((unsigned)p.B * H, prm.by_ctas);
+  if ((units.each + (units.rest > 0 ? 1 : 0)) * longest <= split.each + kQ8Uneven / (16 * 2 * NSRC * D)) {
     c0 = unit_start(units.start(blockIdx.x));
     c1 = unit_start(units.start(blockIdx.x + 1));
   } else {
