@@ -208,9 +208,9 @@ fkv_status fkv_set_window(fkv_ctx* ctx, int layer, int window);
  * position t of a sequence lives at row t % rows, so a sliding-window layer
  * stores only the positions its window can reach instead of S_max rows (the
  * capacity half of the hybrid sliding-window sharing of the FusedKV slides,
- * "MoE and hybrid SWA").  The buffers bound to the layer (fkv_bind_layer_cache
- * or fkv_bind_layer_cache_q4, before or after this call) are then
- * [B, H_kv, rows, D] (or rows records).  rows = 0 (or S_max) restores the
+ * "MoE and hybrid SWA").  The buffers bound to the layer (fkv_bind_layer_cache,
+ * _q4 or _q8, before or after this call) are then [B, H_kv, rows, D] (or rows
+ * records, or codes and fkv_q8_scale_cols(rows) scales).  rows = 0 (or S_max) restores the
  * full-length layout; FKV_ERR_INVALID_ARG for a bad layer or rows outside
  * [0, S_max].
  * Calls over ring caches:
