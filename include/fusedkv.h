@@ -262,7 +262,9 @@ fkv_status fkv_read_kv(fkv_ctx* ctx, int layer, int mode, const int32_t* pos, in
 
 /* Bytes of device workspace fkv_decode_attn needs for this context (split-K
  * partial results).  The caller allocates it; its contents need no
- * initialisation and may be reused by every decode call on the same stream. */
+ * initialisation and may be reused by every decode call on the same stream.
+ * Ask once the caches are bound: 8-bit ones may need more (a call with too
+ * little is FKV_ERR_WORKSPACE). */
 size_t fkv_decode_workspace_bytes(const fkv_ctx* ctx);
 
 /* One decode attention call of a layer (a single query position per sequence).
