@@ -283,7 +283,10 @@ size_t fkv_decode_workspace_bytes(const fkv_ctx* ctx);
  * FKV_ERR_DEVICE_ARG in the device status.
  * Rounding: fp32 throughout; over 8-bit caches queries times key weights keep
  * 22 bits, and bf16 contexts round each probability to fp16 for its product
- * with the values.
+ * with the values (two sources whose value scales' ratio is no power of two:
+ * for each source by itself); a probability whose product with its value scale
+ * is below 2^-31 of the largest may count as 0 there (the softmax's sum takes
+ * it).
  * mode: for storage layers every mode is plain attention over the layer's own
  * cache; for upper layers FKV_VANILLA reads the layer's own cache (needs
  * store_upper), FKV_LITE reads K^n and V^1, FKV_FUSED reads K^1, K^n, V^1, V^n

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from cross_layer_kv_gb300 import fusedkv as B
-from q8_parity import Setup, check_decode, check_prefill
+from q8_parity import Setup, attend, check_decode, check_prefill, decode_bound, reconstruct, values
 
 pytestmark = pytest.mark.gpu
 
@@ -250,4 +250,36 @@ def test_decode_of_no_rows_at_all():
     s.ctx.fkv_decode_attn(q, s.layer, "lite", i32([0, 0, 0]), out, s.ctx.workspace())
     assert s.ctx.fkv_get_device_status() == B.FKV_ERR_DEVICE_ARG
     assert bool((out == 0).all())
+    s.close()
+
+
+@pytest.mark.parametrize("mode,D,window,ring", [("fused", 80, 0, 0), ("fused", 128, 300, 352), ("scaled", 96, 0, 0),
+                                                ("vanilla", 64, 500, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_any_scales_and_steep_scores(mode, D, window, ring, dtype):
+    """Scales that are no powers of two, up to 2^18 apart, and scores of hundreds.  Two sources
+    round P each for itself then, so a rounding is relative to the sums of both sources' magnitudes
+    (of scores and of values), which may cancel; and what falls below 2^-31 of the largest weight
+    times value scale may vanish: at most 2^-31 of the largest value for each of n keys."""
+    s = Setup(mode, 3, 1500, 2, 2, D, dtype=dtype, window=window, ring=ring, seed=18, spread=3.0, powers=False,
+              softmax_scale=0.5)
+    lens = [1500, 700, 33]
+    q = s.query(3, 4, D)
+    out = torch.full_like(q, float("nan"))
+    s.ctx.fkv_decode_attn(q, s.layer, mode, i32(lens), out, s.ctx.workspace())
+    assert s.ctx.fkv_get_device_status() == B.FKV_OK
+    K, V = s.rows()
+    Ka, Va = reconstruct(mode, [x.abs() for x in s.w], [values(x).abs() for x in s.k], [values(x).abs() for x in s.v])
+    for b, L in enumerate(lens):
+        pos = torch.arange(max(0, L - window) if window else 0, L, device="cuda")
+        at = pos % ring if ring else pos
+        for h in range(2):
+            qq = q[b, 2 * h:2 * h + 2].double()
+            see = torch.ones(2, len(pos), dtype=torch.bool, device="cuda")
+            ref, _, _ = attend(qq, K[b, h, at], V[b, h, at], s.scale, see)
+            p = torch.softmax(qq @ K[b, h, at].T * s.scale, -1)
+            size = (qq.abs() @ Ka[b, h, at].T * s.scale).amax(-1, keepdim=True)
+            bound = decode_bound(ref, size, p @ Va[b, h, at], D, len(pos), dtype)
+            bound = bound + len(pos) * 2.0 ** -31 * Va[b, h, at].max()
+            assert bool(((out[b, 2 * h:2 * h + 2].double() - ref).abs() <= bound).all()), (b, h)
     s.close()
