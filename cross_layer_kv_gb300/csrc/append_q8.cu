@@ -6,8 +6,8 @@
 // the block's scale becomes s = need where its first row is new, and
 // max(s, need) where rows before the new ones keep their places in it.  New
 // rows store e4m3(x / s), not finite elements the NaN code; where s grew, the
-// rows before the new ones store e4m3(code * s_old / s).  Rows of the block
-// behind the new ones are free.
+// rows before the new ones store e4m3(code * s_old / s) (zeros, where s_old is
+// 0).  Rows of the block behind the new ones are free.
 //
 // One warp per block; a lane holds up to D/8 runs of 8 channels in registers
 // between the maximum and the codes, so the new rows are read once; a load of
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(AppendArgs a, in
     }
     top = __reduce_max_sync(0xffffffffu, top);
     const float need = scale_for(__uint_as_float(top));
-    const bool had = s_old > 0.f && s_old < INFINITY;
+    const bool had = s_old >= 0.f && s_old < INFINITY;   // (0: the rows before are zeros, whatever their codes)
     const float s = had && s_old > need ? s_old : need;
     // dividing by a power of two is multiplying by its reciprocal
     const bool power = (__float_as_uint(s) & 0x7fffffu) == 0 && s > 0x1p-120f && s < 0x1p+120f;
