@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   // (down to the start of its block) to each group's last position
   const int pos_first = p.q_start + g_row0(0);
   const int start = W > 0 ? max(0, pos_first - W + 1) / kQ8Block * kQ8Block : 0;
-  auto all_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) - start + BN - 1) / BN; };
+  // (positions end at 2^31 - 1: no sum below goes past the chunk's last)
+  auto g_end = [&](int g) { return p.q_start + min(g_row0(g) + BM, p.S); };   // behind its last position
+  auto all_tiles = [&](int g) { return (int)(((unsigned)(g_end(g) - start) + BN - 1) / BN); };
   // of which the CTA takes [jb, je) (all of them but in a cluster), group 1 all
   // and group 0 those up to its own last position, one at least (a tile that is
   // masked for all its rows, if need be); a CTA with none (idle: the first query
@@ -360,10 +362,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     float ns[2 * NSRC];
     float k_power = 1.f;   // what the key weights were divided by
     auto load_scales = [&](int j) {
-      const int pos = pos0 + j * BN + ft * kQ8Block;
 #pragma unroll
       for (int i = 0; i < 2 * NSRC; ++i) ns[i] = 1.f;   // (blocks behind the last key: any finite one)
-      if (ft < NGRP && j < n_max && pos < S_kv) {
+      if (ft < NGRP && j < n_max && ft * kQ8Block < S_kv - (pos0 + j * BN)) {
+        const int pos = pos0 + j * BN + ft * kQ8Block;
         const size_t at = (size_t)unit * scols + (p.ring > 0 ? pos % p.ring : pos) / kQ8Block;
 #pragma unroll
         for (int i = 0; i < NSRC; ++i) {
@@ -386,10 +388,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       sScale[(j % NSR) * NGRP + ft] = make_float4(s * k_power, log2f(r), 1.f / r, ns[NSRC] / r);
     };
     // A value that is not a number: noted for the rows that see it, 0 in the tile.
-    auto note_bad = [&](int pos) {
-      const int q0 = pos_first, q1 = min(p.q_start + g_row0(NG - 1) + BM, S_kv) - 1;   // the CTA's query positions
-      if (pos >= S_kv) return;
-      const int hi = pos - q0, lo = pos - (q0 - W + 1);
+    auto note_bad = [&](int n0, int row) {
+      const int q0 = pos_first, q1 = g_end(NG - 1) - 1;   // the CTA's query positions
+      if (row >= S_kv - n0) return;
+      const int pos = n0 + row, hi = pos - q0, lo = hi <= 0 ? hi + (W - 1) : 0;
       if (hi <= 0 && (W == 0 || pos > q1 - W))
         atomicOr(&bad[0], 1u);
       else {
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xw[e], o[2 * e], o[2 * e + 1]);
       }
     };
-    auto load_item = [&](const uint8_t* raw, int it, int i, int j, bool value, uint4& x, uint4& y, uint2& r) {
+    auto load_item = [&](const uint8_t* raw, int it, int i, int j, int left, bool value, uint4& x, uint4& y, uint2& r) {
       const int row = item_row(it, i);
       x = *reinterpret_cast<const uint4*>(raw + item_raw(it, i));
       y = x;
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         y = *reinterpret_cast<const uint4*>(raw + C::RAW_BYTES + item_raw(it, i));
         r = sRatio[((j % NSR) * 2 + (value ? 1 : 0)) * NGRP + row / kQ8Block];
       }
-      if (pos0 + j * BN + row >= S_kv) x = y = make_uint4(0, 0, 0, 0);   // behind the last key
+      if (row >= left) x = y = make_uint4(0, 0, 0, 0);   // behind the last key
     };
     auto put = [&](uint8_t* dst, int it, int i, const uint32_t* o) {
       *reinterpret_cast<uint4*>(dst + item_place(it, i)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     // over a tile, and this one share the instruction caches (650M fused: 1310 us
     // with the tile's items unrolled for K and for V, 1190 so).
     auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, bool value, uint64_t* empty) {
+      const int left = S_kv - (pos0 + j * BN);   // keys from the tile's first on
       uint32_t nan[4] = {0, 0, 0, 0};   // 0, or not a number once a value was none
       Weights w;
       // N items from `it` on, of the same channels
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         uint2 r[N];
         load_weights(it, value, w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) load_item(raw, it, i, j, value, x[i], y[i], r[i]);
+        for (int i = 0; i < N; ++i) load_item(raw, it, i, j, left, value, x[i], y[i], r[i]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           uint32_t o[8];
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
             uint4 x, y;
             uint2 r;
             uint32_t any = 0, o[8];
-            load_item(raw, it, 0, j, true, x, y, r);
+            load_item(raw, it, 0, j, left, true, x, y, r);
             uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
               xw[e] &= ~((nan_codes(xw[e]) >> 7) * 255u);
               yw[e] &= ~((nan_codes(yw[e]) >> 7) * 255u);
             }
-            if (any) note_bad(pos0 + j * BN + item_row(it, 0));
+            if (any) note_bad(pos0 + j * BN, item_row(it, 0));
             if (!any && whole) continue;
             load_weights(it, true, w);
             combine(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(yw[0], yw[1], yw[2], yw[3]), r, w, o);
@@ -737,8 +740,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int m_row = g_row0(g) + row;       // query row within the chunk
-    const int qpos = p.q_start + m_row;      // its cache position
-    const int pos_g = p.q_start + g_row0(g);
+    const int qpos = p.q_start + min(m_row, p.S - 1);   // its cache position (behind the chunk: the last one)
+    // tiles that start in [full_from, full_to] are seen whole by all of the group's rows
+    const int pos_g = p.q_start + min(g_row0(g), p.S - 1);
+    const int full_to = pos_g - BN, full_from = W == 0 ? 0 : W <= BM ? INT_MAX : pos_g - (W - BM);
     const int ng = n_tiles(g);
     const bool row_valid = m_row < p.S;
     const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + g * GROUP_COLS;
@@ -828,10 +833,10 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       // lowest row-window start of the tile (warp-uniform).  It is done where
       // the scores lie, so that the usual tile's registers are not merged with
       // a masked tile's (128 moves a thread).
-      if (n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W) || idle) {
+      if (n0 > full_to || n0 < full_from || idle) {
         // visible keys of this row, as tile columns: lo <= c < hi
-        const int hi = idle ? 0 : min(qpos + 1, S_kv) - n0;
-        const int lo = W > 0 ? qpos - W + 1 - n0 : INT_MIN;
+        const int hi = idle ? 0 : qpos - n0 + 1;
+        const int lo = W > 0 ? max(qpos - n0, -1) - W + 1 : INT_MIN;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
           float x[32];
