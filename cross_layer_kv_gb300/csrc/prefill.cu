@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(PrefillPlan<D, NSRC, G>::THREADS, 1)
   // key tiles [j0, j_end): up to the last query's position, from the first
   // query's window start (sliding-window layers skip the tiles before it)
   const int j0 = W > 0 ? max(0, pos0 - W + 1) / BN : 0;
-  const int ntiles = (min(pos0 + BM, S_kv) + BN - 1) / BN - j0;   // tiles processed
+  // tiles processed (positions end at 2^31 - 1: no sum goes past the chunk's last)
+  const int ntiles = (int)(((unsigned)(p.q_start + min(m0 + BM, S)) + BN - 1) / BN) - j0;
   const int H_q = p.H_kv * G;
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
 
@@ -404,7 +405,9 @@ __global__ void __launch_bounds__(PrefillPlan<D, NSRC, G>::THREADS, 1)
     const int hh = warp >> 2;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int qpos = pos0 + row;         // cache position of this query
+    const int qpos = p.q_start + min(m0 + row, S - 1);   // cache position of this query (behind the chunk: the last one)
+    // tiles that start in [full_from, full_to] are seen whole by all of the tile's rows
+    const int full_to = pos0 - BN, full_from = W == 0 ? 0 : W <= BM ? INT_MAX : pos0 - (W - BM);
     const bool row_valid = m0 + row < S;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_head = tmem + lane_addr + hh * HEAD_COLS;
@@ -425,14 +428,14 @@ __global__ void __launch_bounds__(PrefillPlan<D, NSRC, G>::THREADS, 1)
       tmem_wait_ld();
       // masking needed: the causal diagonal, the key extent, or (window) the
       // lowest row-window start of the tile (warp-uniform)
-      const bool diag = n0 + BN > pos0 || n0 + BN > S_kv || (W > 0 && n0 < pos0 + BM - W);
+      const bool diag = n0 > full_to || n0 < full_from;
       if (diag) {
-        const int lo = W > 0 ? qpos - W + 1 : INT_MIN;
+        // visible keys of this row, as tile columns: lo <= c < hi
+        const int hi = qpos - n0 + 1;
+        const int lo = W > 0 ? max(qpos - n0, -1) - W + 1 : INT_MIN;
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
-          const int kp = n0 + c;
-          if (kp > qpos || kp >= S_kv || kp < lo) sv[c] = -INFINITY;
-        }
+        for (int c = 0; c < BN; ++c)
+          if (c >= hi || c < lo) sv[c] = -INFINITY;
       }
       // row max of the raw scores (the scale is positive, so it commutes)
       float mx0 = sv[0], mx1 = sv[1], mx2 = sv[2], mx3 = sv[3];

@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   // group's last query position
   const int pos_first = p.q_start + g_row0(0);
   const int j0 = W > 0 ? max(0, pos_first - W + 1) / BN : 0;
-  auto n_tiles = [&](int g) { return (min(p.q_start + g_row0(g) + BM, S_kv) + BN - 1) / BN - j0; };
+  // (positions end at 2^31 - 1: no sum goes past the chunk's last)
+  auto n_tiles = [&](int g) {
+    return (int)(((unsigned)(p.q_start + min(g_row0(g) + BM, p.S)) + BN - 1) / BN) - j0;
+  };
   const int n_max = max(n_tiles(0), n_tiles(1));
   const bool scaled = p.a != nullptr;
   const unsigned long long wlim = wait_limit_ns(p.wait_limit);
@@ -293,8 +296,10 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int m_row = g_row0(g) + row;       // query row within the chunk
-    const int qpos = p.q_start + m_row;      // its cache position
-    const int pos_g = p.q_start + g_row0(g);
+    const int qpos = p.q_start + min(m_row, p.S - 1);   // its cache position (behind the chunk: the last one)
+    // tiles that start in [full_from, full_to] are seen whole by all of the group's rows
+    const int pos_g = p.q_start + min(g_row0(g), p.S - 1);
+    const int full_to = pos_g - BN, full_from = W == 0 ? 0 : W <= BM ? INT_MAX : pos_g - (W - BM);
     const int ng = n_tiles(g);
     const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + g * GROUP_COLS;
     const uint32_t t_o = t_s + BN;
@@ -339,11 +344,11 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       tmem_wait_ld();
       // masking needed: the causal diagonal, the key extent, or (window) the
       // lowest row-window start of the tile (warp-uniform)
-      const bool diag = n0 + BN > pos_g || n0 + BN > S_kv || (W > 0 && n0 < pos_g + BM - W);
+      const bool diag = n0 > full_to || n0 < full_from;
       if (diag) {
         // visible keys of this row, as tile columns: lo <= c < hi
-        const int hi = min(qpos + 1, S_kv) - n0;
-        const int lo = W > 0 ? qpos - W + 1 - n0 : INT_MIN;
+        const int hi = qpos - n0 + 1;
+        const int lo = W > 0 ? max(qpos - n0, -1) - W + 1 : INT_MIN;
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (c >= hi || c < lo) sv[c] = -INFINITY;
