@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       }
       int f, rows;
       attended(L, f, rows);
-      x = rows > 0 ? (f % 16 + rows + 15) / 16 : 0;
+      x = rows > 0 ? (int)(((unsigned)(f % 16) + rows + 15u) / 16) : 0;   // (rows may be 2^31 - 1)
     }
     int incl = x;
 #pragma unroll
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
     if (p.ring > 0 && row0 >= p.ring) row0 -= p.ring;
     nrows = min(16 * n, lead + rows - 16 * t);
     skip = t == 0 ? lead : 0;
-    n1 = p.ring > 0 && row0 + nrows > p.ring ? p.ring - row0 : nrows;
+    n1 = p.ring > 0 && nrows > p.ring - row0 ? p.ring - row0 : nrows;
   };
 
   // This lane's scale of a tile: of plane lane / GROUPS (key sources, then

@@ -74,3 +74,35 @@ def test_prefill_over_bf16_rings(end, C, window, D, G, mode):
     assert ctx.fkv_get_device_status() == B.FKV_OK
     assert bool(out.isfinite().all()) and torch.equal(out, before)
     ctx.close()
+
+
+def test_decode_and_read_back_of_a_full_length_of_2_31_rows():
+    """One sequence of every position there is (planes of 137 GB: keys and values share their codes).
+    Queries of zeros weigh all keys alike, and the last block alone holds values."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 150 << 30:
+        pytest.skip("needs 150 GiB of device memory")
+    D = 64
+    ctx = B.Context(2, 1, LAST, 1, 1, D, "f32")
+    codes = torch.zeros(1, 1, LAST, D, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(1, 1, ctx.fkv_q8_scale_cols(), device="cuda")
+    last = LAST - LAST // 32 * 32                               # rows of the last block
+    codes[0, 0, -last:] = 0x78                                  # 256
+    scales[0, 0, LAST // 32] = 2.0 ** 20
+    ctx.fkv_bind_layer_cache_q8(1, codes, codes, scales, scales)
+    q = torch.zeros(1, 1, D, device="cuda")
+    out = torch.empty_like(q)
+    ctx.fkv_decode_attn(q, 1, "vanilla", i32([LAST]), out, ctx.workspace())
+    assert ctx.fkv_get_device_status() == B.FKV_OK
+    # a lane adds one sum of four weights a group of 16 rows: as many fp32 roundings as its warp
+    # (of 12 a CTA) has groups
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ref = last * 2.0 ** 28 / LAST
+    assert float((out - ref).abs().max()) <= ref * (LAST / 16 / (12 * sms) + 128) * 2.0 ** -24
+    k, v = (torch.empty(1, 1, 40, D, device="cuda") for _ in range(2))
+    ctx.fkv_read_kv(1, "vanilla", i32([LAST - 40]), k, v)
+    want = torch.where(torch.arange(40, device="cuda") >= 40 - last, 2.0 ** 28, 0.0)[:, None].expand(40, D)
+    assert torch.equal(k[0, 0], want) and torch.equal(v[0, 0], want)
+    ctx.close()
+    del codes, scales
+    torch.cuda.empty_cache()
