@@ -35,13 +35,16 @@
 // query, at no cost, since the rows are there.
 // Values: O^T [16 channels x 8] += V^T [16 x 16 keys] . P^T, whose column g is
 // head g (a score's place in the first product is its weight's place in the
-// second).  With the value scale r in the exponent, P' = p r = 2^(s + log2 r
-// - M), no scale can take P' out of fp16's range (M is the running maximum of
-// that sum, with a slack of 2^8 before O is rescaled; r below kQ8MinValue takes the
-// rest with P'); the softmax's sum takes
-// P' / r.  P' is rounded to fp16, 2^-12, for bf16 outputs; fp32 contexts add a
+// second).  With the value scale r in the exponent, P' = p 2^e = 2^(s + e - M),
+// 2^(e - 1) < r <= 2^e, no scale can take P' out of fp16's range (M is the
+// running maximum of that sum, rounded down to a whole number, with a slack of
+// 2^8 before O is rescaled); the softmax's sum takes P' 2^-e, and the product
+// P' (r 2^-e), which is P' itself where r is a power of two (appended rows).
+// e - M is a whole number, so that a scale adds nothing to the score's rounding.
+// (e stops at kQ8MinValue's; smaller scales take the rest with r 2^-e.)
+// P' is rounded to fp16, 2^-12, for bf16 outputs; fp32 contexts add a
 // second product with what the rounding left.  Two value sources have one
-// exponent, of the larger scale, and two P with the factors r_i / r.
+// exponent, of the larger scale, and two P with the factors r_i 2^-e.
 //
 // Fragment layout: lane 4 n + q holds channels [q D/4, (q + 1) D/4) of key n
 // for the scores: contiguous bytes of a row, in which a step of 16 channels
@@ -213,11 +216,11 @@ __device__ __forceinline__ void store2(__nv_bfloat16* dst, float x, float y) {
   *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(x, y);
 }
 
-// log2, within 2^-22 (exact for powers of two).
-__device__ __forceinline__ float fast_log2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// The smallest e with x <= 2^e, for a normal x > 0 (126 at most); and 2^-e.
+__device__ __forceinline__ void ceil_log2(float x, float& e, float& inverse) {
+  const uint32_t biased = min((__float_as_uint(x) + 0x7fffffu) >> 23, 253u);
+  e = __uint_as_float(0x4b000000u | biased) - (8388608.f + 127.f);   // (2^23 + biased, as it lies)
+  inverse = __uint_as_float((254u - biased) << 23);
 }
 
 // Count one arrival on a unit's word for call `epoch`; the count with this one
@@ -784,17 +787,15 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
       const uint8_t* codes = st + 16 * g0 * D;
       // scale of plane i (key sources, then value sources), group g0 + gr
       auto scale = [&](int i, int gr) { return scales[i * GROUPS + g0 + gr]; };
-      // scores in base 2 plus the group's value exponent: s[gr][2 half + e] is
-      // key 2 q4 + e of the half
-      float s[NG][4], lv[NG];
+      // scores in base 2: s[gr][2 half + e] is key 2 q4 + e of the half; and
+      // the groups' value exponents
+      float s[NG][4], ev[NG], rv[NG];   // rv: 2^-ev
       float mt = -INFINITY;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float vs = scale(NSRC, gr);
         if constexpr (NSRC == 2) vs = fmaxf(vs, scale(NSRC + 1, gr));
-        lv[gr] = fast_log2(fmaxf(vs, kQ8MinValue));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[gr][e] = lv[gr];
+        ceil_log2(fmaxf(vs, kQ8MinValue), ev[gr], rv[gr]);
 #pragma unroll
         for (int sidx = 0; sidx < NSRC; ++sidx) {
           const float f = scale(sidx, gr) * c_row;
@@ -809,8 +810,8 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
               e4m3x4_to_f16(kw[j], b0, b1);
               mma16816(d, qf[sidx][j], b0, b1);
             }
-            s[gr][2 * half] = fmaf(d[0] + d[2], f, s[gr][2 * half]);
-            s[gr][2 * half + 1] = fmaf(d[1] + d[3], f, s[gr][2 * half + 1]);
+            s[gr][2 * half] = sidx == 0 ? (d[0] + d[2]) * f : fmaf(d[0] + d[2], f, s[gr][2 * half]);
+            s[gr][2 * half + 1] = sidx == 0 ? (d[1] + d[3]) * f : fmaf(d[1] + d[3], f, s[gr][2 * half + 1]);
           }
         }
         if constexpr (EDGE) {
@@ -821,13 +822,13 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
           if (ra + 8 < skip || ra + 8 >= nrows) s[gr][2] = -INFINITY;
           if (rb + 8 < skip || rb + 8 >= nrows) s[gr][3] = -INFINITY;
         }
-        mt = fmaxf(mt, fmaxf(fmaxf(s[gr][0], s[gr][1]), fmaxf(s[gr][2], s[gr][3])));
+        mt = fmaxf(mt, fmaxf(fmaxf(s[gr][0], s[gr][1]), fmaxf(s[gr][2], s[gr][3])) + ev[gr]);
       }
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
       const bool grow = mt > m + kQ8Slack;
       if (__any_sync(0xffffffffu, grow)) {
-        const float m_new = grow ? mt : m;
+        const float m_new = grow ? floorf(mt) : m;
         const float alpha = fast_exp2(m - m_new);
         l *= alpha;
         m = m_new;
@@ -849,17 +850,17 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float pv[4];
+        const float add = ev[gr] + off;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(s[gr][e] + off);
-        const float rv = fast_exp2(-lv[gr]);
-        l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), rv, l);
+        for (int e = 0; e < 4; ++e) pv[e] = fast_exp2(s[gr][e] + add);
+        l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), rv[gr], l);
 #pragma unroll
         for (int sidx = 0; sidx < NSRC; ++sidx) {
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = pv[e];
-          if (NSRC == 2 || scale(NSRC, gr) < kQ8MinValue) {
-            const float ratio = scale(NSRC + sidx, gr) * rv;
+          const float ratio = scale(NSRC + sidx, gr) * rv[gr];
+          if (NSRC == 2 || ratio != 1.f) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] *= ratio;
           }

@@ -1,9 +1,11 @@
-"""8-bit caches whose scales are zero: appends against the oracle."""
+"""8-bit caches whose scales are zero or no powers of two: appends against the oracle, attention
+against float64 with derived bounds."""
 
 import pytest
 import torch
 
-from q8_parity import BLOCK
+from cross_layer_kv_gb300 import fusedkv as B
+from q8_parity import BLOCK, Setup, values
 from test_q8_gpu import Cache, u8
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +44,47 @@ def test_append_joins_a_block_of_scale_zero_on_a_ring():
     c.check(c.new(3), c.new(3, 20.0), [96 + 40, 3 * 96 + 63])
     assert not u8(c.k[0])[:, :, 32:40].view("int8").__and__(0x7F).any()
     c.ctx.close()
+
+
+@pytest.mark.parametrize("mode", ["vanilla", "scaled", "fused"])
+def test_fp32_decode_of_scales_that_are_no_powers_of_two(mode):
+    """One key: the output is its value, off by P's two halves (2^-22), two sums of a matrix product
+    (2^-23 each, should it truncate) and about six more fp32 roundings (2^-24 each): below 2^-20 of
+    the magnitudes that are added up, for any scale of the range that is promised."""
+    n = 64
+    s = Setup(mode, n, 40, 2, 2, 64, dtype="f32", seed=12)
+    g = s.gen
+    e = torch.randint(-63, 38, (n, 2, 1), generator=g, device="cuda").double()
+    e[:8], e[8:16] = -63, 37
+    for planes in s.planes.values():
+        for _, scales in planes:
+            m = torch.rand(n, 2, 1, generator=g, device="cuda").double() + 1
+            scales[:] = (torch.exp2(e) * m).float()
+    q = s.query(n, 4, 64)
+    out = torch.empty_like(q)
+    s.ctx.fkv_decode_attn(q, s.layer, mode, i32([1] * n), out, s.ctx.workspace())
+    v = [values(x)[:, :, 0] for x in s.v]
+    w = [s.w[2].double(), s.w[3].double()] if mode != "vanilla" else [torch.ones(2, 64, device="cuda").double()]
+    ref, size = sum(a * b for a, b in zip(w, v)), sum((a * b).abs() for a, b in zip(w, v))
+    err = (out.view(n, 2, 2, 64).double() - ref[:, :, None]).abs()
+    assert s.ctx.fkv_get_device_status() == B.FKV_OK
+    assert bool((err <= 2.0 ** -20 * size[:, :, None]).all()), float((err / size[:, :, None].clamp(min=1e-300)).max())
+    s.close()
+
+
+def test_fp32_decode_of_equal_scores_under_other_scales():
+    """Keys of zeros: every weight is 1 / n, whatever its block's value scale (n + 64 sums, decode_bound)."""
+    n = 200
+    s = Setup("vanilla", 4, n, 2, 2, 64, dtype="f32", seed=13)
+    s.k[0][0].view(torch.uint8).zero_()
+    scales = s.v[0][1]
+    scales[:] = torch.exp2(torch.tensor([-60.0, -31.0, 0.0, 30.0], device="cuda"))[:, None, None] * \
+        (torch.rand(scales.shape, generator=s.gen, device="cuda") + 1)
+    s.v[0][0].view(torch.uint8).bitwise_and_(0x7F)      # no cancellation
+    q = s.query(4, 4, 64)
+    out = torch.empty_like(q)
+    s.ctx.fkv_decode_attn(q, s.layer, "vanilla", i32([n] * 4), out, s.ctx.workspace())
+    ref = values(s.v[0]).mean(2)
+    err = (out.view(4, 2, 2, 64).double() - ref[:, :, None]).abs() / ref[:, :, None]
+    assert float(err.max()) <= 2.0 ** -20 + (n + 64) * 2.0 ** -24, float(err.max())
+    s.close()
