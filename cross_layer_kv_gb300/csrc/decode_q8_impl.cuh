@@ -44,7 +44,11 @@
 // (e stops at kQ8MinValue's; smaller scales take the rest with r 2^-e.)
 // P' is rounded to fp16, 2^-12, for bf16 outputs; fp32 contexts add a
 // second product with what the rounding left.  Two value sources have one
-// exponent, of the larger scale, and two P with the factors r_i 2^-e.
+// exponent, of the larger scale, and two P with the factors r_i 2^-e, where a
+// source's scales count times its largest weight (as a power of two, which the
+// weights of the output are divided by): a source whose small weights make up
+// for its large scales does not push the other out of fp16's range.  The query
+// has a power of two for each source's key weights, too.
 //
 // Fragment layout: lane 4 n + q holds channels [q D/4, (q + 1) D/4) of key n
 // for the scores: contiguous bytes of a row, in which a step of 16 channels
@@ -703,7 +707,10 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
   // O^T fragments: this lane's channels 2 i, 2 i + 1 of heads 2 q4 (elements
   // 0, 2) and 2 q4 + 1 (1, 3)
   float o[NSRC][VT][4];
-  float c_row = 0.f;           // 2^-e of the head's query
+  float c_row[NSRC];           // 2^-e of the head's query times a source's key weights
+  // what a source's value scales are multiplied by: its largest value weight over
+  // the larger source's, as powers of two (below 2^-126: 0)
+  [[maybe_unused]] float gv[2] = {1.f, 1.f};
   float m = -FLT_MAX, l = 0.f; // of head n8, this lane's keys
   bool fresh = true;
   bool whole = false;          // the range has the unit from its first group on
@@ -719,12 +726,21 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 
     if (fresh) {
       whole = t0 == 0;
-      // head n8's query, channels [q4 D/4, + D/4), brought to [2^14, 2^15)
-      float top = 0.f, x[D / 4], wk[NSRC][D / 4];
+      // head n8's query, channels [q4 D/4, + D/4), times the source's key weights,
+      // brought to [2^14, 2^15)
+      float x[D / 4], wk[NSRC][D / 4];
 #pragma unroll
       for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
       if (n8 < G)
         load_floats<D / 4>(static_cast<const T*>(p.q) + (((size_t)b * H + h) * G + n8) * D + q4 * (D / 4), x);
+      [[maybe_unused]] float wv[2][(D + 31) / 32];
+      if constexpr (NSRC == 2) {
+#pragma unroll
+        for (int sidx = 0; sidx < 2; ++sidx)
+#pragma unroll
+          for (int k = 0; k < (D + 31) / 32; ++k)
+            wv[sidx][k] = lane + 32 * k < D ? (sidx ? p.b1 : p.b0)[(size_t)h * D + lane + 32 * k] : 0.f;
+      }
 #pragma unroll
       for (int sidx = 0; sidx < NSRC; ++sidx) {
         const float* ap = sidx == 0 ? p.a0 : p.a1;
@@ -737,17 +753,37 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) {
           wk[sidx][e] *= x[e] * p.qscale;
-          top = fmaxf(top, fabsf(wk[sidx][e]));
         }
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int eq = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-      eq = eq > 120 ? 120 : (eq < -120 ? -120 : eq);   // (2^eq and its inverse stay normal)
-      const float f = __uint_as_float((uint32_t)(eq + 127) << 23);
-      c_row = __uint_as_float((uint32_t)(127 - eq) << 23);
+      if constexpr (NSRC == 2) {
+        uint32_t e[2];   // the largest weights' exponents
+#pragma unroll
+        for (int sidx = 0; sidx < 2; ++sidx) {
+          uint32_t most = 0;
+#pragma unroll
+          for (int k = 0; k < (D + 31) / 32; ++k) {
+            const uint32_t u = __float_as_uint(fabsf(wv[sidx][k]));
+            if (u < 0x7f800000u) most = max(most, u);
+          }
+          e[sidx] = __reduce_max_sync(0xffffffffu, most) >> 23;
+        }
+#pragma unroll
+        for (int sidx = 0; sidx < 2; ++sidx) {
+          const uint32_t below = max(e[0], e[1]) - e[sidx];
+          gv[sidx] = below > 126 ? 0.f : __uint_as_float((127 - below) << 23);
+        }
+      }
 #pragma unroll
       for (int sidx = 0; sidx < NSRC; ++sidx) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(wk[sidx][e]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int eq = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+        eq = eq > 120 ? 120 : (eq < -120 ? -120 : eq);   // (2^eq and its inverse stay normal)
+        const float f = __uint_as_float((uint32_t)(eq + 127) << 23);
+        c_row[sidx] = __uint_as_float((uint32_t)(127 - eq) << 23);
 #pragma unroll
         for (int j = 0; j < KW; ++j) {
           const float* y = wk[sidx] + 4 * j;
@@ -794,11 +830,11 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float vs = scale(NSRC, gr);
-        if constexpr (NSRC == 2) vs = fmaxf(vs, scale(NSRC + 1, gr));
+        if constexpr (NSRC == 2) vs = fmaxf(vs * gv[0], scale(NSRC + 1, gr) * gv[1]);
         ceil_log2(fmaxf(vs, kQ8MinValue), ev[gr], rv[gr]);
 #pragma unroll
         for (int sidx = 0; sidx < NSRC; ++sidx) {
-          const float f = scale(sidx, gr) * c_row;
+          const float f = scale(sidx, gr) * c_row[sidx];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t kw[KW];
@@ -859,7 +895,7 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = pv[e];
-          const float ratio = scale(NSRC + sidx, gr) * rv[gr];
+          const float ratio = (NSRC == 2 ? scale(NSRC + sidx, gr) * gv[sidx] : scale(NSRC, gr)) * rv[gr];
           if (NSRC == 2 || ratio != 1.f) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] *= ratio;
@@ -933,6 +969,9 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int head = 2 * q4 + e;
+        // (1 / gv; 0: a finite one, times sums of zeros)
+        [[maybe_unused]] const float ug[2] = {__uint_as_float((254u << 23) - __float_as_uint(gv[0])),
+                                              __uint_as_float((254u << 23) - __float_as_uint(gv[1]))};
         const float inv = 1.f / __shfl_sync(0xffffffffu, l, 8 * q4 + 4 * e);
         if (head >= G) continue;
 #pragma unroll
@@ -941,13 +980,13 @@ __global__ void __launch_bounds__(Q8Shape<D, NSRC>::W * 32, 1) decode_q8_kernel(
           float x = o[0][i][e], y = o[0][i][e + 2];
           if (NSRC == 2 || p.b0) {
             const float2 w0 = *reinterpret_cast<const float2*>(p.b0 + (size_t)h * D + c);
-            x *= w0.x;
-            y *= w0.y;
+            x *= NSRC == 2 ? w0.x * ug[0] : w0.x;
+            y *= NSRC == 2 ? w0.y * ug[0] : w0.y;
           }
           if constexpr (NSRC == 2) {
             const float2 w1 = *reinterpret_cast<const float2*>(p.b1 + (size_t)h * D + c);
-            x = fmaf(o[1][i][e], w1.x, x);
-            y = fmaf(o[1][i][e + 2], w1.y, y);
+            x = fmaf(o[1][i][e], w1.x * ug[1], x);
+            y = fmaf(o[1][i][e + 2], w1.y * ug[1], y);
           }
           if (whole && ends)
             store2(static_cast<T*>(p.out) + ((size_t)u * G + head) * D + c, x * inv, y * inv);

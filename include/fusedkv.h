@@ -282,11 +282,13 @@ size_t fkv_decode_workspace_bytes(const fkv_ctx* ctx);
  * [1, S_max] is clamped (0 yields a zero output) and flagged as
  * FKV_ERR_DEVICE_ARG in the device status.
  * Rounding: fp32 throughout; over 8-bit caches queries times key weights keep
- * 22 bits, and bf16 contexts round each probability to fp16 for its product
- * with the values (two sources whose value scales' ratio is no power of two:
- * for each source by itself); a probability whose product with its value scale
- * is below 2^-31 of the largest may count as 0 there (the softmax's sum takes
- * it).
+ * 22 bits (for each source by itself), and for its product with the values a
+ * probability times its value scale keeps 22 bits in fp32 contexts and 11 in
+ * bf16 ones (for each source by itself, unless their scales' ratio is a power of
+ * two), and not what lies below 2^-31 of the largest such product: scales count
+ * times the source's largest weight, as a power of two, so that sources whose
+ * weights make up for their scales keep all bits.  The softmax's sum takes the
+ * probabilities as they are.
  * mode: for storage layers every mode is plain attention over the layer's own
  * cache; for upper layers FKV_VANILLA reads the layer's own cache (needs
  * store_upper), FKV_LITE reads K^n and V^1, FKV_FUSED reads K^1, K^n, V^1, V^n

@@ -1,11 +1,11 @@
-"""8-bit caches whose scales are zero or no powers of two: appends against the oracle, attention
-against float64 with derived bounds."""
+"""8-bit caches whose scales are zero, no powers of two, or far apart between the two sources of a
+fused layer: appends against the oracle, attention against float64 with derived bounds."""
 
 import pytest
 import torch
 
 from cross_layer_kv_gb300 import fusedkv as B
-from q8_parity import BLOCK, Setup, values
+from q8_parity import BLOCK, Setup, check_decode, values
 from test_q8_gpu import Cache, u8
 
 pytestmark = pytest.mark.gpu
@@ -87,4 +87,53 @@ def test_fp32_decode_of_equal_scores_under_other_scales():
     ref = values(s.v[0]).mean(2)
     err = (out.view(4, 2, 2, 64).double() - ref[:, :, None]).abs() / ref[:, :, None]
     assert float(err.max()) <= 2.0 ** -20 + (n + 64) * 2.0 ** -24, float(err.max())
+    s.close()
+
+
+def _apart(s, gap, how):
+    """The blocks of one source get scales 2^gap times the other's.  `weights`: and weights 2^-gap
+    times; `zero weights`: its weights are 0; `zeros`: its codes are."""
+    first, last = min(s.planes), max(s.planes)
+    big = last if gap > 0 else first
+    for codes, scales in s.planes[big]:
+        scales *= 2.0 ** abs(gap)
+        if how == "zeros":
+            codes.view(torch.uint8).zero_()
+    mine = (1, 3) if big == last else (0, 2)
+    for i in mine:
+        if how == "weights":
+            s.w[i] *= 2.0 ** -abs(gap)
+        elif how == "zero weights":
+            s.w[i].zero_()
+
+
+APART = [(28, "weights"), (-28, "weights"), (20, "weights"), (28, "zero weights"), (-28, "zero weights"),
+         (18, "zeros"), (-18, "zeros")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 80, 96, 128])
+@pytest.mark.parametrize("gap,how", [a for a in APART if a[1] != "zeros"])
+def test_decode_of_sources_whose_scales_are_far_apart(gap, how, D, dtype):
+    s = Setup("fused", 2, 300, 2, 2, D, dtype=dtype, seed=D + gap)
+    _apart(s, gap, how)
+    check_decode(s, [300, 77], what="%s 2^%d" % (how, gap))
+    s.close()
+
+
+def _by_head(batch, seed):
+    """Gaps of other sizes and signs in heads beside each other."""
+    s = Setup("fused", batch, 130, 4, 2, 96, seed=seed)
+    first, last = min(s.planes), max(s.planes)
+    for h, gap in enumerate((0, 26, -26, 12)):
+        for _, scales in s.planes[last if gap > 0 else first]:
+            scales[:, h] *= 2.0 ** abs(gap)
+        for i in ((1, 3) if gap > 0 else (0, 2)):
+            s.w[i][h] *= 2.0 ** -abs(gap)
+    return s
+
+
+def test_decode_of_heads_whose_sources_lie_apart_each_in_its_way():
+    s = _by_head(3, 5)
+    check_decode(s, [130, 1, 66])
     s.close()
