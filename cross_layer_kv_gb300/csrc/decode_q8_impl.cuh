@@ -220,13 +220,6 @@ __device__ __forceinline__ void store2(__nv_bfloat16* dst, float x, float y) {
   *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(x, y);
 }
 
-// The smallest e with x <= 2^e, for a normal x > 0 (126 at most); and 2^-e.
-__device__ __forceinline__ void ceil_log2(float x, float& e, float& inverse) {
-  const uint32_t biased = min((__float_as_uint(x) + 0x7fffffu) >> 23, 253u);
-  e = __uint_as_float(0x4b000000u | biased) - (8388608.f + 127.f);   // (2^23 + biased, as it lies)
-  inverse = __uint_as_float((254u - biased) << 23);
-}
-
 // Count one arrival on a unit's word for call `epoch`; the count with this one
 // (0 if the retry bound ran out).  One atomic addition where the word carries
 // the epoch already.  A word with another epoch (whatever the workspace held)

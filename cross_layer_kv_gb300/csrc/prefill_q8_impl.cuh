@@ -19,9 +19,16 @@
 // scales are.  The softmax's sum takes p = P' / r.  A row of Q (times its key
 // weights in the scaled mode) is brought to fp16 with a power of two that
 // places its largest element below 2^15.  Two sources are combined as
-//     w0 (c0 (s0 / s)) + w1 (c1 (s1 / s)),  s = max(s0, s1),
-// in packed fp16 arithmetic (four instructions for two channels), with the
-// head's weights brought below 1 by one power of two.
+//     w0 (c0 r0) + w1 (c1 r1),  r_i = s_i W_i / s,  s = max(s0 W0, s1 W1) or the power of two above,
+// in packed fp16 arithmetic (four instructions for two channels), with each
+// source's weights divided by the power of two above the head's largest, W_i.
+// So a source counts by its scales times its weights, whichever make it large
+// (weights that share one power of two, and ratios of the scales alone, lost a
+// source whose scales were 2^25 times smaller although its weights made up for
+// it).  The weights come times 2^4 and the ratios times 2^2, which keeps the sum
+// below 2^16 and leaves the weights 11 bits down to 2^-18 of their head's largest,
+// the ratios down to 2^-16 (powers of two: to 2^-26, which is what appended rows
+// have), and a source's codes 2^-12 of their largest down to ratios of 2^-26.
 //
 // Structure (as prefill_wide.cu): a CTA owns two groups of 128 query rows over
 // the same keys (two heads of a KV head, or two row tiles of one head), each
@@ -48,8 +55,8 @@
 // of 96 channels), hand-offs (400) and products (1450, in turns with the other
 // group's), at 39% of the tensor pipe's cycles, half of the issue slots and 44%
 // of shared memory's; and about 8 us a CTA before its first scores and after
-// its last products.  650M calls of 8192 rows, 824.7 GFLOP: Lite 891 us (926
-// TFLOP/s), fused 1182 (698); 1.5B: Lite 989 (1112), fused 1562 (704).
+// its last products.  650M calls of 8192 rows, 824.7 GFLOP: Lite 892 us (925
+// TFLOP/s), fused 1153 (715); 1.5B: Lite 991 (1110), fused 1484 (741).
 //
 // Every wait is bounded; a wait that runs out sets an abort flag that each
 // role checks, flags the device status, and the CTA frees its tensor memory.
@@ -74,6 +81,9 @@ constexpr int SMEM_LIMIT = 232448; // opt-in dynamic shared memory per CTA (227 
 constexpr float kSlack = 8.f;      // log2 growth of the running max tolerated before O is rescaled
 constexpr float kBias = 7.f;       // P' <= 2^(7 + 8) < 65504, and is not flushed above 2^-31
 constexpr int NSR = 8;             // conversion-step barriers and scale records
+constexpr float kWeightFrame = 16.f, kRatioFrame = 4.f;   // of two sources' weights and ratios
+constexpr float kFrame = 64.f, kLogFrame = 6.f;          // and of their elements
+static_assert(kWeightFrame * kRatioFrame == kFrame, "");
 
 constexpr int cap(int x, int most) { return x > most ? most : x; }
 
@@ -106,9 +116,9 @@ struct Cfg {
   static constexpr int CONV_WARP = SOFTMAX_WARPS + 4;
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 8);
   // registers: 128 per thread at launch (65536 / 512); a warpgroup may only give
-  // some up (conversion, control) or take some (softmax).  Two sources: 650M
-  // fused 1190 us with 104 and 184, 1182 with 120 and 176 (88, 192: 1226); one
-  // source: 650M Lite 902 with 72 and 200, 891 with 104 and 184.
+  // some up (conversion, control) or take some (softmax).  Two sources
+  // (650M fused): 104 and 184 take 0.7% more than 120 and 176, 88 and 192 4%
+  // more; one source (650M Lite): 72 and 200 1.2% more than 104 and 184.
   static constexpr int REGS_CONTROL = 40, REGS_CONV = NSRC == 2 ? 120 : 104, REGS_SOFTMAX = NSRC == 2 ? 176 : 184;
   static constexpr long long REGS_SPLIT =
       (long long)NG * 128 * REGS_SOFTMAX + 128LL * REGS_CONTROL + 128LL * REGS_CONV;
@@ -228,6 +238,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 
 // 2^e with 2^e <= x < 2^(e+1) for a normal x > 0 (0 for what is smaller).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+__device__ __forceinline__ float reciprocal_of_power(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 __device__ __forceinline__ float power_of_two(int e) {   // e clamped to the normal range
   e = e < -126 ? -126 : (e > 127 ? 127 : e);
   return __uint_as_float((uint32_t)(e + 127) << 23);
@@ -247,9 +258,9 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
   uint8_t* sRawK = sV + NS * C::KV_BYTES;               // codes, the sources of a slot side by side
   uint8_t* sRawV = sRawK + NR * NSRC * C::RAW_BYTES;
   float4* sScale = reinterpret_cast<float4*>(sRawV + NR * NSRC * C::RAW_BYTES);   // {s (times what the weights were divided by), log2 r, 1 / r, rest of r}
-  // of K and V: (s0 / s, s1 / s), each as two equal halves
+  // of K and V: 2^2 (r0, r1), each as two equal halves
   uint2* sRatio = reinterpret_cast<uint2*>(sScale + NSR * NGRP);
-  uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + (NSRC == 2 ? NSR * 2 * NGRP : 0));   // fp16 a0, a1, b0, b1
+  uint16_t* sW = reinterpret_cast<uint16_t*>(sRatio + (NSRC == 2 ? NSR * 2 * NGRP : 0));   // fp16 2^4 (a0 / W0, a1 / W1), of b0 and b1 alike
   uint64_t* bars = reinterpret_cast<uint64_t*>(sW + (NSRC == 2 ? 4 * D : 0));
   uint64_t* q_ready = bars;
   uint64_t* q_raw = q_ready + 1;          // [NG]
@@ -361,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     // Scale records of tile j, one thread per block.
     float ns[2 * NSRC];
     float k_power = 1.f;   // what the key weights were divided by
+    [[maybe_unused]] float by_top[4];   // W_i over the larger one's, of keys and of values
     auto load_scales = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 2 * NSRC; ++i) ns[i] = 1.f;   // (blocks behind the last key: any finite one)
@@ -376,16 +388,25 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     };
     auto store_scales = [&](int j) {
       if (ft >= NGRP) return;
-      float s = ns[0], r = fmaxf(ns[NSRC], kQ8MinValue);
-      if constexpr (NSRC == 2) {
-        s = fmaxf(fmaxf(ns[0], ns[1]), FLT_MIN);
-        r = fmaxf(fmaxf(ns[2], ns[3]), kQ8MinValue);
-        const float is = 1.f / s, ir = 1.f / r;
-        uint2* rec = sRatio + (size_t)(j % NSR) * 2 * NGRP;
-        rec[ft] = make_uint2(f16x2_of(ns[0] * is, ns[0] * is), f16x2_of(ns[1] * is, ns[1] * is));
-        rec[NGRP + ft] = make_uint2(f16x2_of(ns[2] * ir, ns[2] * ir), f16x2_of(ns[3] * ir, ns[3] * ir));
+      float4& rec = sScale[(j % NSR) * NGRP + ft];
+      if constexpr (NSRC == 1) {
+        const float r = fmaxf(ns[1], kQ8MinValue);
+        rec = make_float4(ns[0], log2f(r), 1.f / r, ns[1] / r);
+      } else {
+        // the larger scale's power of two goes into the record, the rest into the
+        // ratios (two divisions and a logarithm here, in the chain from a step's
+        // tiles to its barrier, were 3 to 6% of a call)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ns[i] *= by_top[i];
+        float es, is, er, ir;
+        ceil_log2(fmaxf(fmaxf(ns[0], ns[1]), FLT_MIN), es, is);
+        ceil_log2(fmaxf(fmaxf(ns[2], ns[3]), kQ8MinValue), er, ir);
+        auto twice = [](float x) { return f16x2_of(x * kRatioFrame, x * kRatioFrame); };
+        uint2* ratio = sRatio + (size_t)(j % NSR) * 2 * NGRP;
+        ratio[ft] = make_uint2(twice(ns[0] * is), twice(ns[1] * is));
+        ratio[NGRP + ft] = make_uint2(twice(ns[2] * ir), twice(ns[3] * ir));
+        rec = make_float4(k_power * reciprocal_of_power(is), er - kLogFrame, ir * kFrame, 1.f);
       }
-      sScale[(j % NSR) * NGRP + ft] = make_float4(s * k_power, log2f(r), 1.f / r, ns[NSRC] / r);
     };
     // A value that is not a number: noted for the rows that see it, 0 in the tile.
     auto note_bad = [&](int n0, int row) {
@@ -447,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
         }
       }
     };
-    // 16 codes of one source or two -> 8 fp16 pairs; r: the sources' scales over the larger one
+    // 16 codes of one source or two -> 8 fp16 pairs; r: the sources' ratios
     auto combine = [&](const uint4& x, const uint4& y, const uint2& r, const Weights& w, uint32_t* o) {
       const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
       if constexpr (NSRC == 2) {
@@ -482,8 +503,8 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
     };
     // Tile j of codes -> fp16 in the swizzled layout; then `empty` is told.
     // One copy of a short loop for K and V: the softmax warps' code, unrolled
-    // over a tile, and this one share the instruction caches (650M fused: 1310 us
-    // with the tile's items unrolled for K and for V, 1190 so).
+    // over a tile, and this one share the instruction caches (650M fused: 10% more
+    // with the tile's items unrolled for K and for V).
     auto convert = [&](uint8_t* dst, const uint8_t* raw, int j, bool value, uint64_t* empty) {
       const int left = S_kv - (pos0 + j * BN);   // keys from the tile's first on
       uint32_t nan[4] = {0, 0, 0, 0};   // 0, or not a number once a value was none
@@ -551,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       mbar_arrive(empty);
     };
     if constexpr (NSRC == 2) {
-      // the head's weights below 1: one power of two for keys, one for values
+      // the head's weights below 2^4, by a power of two for each vector
       const int v = ft / 32;   // a warp's vector
       const float* src = (v == 0 ? p.a[0] : v == 1 ? p.a[1] : v == 2 ? p.b[0] : p.b[1]) + kh * D;
       float x[(D + 31) / 32];
@@ -565,12 +586,22 @@ __global__ void __launch_bounds__(Cfg<D, NSRC>::THREADS, 1) prefill_q8_kernel(co
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) w_top[v] = top;
       (void)group_and(true);
-      const float f = power_of_two(-exponent_of(__uint_as_float(max(w_top[v & 2], w_top[v | 1]))) - 1);
-      k_power = power_of_two(exponent_of(__uint_as_float(max(w_top[0], w_top[1]))) + 1);
+      int e[4];   // W_i = 2^e
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = exponent_of(__uint_as_float(w_top[i])) + 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int below = max(e[i & 2], e[i | 1]) - e[i];
+        by_top[i] = below > 126 ? 0.f : power_of_two(-below);
+      }
+      k_power = power_of_two(max(e[0], e[1])) * (1.f / kFrame);
+      // (two factors, since 2^-e alone may lie outside the normal range)
+      const int ev = v == 0 ? e[0] : v == 1 ? e[1] : v == 2 ? e[2] : e[3];
+      const float f0 = power_of_two(-(ev / 2)), f1 = power_of_two(ev / 2 - ev) * kWeightFrame;
 #pragma unroll
       for (int i = 0; i < (D + 31) / 32; ++i)
         if (lane + 32 * i < D) {
-          const __half h = __float2half_rn(x[i] * f);
+          const __half h = __float2half_rn(x[i] * f0 * f1);
           sW[v * D + lane + 32 * i] = *reinterpret_cast<const uint16_t*>(&h);
         }
     }

@@ -55,4 +55,11 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
   f[3] = b.y;
 }
 
+// The smallest e with x <= 2^e, for a normal x > 0 (126 at most); and 2^-e.
+__device__ __forceinline__ void ceil_log2(float x, float& e, float& inverse) {
+  const uint32_t biased = min((__float_as_uint(x) + 0x7fffffu) >> 23, 253u);
+  e = __uint_as_float(0x4b000000u | biased) - (8388608.f + 127.f);   // (2^23 + biased, as it lies)
+  inverse = __uint_as_float((254u - biased) << 23);
+}
+
 }  // namespace fkv

@@ -346,9 +346,15 @@ fkv_status fkv_decode_attn_noalloc(fkv_ctx* ctx, const void* q, int layer, int m
  * Over 8-bit caches H_q / H_kv may be 4 too, rings of any number of blocks
  * serve (no key tile to be a multiple of), scores and values take fp16
  * operands (the codes are exact in them; queries times key weights, fused rows
- * and probabilities are rounded to 2^-11 or better, fused weights likewise),
- * and a stored value that is not a number gives NaN in the rows that see it
- * and does not reach the others. */
+ * and probabilities are rounded to 2^-11 or better, and so are fused weights,
+ * and the ratio of the sources' block scales where it is no power of two), and a
+ * stored value that is not a number gives NaN in all channels of the rows that
+ * see it (fkv_decode_attn: in its own channel) and does not reach the others.
+ * Fused rows have fp16's range: with a block's scales taken times the power of
+ * two above their source's largest weight of the head, a source whose scale is
+ * below 2^-16 of the other's keeps fewer bits (if it is not a power of two
+ * times the other's), and below 2^-26 it may count as 0; a weight keeps fewer bits
+ * below 2^-18 of its source's largest. */
 fkv_status fkv_prefill_attn(fkv_ctx* ctx, const void* q, int layer, int mode, int S,
                             void* out, void* stream);
 

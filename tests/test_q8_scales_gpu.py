@@ -1,11 +1,13 @@
 """8-bit caches whose scales are zero, no powers of two, or far apart between the two sources of a
 fused layer: appends against the oracle, attention against float64 with derived bounds."""
 
+import math
+
 import pytest
 import torch
 
 from cross_layer_kv_gb300 import fusedkv as B
-from q8_parity import BLOCK, Setup, check_decode, values
+from q8_parity import BLOCK, Setup, check_decode, check_prefill, reconstruct, values
 from test_q8_gpu import Cache, u8
 
 pytestmark = pytest.mark.gpu
@@ -92,7 +94,7 @@ def test_fp32_decode_of_equal_scores_under_other_scales():
 
 def _apart(s, gap, how):
     """The blocks of one source get scales 2^gap times the other's.  `weights`: and weights 2^-gap
-    times; `zero weights`: its weights are 0; `zeros`: its codes are."""
+    times; `zero weights`: its weights are 0; `zeros`: its codes are (and its scales still count)."""
     first, last = min(s.planes), max(s.planes)
     big = last if gap > 0 else first
     for codes, scales in s.planes[big]:
@@ -107,13 +109,12 @@ def _apart(s, gap, how):
             s.w[i].zero_()
 
 
-APART = [(28, "weights"), (-28, "weights"), (20, "weights"), (28, "zero weights"), (-28, "zero weights"),
-         (18, "zeros"), (-18, "zeros")]
+APART = [(28, "weights"), (-28, "weights"), (20, "weights"), (28, "zero weights"), (-28, "zero weights")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D", [64, 80, 96, 128])
-@pytest.mark.parametrize("gap,how", [a for a in APART if a[1] != "zeros"])
+@pytest.mark.parametrize("gap,how", APART)
 def test_decode_of_sources_whose_scales_are_far_apart(gap, how, D, dtype):
     s = Setup("fused", 2, 300, 2, 2, D, dtype=dtype, seed=D + gap)
     _apart(s, gap, how)
@@ -136,4 +137,59 @@ def _by_head(batch, seed):
 def test_decode_of_heads_whose_sources_lie_apart_each_in_its_way():
     s = _by_head(3, 5)
     check_decode(s, [130, 1, 66])
+    s.close()
+
+
+@pytest.mark.parametrize("D", [64, 80, 96, 128])
+@pytest.mark.parametrize("gap,how", APART)
+def test_prefill_of_sources_whose_scales_are_far_apart(gap, how, D):
+    """What a source brings counts by its scales times its weights."""
+    s = Setup("fused", 1, 300, 2, 2, D, seed=D + gap)
+    _apart(s, gap, how)
+    check_prefill(s, 0, 300, what="%s 2^%d" % (how, gap))
+    s.close()
+
+
+def test_prefill_of_heads_whose_sources_lie_apart_each_in_its_way():
+    s = _by_head(1, 6)
+    check_prefill(s, 0, 130)
+    s.close()
+
+
+@pytest.mark.parametrize("D", [64, 80, 96, 128])
+@pytest.mark.parametrize("gap", [18, -18])
+def test_prefill_beside_a_source_of_zeros_whose_scales_are_larger(gap, D):
+    """The other source's rows keep what fp16 has below the frame of their block.  With S the larger of
+    the sources' scales times the powers of two above their heads' largest weights, elements are held
+    in units of S / 64; a ratio of scales (a power of two) is exact; a code times it is off by 2^-25
+    below fp16's normal range, times a weight of up to 2^4; the product and the sum by 2^-25 each; and a
+    weight by 2^-25 / 2^4 of that power of two, below the normal range, times its own scale and code."""
+    s = Setup("fused", 1, 300, 2, 2, D, seed=D + gap)
+    _apart(s, gap, "zeros")
+    C, h = 300, 2.0 ** -11
+    q = s.query(1, 4, C, D)
+    out = torch.full_like(q, float("nan"))
+    s.ctx.fkv_prefill_attn(q, s.layer, "fused", C, out)
+    assert s.ctx.fkv_get_device_status() == B.FKV_OK
+    K, V = s.rows()
+    w = [x.double().abs() for x in s.w]
+    Ka, Va = reconstruct("fused", w, [values(x).abs() for x in s.k], [values(x).abs() for x in s.v])
+    top = [torch.exp2(torch.floor(torch.log2(x.amax(-1))) + 1)[None, :, None] for x in w]
+    rows = torch.arange(C, device="cuda") // BLOCK
+    off = []
+    for p, i in ((s.k, 0), (s.v, 2)):
+        a, b = p[0][1].double() * top[i], p[1][1].double() * top[i + 1]
+        off.append((torch.maximum(a, b) * (18 * 2.0 ** -25 / 64) + (a + b) * 448 * 2.0 ** -29)[:, :, rows])
+    see = torch.ones(C, C, dtype=torch.bool, device="cuda").tril()
+    for g in range(4):
+        kh, qq = g // 2, q[0, g].double()
+        p = torch.softmax((qq @ K[0, kh].T * s.scale).masked_fill(~see, -math.inf), -1)
+        size = (qq.abs() @ Ka[0, kh].T * s.scale).masked_fill(~see, 0.0).amax(-1, keepdim=True)
+        keys = (off[0][0, kh][None].expand(C, C).masked_fill(~see, 0.0)).amax(-1, keepdim=True)
+        score = (4 * h + (2 * D + 8) * 2.0 ** -23) * size + 2.0 ** -21 + qq.abs().sum(-1, keepdim=True) * s.scale * keys
+        pv, ref = p @ Va[0, kh], p @ V[0, kh]
+        bound = (2 * score + 5 * h + (C + 64) * 2.0 ** -23) * pv + (p @ off[1][0, kh])[:, None] \
+            + C * 2.0 ** -31 * Va[0, kh].max() + 2.0 ** -8 * ref.abs()
+        err = (out[0, g].double() - ref).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
     s.close()
