@@ -30,7 +30,9 @@ cudaError_t decode_q8_plan(const DecodeArgs& a, int num_sms, DecodePlan* plan) {
   }
   const long long rows = (long long)a.batch * a.kv_heads * a.max_seq;
   long long ctas = a.num_ctas > 0 ? a.num_ctas : num_sms;
-  // small calls: CTAs of 8 rows a warp, which take whole units where they can
+  // small calls (by the rows that the context's caches hold: the workspace is
+  // asked for once, whatever the calls' windows and lengths): CTAs of 8 rows a
+  // warp, which take whole units where they can
   // (fused, 64 channels, us with 8, 16 and 64 rows a warp: 128 units of 100 rows
   // 6.6, 8.4, 12.2; 64 of 300 7.4, 7.3, 10.7; 2 of 256 6.9, 6.8, 8.5)
   const long long by_rows = (rows + 8LL * W - 1) / (8LL * W);

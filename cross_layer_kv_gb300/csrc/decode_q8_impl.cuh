@@ -126,11 +126,6 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // (x, y) = hi + lo in fp16 pairs.
 __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -488,10 +483,14 @@ struct Q8Walker {
 
 // A CTA takes whole units where the busiest one then has at most these codes
 // (bytes) more than an equal share: a merge through global memory costs 4 us,
-// about what they take.  At 96 channels, one source, 75 groups of 16 rows, in
-// us whole and split: 128 units of 1000 rows 10.4 and 15.9, of 4000 24.2 and
-// 27.2, of 8000 (75 groups more) 40.7 and 40.9; 32 of 1500 11.9 and 13.3, of
-// 2000 (99 more) 14.6 and 14.2; 160 of 2000 (118 more) 24.4 and 22.1.
+// about what they take.  Both ways measured with 32, 128 and 160 units of 500 to
+// 6000 rows, at 64, 96 and 128 channels, one source and two, bf16 and fp32
+// contexts: whole units are 1.0 to 6.2 us faster in every call with up to 200 KB
+// more on the busiest CTA, both are within 2.2 us of each other from there to 303
+// KB, and split ones are 1.6 to 34 us faster from 320 KB on.  Us whole and split: 64
+// channels, one source, 128 units of 2000 rows (40 KB) 11.4 and 16.7; 96, 32 of
+// 1500 (227 KB) 11.9 and 13.1; 128, two sources, 128 of 3000 (243 KB) 50.5 and
+// 49.9, of 4000 (323 KB) 64.4 and 61.2.
 constexpr int kQ8Uneven = 230400;
 
 template <typename T, int D, int NSRC>

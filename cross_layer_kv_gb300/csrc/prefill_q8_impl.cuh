@@ -205,10 +205,6 @@ __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
                             *reinterpret_cast<__half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
-  const __half2 r = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // Packed fp32 pairs as 64-bit operands (made once where a pair is used often:
 // the compiler copies both halves for every use of a pair made in place).
@@ -1152,7 +1148,7 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   // Few CTAs with many key tiles each: clusters that share them, of as many
   // CTAs as still find an SM each, with two tiles a CTA at least (a join costs
   // about a tile).  8 units of 16 rows behind 16368 keys (D = 96): 232 us with
-  // one CTA a unit, 43 with 8.
+  // one CTA a unit, 42 with 8.
   long long keys = p.S_kv;
   if (a.window > 0 && (long long)a.window + rows_per_cta < keys) keys = (long long)a.window + rows_per_cta;
   const long long key_tiles = (keys + C::BN - 1) / C::BN;

@@ -7,8 +7,9 @@
 // so a block's scale only has to place the block's largest value below 448:
 // the append takes the power of two that does.  A later, larger row of the
 // same block then moves the codes before it by whole exponents, which rounds
-// nothing but what falls below 2^-6 (an error of at most 2^-10 scales, 2^-18
-// of the block's largest value).
+// nothing but what falls below 2^-6: by at most 2^-10 new scales each time that
+// the scale grows, below 2^-9 of the last one in all (a scale at least doubles),
+// 2^-16.8 of the block's largest value, which is above 224 scales.
 #pragma once
 
 #include <cstdint>
@@ -31,6 +32,11 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Two fp32 -> e4m3 codes (x in the low byte): nearest even, above 448 to 448,

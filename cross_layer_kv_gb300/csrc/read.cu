@@ -21,7 +21,7 @@ constexpr int kThreads = 256;   // of a CTA, at most
 // with 2), and short calls spread over more CTAs with 2 (32 x 8 heads x 77 rows,
 // two sources: 4.5 us, against 5.7 with 8).
 constexpr int kRunsLong = 8, kRunsShort = 2;
-constexpr long long kLongCtas = 1216;   // 8 an SM
+constexpr long long kLongCtas = 8 * 152;   // 8 an SM of a GB300
 
 // 8 elements of a plain row.
 template <typename T>

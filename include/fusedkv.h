@@ -155,10 +155,12 @@ int fkv_q8_scale_cols(int rows);
  *   - rows of the block before the new ones keep their values: where the scale
  *     grew, their codes become the nearest of code * old scale / new scale,
  *     which is exact but for values below 2^-6 new scales (off by at most 2^-10
- *     new scales);
+ *     new scales each time, below 2^-9 of the last one in all); rows of a block of
+ *     scale 0 stay zeros, whatever their codes;
  *   - rows of the block behind the new ones are lost.
  * So rows are appended in order, as for a ring; rows taken back (a shorter
- * length, then an append there) are fine, and leave a scale that they raised.
+ * length, then an append there) are fine, and leave a scale that they raised (on
+ * a ring, the older rows that they replaced are lost).
  * Calls over 8-bit caches: fkv_append_kv, fkv_read_kv, fkv_decode_attn
  * (_noalloc) and, in bf16 contexts, fkv_prefill_attn (_chunk), where every
  * source of the call is 8-bit (a mix of formats is FKV_ERR_UNSUPPORTED).
